@@ -1,4 +1,5 @@
-"""ctypes view of libmoe_decode.so (the C ABI declared in include/moe_decode.h).
+"""ctypes view of libmoe_decode.so (the C ABI declared in include/moe_decode.h
+and include/moe_prompt.h).
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels. Importing this module fails loudly when the library has not been
@@ -19,6 +20,7 @@ MOE_FLAG_NO_PDL = 0x1
 MOE_FLAG_HOST_COPY = 0x2
 MOE_FLAG_MXFP4 = 0x4
 MOE_FLAG_WARP_MMA = 0x8
+MOE_PRODUCT_SILU_MUL = 0x10
 MOE_PATH_AUTO = 0
 MOE_PATH_WARP = 1
 MOE_PATH_TENSOR = 2
@@ -37,6 +39,12 @@ STATUS_NAMES = {
 class MoEConfig(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("k", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("I", ctypes.c_int32), ("max_T", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class MoEProductConfig(ctypes.Structure):
+    """moe_product_config_t."""
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
 
 
 class MoEError(RuntimeError):
@@ -83,6 +91,17 @@ SIGNATURES = {
                                        _p, _p]),
 }
 
+# the same for include/moe_prompt.h
+PROMPT_SIGNATURES = {
+    "moe_add_rms_norm": (_st, [_i32, _i32, _p, _p, _p, ctypes.c_float, _p, _p, _p, _p, _p]),
+    "moe_group": (_st, [_i32, _i32, _i32, _p, _p, _p, _p, _p]),
+    "moe_combine": (_st, [_i32, _i32, _i32, _i32, _p, _p, _p, _p, _p, _p]),
+    "moe_product_create": (_st, [ctypes.POINTER(MoEProductConfig), _p, _p, ctypes.POINTER(_p), _p]),
+    "moe_product_destroy": (_st, [_p]),
+    "moe_product_run": (_st, [_p, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p]),
+    "moe_product_get_error": (_st, [_p, _p, ctypes.POINTER(ctypes.c_uint32)]),
+}
+
 
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
@@ -90,7 +109,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             f"{path} is missing: build the CUDA library first "
             "(python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(path)
-    for name, (res, args) in SIGNATURES.items():
+    for name, (res, args) in {**SIGNATURES, **PROMPT_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

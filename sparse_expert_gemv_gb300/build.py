@@ -1,4 +1,6 @@
-"""Build libmoe_decode.so in-tree with nvcc for sm_103a (no cmake, one TU).
+"""Build libmoe_decode.so in-tree with nvcc for sm_103a (no cmake; the decode
+layer and the prompt operators are one translation unit each, compiled side by
+side).
 
     python -m sparse_expert_gemv_gb300.build
 """
@@ -11,7 +13,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRC = os.path.join(HERE, "csrc", "moe_decode.cu")
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_decode.cu", "moe_prompt.cu")]
 OUT = os.path.join(HERE, "libmoe_decode.so")
 # the same library with the one-launch kernel's per-CTA timeline compiled in
 # (-DMOE_TIMELINE: globaltimer stamps per CTA and phase, written to a
@@ -32,7 +34,7 @@ def command(out: str = OUT, extra=()) -> list[str]:
     cuda_lib = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "lib64")
     return [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
             "-cudart", "shared", f"-I{os.path.join(ROOT, 'include')}",
-            f"-Xlinker", f"-rpath,{cuda_lib}", *extra, SRC, "-o", out]
+            f"-Xlinker", f"-rpath,{cuda_lib}", "--threads", "0", *extra, *SRCS, "-o", out]
 
 
 def build(verbose: bool = False, timeline: bool = False) -> str:

@@ -1,0 +1,344 @@
+// The row operators of the layer's prompt form: the residual addition with
+// its root-mean-square norm and MXFP8 output, the grouping of routed slots by
+// expert, and the routing-weighted combination of expert rows.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "moe_device.cuh"
+
+namespace moe {
+
+// ---------------------------------------------------------------------------
+// MXFP8 quantisation
+// ---------------------------------------------------------------------------
+
+// Scale code of a block whose largest magnitude has the bits `amax`
+// (sign cleared): floor(log2 amax) - 8 + 127, i.e. the biased exponent less 8,
+// at least 0; 127 for a block of zeros; 255 (NaN) when a value of the block
+// is infinite or NaN (their bits compare above every finite value's).
+__device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax) {
+  const uint32_t b = amax >> 23;
+  uint32_t s = b > 8u ? b - 8u : 0u;
+  s = amax == 0u ? 127u : s;
+  return b == 255u ? 255u : s;
+}
+
+// 2^(127 - s), what a block's values are multiplied by before they round to
+// E4M3: a normal number for every code mx_scale_code gives (s <= 246); NaN
+// for 255, so that every code of such a block is NaN.
+__device__ __forceinline__ float mx_inverse(uint32_t s) {
+  return s == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - s) << 23);
+}
+
+// Two values -> two E4M3 codes (a in the low byte), rounded to nearest even
+// and saturated to 448; NaN -> 0x7F.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// rows in vectors: V = 8 bf16 values (16 bytes) or single values
+// ---------------------------------------------------------------------------
+template <int V>
+struct RowVec;
+
+template <>
+struct RowVec<8> {
+  __device__ __forceinline__ static void load(const uint16_t* p, float (&f)[8]) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+  }
+  __device__ __forceinline__ static uint32_t pack(float a, float b) {
+    return (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16);
+  }
+  __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+  }
+  __device__ __forceinline__ static void store_codes(uint8_t* p, const float (&f)[8]) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16),
+                                              e4m3x2(f[4], f[5]) | (e4m3x2(f[6], f[7]) << 16));
+  }
+};
+
+template <>
+struct RowVec<1> {
+  __device__ __forceinline__ static void load(const uint16_t* p, float (&f)[1]) {
+    f[0] = __uint_as_float((uint32_t)*p << 16);
+  }
+  __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[1]) {
+    *p = f32_to_bf16_rn(f[0]);
+  }
+  __device__ __forceinline__ static void store_codes(uint8_t* p, const float (&f)[1]) {
+    *p = (uint8_t)e4m3x2(f[0], f[0]);
+  }
+};
+
+// ---------------------------------------------------------------------------
+// moe_add_rms_norm_rows: one CTA a row. The row's sums stay in registers
+// (NV vectors of V values a thread) between the reduction and the outputs, so
+// every operand is read once and every output written once. A quantisation
+// block is 32 / V neighbouring lanes, whose largest magnitude is a butterfly
+// over them.
+// ---------------------------------------------------------------------------
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* residual;   // or null
+  const uint16_t* weight;
+  uint16_t* sum;              // or null; may be x or residual
+  uint16_t* y;                // or null
+  uint8_t* codes;             // or null (then scales too)
+  uint8_t* scales;
+  int H;
+  float eps;
+};
+
+constexpr int kNormMaxH = 16384;   // 1024 threads hold 16 values each
+
+template <int V, int NV>
+__global__ void __launch_bounds__(1024) moe_add_rms_norm_rows(const NormParams p) {
+  __shared__ float part[32];
+  const int H = p.H, nv = H / V;
+  const size_t base = (size_t)blockIdx.x * H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  float f[NV][V];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * blockDim.x + threadIdx.x;
+    if (v < nv) {
+      const size_t at = base + (size_t)v * V;
+      RowVec<V>::load(p.x + at, f[i]);
+      if (p.residual) {
+        float r[V];
+        RowVec<V>::load(p.residual + at, r);
+        // the residual stream is kept in bf16, and what is kept is normalised
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          f[i][j] = __uint_as_float((uint32_t)f32_to_bf16_rn(f[i][j] + r[j]) << 16);
+      }
+      if (p.sum) RowVec<V>::store(p.sum + at, f[i]);
+#pragma unroll
+      for (int j = 0; j < V; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) f[i][j] = 0.f;
+    }
+  }
+  ss = warp_sum(ss);
+  if (lane == 0) part[warp] = ss;
+  __syncthreads();
+  ss = warp_sum(lane < (int)(blockDim.x >> 5) ? part[lane] : 0.f);
+  const float r = rsqrtf(ss / (float)H + p.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int v = i * blockDim.x + threadIdx.x;
+    float n[V];
+    uint32_t amax = 0u;
+    if (v < nv) {
+      RowVec<V>::load(p.weight + (size_t)v * V, n);
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        n[j] = f[i][j] * r * n[j];
+        amax = max(amax, __float_as_uint(n[j]) & 0x7fffffffu);
+      }
+      if (p.y) RowVec<V>::store(p.y + base + (size_t)v * V, n);
+    }
+    if (p.codes) {   // H is a multiple of 32: a block's lanes are all in or all out
+#pragma unroll
+      for (int o = 16 / V; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(kFull, amax, o));
+      if (v < nv) {
+        const uint32_t s = mx_scale_code(amax);
+        const float inv = mx_inverse(s);
+#pragma unroll
+        for (int j = 0; j < V; ++j) n[j] *= inv;
+        RowVec<V>::store_codes(p.codes + base + (size_t)v * V, n);
+        if (v % (32 / V) == 0) p.scales[(base + (size_t)v * V) / 32] = (uint8_t)s;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// moe_group_slots: stable counting sort of S = T * k slots by expert, one
+// cluster of C CTAs (1 or kGroupCluster). The slots are cut into one
+// contiguous range per warp of the cluster. Each warp counts its range into a
+// table of its own (lanes of equal id find one another with a match, so no
+// atomics and a fixed order); the CTAs exchange their totals through
+// distributed shared memory; each warp then walks its range again and hands
+// out places.
+// ---------------------------------------------------------------------------
+constexpr int kGroupCluster = 8;
+constexpr int kGroupThreads = 1024;
+
+struct GroupParams {
+  const int32_t* ids;
+  int32_t* offsets;
+  int32_t* rows;
+  int32_t* slots;
+  int S, k, E;
+  int per_warp;   // slots a warp takes, a multiple of 32
+};
+
+__host__ __device__ constexpr size_t group_smem(int warps, int E) {
+  return (size_t)(warps + 2) * E * sizeof(int);
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Word `p` of this CTA's shared memory, read from CTA `rank` of the cluster.
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\t"
+      "ld.shared::cluster.b32 %0, [a];\n\t}"
+      : "=r"(v)
+      : "r"(smem_addr(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
+__global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupParams p) {
+  extern __shared__ int sm_group[];
+  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int E = p.E, C = gridDim.x, rank = blockIdx.x;
+  int* mine = sm_group;              // [E] this CTA's slots of each expert
+  int* start = mine + E;             // [E] all CTAs' slots, then the groups' starts
+  int* tab = start + E;              // [warps][E] each warp's count, then its next place
+  int* cnt = tab + warp * E;
+  pdl_wait();
+  for (int e = lane; e < E; e += 32) cnt[e] = 0;
+  __syncwarp();
+  const long long w0 = (long long)(rank * warps + warp) * p.per_warp;
+  const int lo = (int)min((long long)p.S, w0), hi = (int)min((long long)p.S, w0 + p.per_warp);
+  const unsigned below = (1u << lane) - 1u;
+  for (int s = lo; s < hi; s += 32) {
+    int e = s + lane < hi ? p.ids[s + lane] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const unsigned same = __match_any_sync(kFull, e);
+    if (e >= 0 && (same & below) == 0u) cnt[e] += __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int sum = 0;
+    for (int w = 0; w < warps; ++w) {
+      const int c = tab[w * E + e];
+      tab[w * E + e] = sum;
+      sum += c;
+    }
+    mine[e] = sum;
+  }
+  if (C > 1) cluster_sync(); else __syncthreads();
+  // experts' totals, and what lower CTAs place before this one's slots
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    int total = 0, before = 0;
+    for (int c = 0; c < C; ++c) {
+      const int v = C > 1 ? ld_cluster(mine + e, c) : mine[e];
+      if (c < rank) before += v;
+      total += v;
+    }
+    start[e] = total;
+    for (int w = 0; w < warps; ++w) tab[w * E + e] += before;
+  }
+  // no CTA leaves (or changes `mine`) while another still reads it
+  if (C > 1) cluster_sync(); else __syncthreads();
+  if (warp == 0) {   // exclusive prefix over the experts
+    int carry = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int v = e0 + lane < E ? start[e0 + lane] : 0;
+      int incl = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += u;
+      }
+      if (e0 + lane < E) {
+        start[e0 + lane] = carry + incl - v;
+        if (rank == 0) p.offsets[e0 + lane] = carry + incl - v;
+      }
+      carry += __shfl_sync(kFull, incl, 31);
+    }
+    if (lane == 0) {
+      mine[0] = carry;   // rows in all groups
+      if (rank == 0) p.offsets[E] = carry;
+    }
+  }
+  __syncthreads();
+  for (int s = lo; s < hi; s += 32) {
+    const bool in = s + lane < hi;
+    int e = in ? p.ids[s + lane] : -1;
+    if (e < 0 || e >= E) e = -1;
+    const unsigned same = __match_any_sync(kFull, e);
+    int q = -1;
+    if (e >= 0) q = start[e] + cnt[e] + __popc(same & below);
+    __syncwarp();
+    if (e >= 0 && (same & below) == 0u) cnt[e] += __popc(same);
+    __syncwarp();
+    if (in) p.slots[s + lane] = q;
+    if (q >= 0) p.rows[q] = (s + lane) / p.k;
+  }
+  // rows past the last group
+  const int used = mine[0];
+  for (long long r = (long long)used + rank * blockDim.x + threadIdx.x; r < p.S;
+       r += (long long)C * blockDim.x)
+    p.rows[r] = -1;
+}
+
+// ---------------------------------------------------------------------------
+// moe_combine_rows: a thread owns V neighbouring values of one token's output
+// and adds that token's rows in slot order (no atomics, a fixed order).
+// ---------------------------------------------------------------------------
+struct CombineParams {
+  const uint16_t* y;
+  const int32_t* slots;
+  const float* w;
+  const uint16_t* residual;   // or null
+  uint16_t* out;
+  int k, H, R;
+  int nb;                     // CTAs a token
+};
+
+constexpr int kCombineThreads = 256;
+
+template <int V>
+__global__ void __launch_bounds__(kCombineThreads) moe_combine_rows(const CombineParams p) {
+  const int t = blockIdx.x / p.nb;
+  const int v = (blockIdx.x % p.nb) * blockDim.x + threadIdx.x;
+  pdl_wait();
+  if (v >= p.H / V) return;
+  float acc[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) acc[j] = 0.f;
+  const int32_t* slots = p.slots + (size_t)t * p.k;
+  const float* w = p.w + (size_t)t * p.k;
+#pragma unroll 4
+  for (int j = 0; j < p.k; ++j) {
+    const int q = slots[j];
+    if (q < 0 || q >= p.R) continue;
+    const float wj = w[j];
+    float f[V];
+    RowVec<V>::load(p.y + (size_t)q * p.H + (size_t)v * V, f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
+  }
+  const size_t at = (size_t)t * p.H + (size_t)v * V;
+  if (p.residual) {
+    float f[V];
+    RowVec<V>::load(p.residual + at, f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] += f[i];
+  }
+  RowVec<V>::store(p.out + at, acc);
+}
+
+}  // namespace moe

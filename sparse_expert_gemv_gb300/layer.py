@@ -11,42 +11,8 @@ import torch
 
 from ._lib import (MOE_FLAG_MXFP4, MOE_PATH_AUTO, MOE_PATH_TENSOR, MOE_PATH_WARP, MoEConfig, check,
                    lib)
-
-
-def _ptr(t: torch.Tensor | None) -> int:
-    # a plain int: the entry points' argtypes make it a void*
-    return 0 if t is None else t.data_ptr()
-
-
-def _stream(stream: torch.cuda.Stream | None) -> int:
-    if stream is not None:
-        return stream.cuda_stream
-    # the current stream's handle, without building a Stream object per call
-    # where torch offers that
-    if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
-    return torch.cuda.current_stream().cuda_stream
-
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _need(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str, cuda: bool = True) -> None:
-    # one cheap test on the common path; the detailed ones only on failure
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
-            and t.is_cuda is cuda and t.is_contiguous()):
-        return
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if cuda and not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    raise ValueError(f"{name} must be a host tensor")
+from ._tensors import _need, _ptr, _stream
+from .prompt import GroupedProduct, combine, group_by_expert
 
 
 class MoEDecode:
@@ -73,6 +39,7 @@ class MoEDecode:
         _need(s_down, torch.uint8, (E, H, I // 32), "s_down")
         self.E, self.k, self.H, self.I, self.max_T, self.fmt = E, k, H, I, max_T, fmt
         self._weights = (w_gateup, s_gateup, w_down, s_down)
+        self._products = None       # prompt()'s two GroupedProducts
         if fmt == "mxfp4":
             flags |= MOE_FLAG_MXFP4
         cfg = MoEConfig(E, k, H, I, max_T, flags)
@@ -87,6 +54,7 @@ class MoEDecode:
         if getattr(self, "_h", None):
             lib.moe_decode_destroy(self._h)
             self._h = None
+        self._products = None
 
     def __del__(self):
         try:
@@ -202,6 +170,26 @@ class MoEDecode:
                                           _stream(stream)), "moe_decode_forward_host")
         return y
 
+    def prompt(self, codes, scales, ids, w, residual=None, out=None, stream=None):
+        """The routed experts over a prompt's MXFP8 rows (codes uint8 [T, H],
+        scales uint8 [T, H/32], e.g. add_rms_norm's): grouping, both products
+        on the tensor cores with h in MXFP8, and the weighted sum with
+        `residual` (bf16 [T, H], optional) added; bf16 [T, H]. T is not bound
+        by max_T. The first call lays out the weights' scales for the two
+        products (see GroupedProduct), which the layer then keeps."""
+        if stream is not None:      # the intermediates belong to that stream too
+            with torch.cuda.stream(stream):
+                return self.prompt(codes, scales, ids, w, residual, out)
+        if self._products is None:
+            wgu, sgu, wd, sd = self._weights
+            self._products = (GroupedProduct(wgu, sgu, fmt=self.fmt, silu_mul=True),
+                              GroupedProduct(wd, sd, fmt=self.fmt))
+        gate_up, down = self._products
+        _need(ids, torch.int32, (codes.shape[0], self.k), "topk_ids")
+        offsets, rows, slots = group_by_expert(ids, self.E)
+        hc, hs = gate_up(codes, scales, offsets, rows)
+        return combine(down(hc, hs, offsets), slots, w, residual=residual, out=out)
+
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits. Waits for this
         handle's latest call, or, given a stream, for that stream."""
@@ -212,4 +200,6 @@ class MoEDecode:
             st = lib.moe_decode_get_error_stream(self._h, _stream(stream), ctypes.byref(flags))
         if st not in (0, 5):
             check(st, "moe_decode_get_error")
+        for p in self._products or ():
+            flags.value |= p.get_error(stream)
         return int(flags.value)

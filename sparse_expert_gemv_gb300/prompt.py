@@ -1,0 +1,194 @@
+"""The operators around the routed experts for calls of many tokens.
+
+The mixture-of-experts half of a transformer block over a prompt, with MXFP8
+activations between the operators (include/moe_prompt.h states each one's
+arithmetic):
+
+    n = add_rms_norm(x, weight, residual)              # n.sum, n.y, n.codes, n.scales
+    ids, w = layer.route(router_logits(n.y))
+    offsets, rows, slots = group_by_expert(ids, E)
+    hc, hs = gate_up(n.codes, n.scales, offsets, rows=rows)   # GroupedProduct, silu_mul=True
+    y = down(hc, hs, offsets)                                 # GroupedProduct
+    out = combine(y, slots, w, residual=n.sum)
+
+MoEDecode.prompt is the part after the router on a layer's own weights. As in
+the decode layer, every call forwards device pointers and a stream to
+libmoe_decode.so; nothing is computed here.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from ._lib import MOE_FLAG_MXFP4, MOE_PRODUCT_SILU_MUL, MoEProductConfig, check, lib
+from ._tensors import _need, _ptr, _stream
+
+
+class RmsNorm(NamedTuple):
+    """What add_rms_norm returns; outputs that were not asked for are None."""
+    sum: torch.Tensor | None      # bf16 [T, H]: the new residual stream
+    y: torch.Tensor | None        # bf16 [T, H]: the normalised rows
+    codes: torch.Tensor | None    # uint8 [T, H]: their E4M3 codes
+    scales: torch.Tensor | None   # uint8 [T, H/32]: and UE8M0 scale codes
+
+
+def _matrix(t, dtype, name) -> tuple:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected two dimensions, got {t.dim()}")
+    _need(t, dtype, t.shape, name)
+    return t.shape
+
+
+def _out(t, dtype, shape, name, like):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _need(t, dtype, shape, name)
+    return t
+
+
+def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = True,
+                 mxfp8: bool = False, sum=None, y=None, codes=None, scales=None,
+                 stream=None) -> RmsNorm:
+    """The residual stream s = bf16(x + residual) and s * rsqrt(mean(s^2) + eps) * weight,
+    in bf16 (`bf16`), as MXFP8 codes and scales (`mxfp8`), or both.
+
+    x and residual are bf16 [T, H], weight is bf16 [H]. Without a residual, s
+    is x and RmsNorm.sum is None (unless a buffer for it is passed). The
+    buffers sum, y, codes and scales may be passed in; sum may be x or
+    residual, which is then updated in place.
+    """
+    T, H = _matrix(x, torch.bfloat16, "x")
+    _need(weight, torch.bfloat16, (H,), "weight")
+    if residual is not None:
+        _need(residual, torch.bfloat16, (T, H), "residual")
+    if not (bf16 or mxfp8):
+        raise ValueError("add_rms_norm: ask for bf16 rows, mxfp8 rows or both")
+    if sum is not None or residual is not None:
+        sum = _out(sum, torch.bfloat16, (T, H), "sum", x)
+    y = _out(y, torch.bfloat16, (T, H), "y", x) if bf16 else None
+    if mxfp8:
+        codes = _out(codes, torch.uint8, (T, H), "codes", x)
+        scales = _out(scales, torch.uint8, (T, H // 32), "scales", x)
+    else:
+        codes = scales = None
+    check(lib.moe_add_rms_norm(T, H, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(sum),
+                               _ptr(y), _ptr(codes), _ptr(scales), _stream(stream)),
+          "moe_add_rms_norm")
+    return RmsNorm(sum, y, codes, scales)
+
+
+def group_by_expert(ids, E: int, *, offsets=None, rows=None, slots=None, stream=None):
+    """(offsets, rows, slots) of routed ids int32 [T, k]: group e is the rows
+    offsets[e] .. offsets[e + 1] - 1 in the order of the slots t * k + j;
+    rows[q] is the token of grouped row q (-1 past the last group) and
+    slots[t, j] the grouped row of a slot (-1 for an id outside [0, E), which
+    joins no group)."""
+    T, k = _matrix(ids, torch.int32, "ids")
+    offsets = _out(offsets, torch.int32, (E + 1,), "offsets", ids)
+    rows = _out(rows, torch.int32, (T * k,), "rows", ids)
+    slots = _out(slots, torch.int32, (T, k), "slots", ids)
+    check(lib.moe_group(T, k, E, _ptr(ids), _ptr(offsets), _ptr(rows), _ptr(slots),
+                        _stream(stream)), "moe_group")
+    return offsets, rows, slots
+
+
+def combine(y, slots, w, *, residual=None, out=None, stream=None):
+    """out[t] = bf16(residual[t] + sum_j w[t, j] * y[slots[t, j]]) over expert
+    rows y bf16 [R, H], slots int32 [T, k] (outside [0, R): nothing) and w
+    float32 [T, k]; residual bf16 [T, H] is optional and may be `out`."""
+    R, H = _matrix(y, torch.bfloat16, "y")
+    T, k = _matrix(slots, torch.int32, "slots")
+    _need(w, torch.float32, (T, k), "w")
+    if residual is not None:
+        _need(residual, torch.bfloat16, (T, H), "residual")
+    out = _out(out, torch.bfloat16, (T, H), "out", y)
+    check(lib.moe_combine(T, k, H, R, _ptr(y), _ptr(slots), _ptr(w), _ptr(residual), _ptr(out),
+                          _stream(stream)), "moe_combine")
+    return out
+
+
+class GroupedProduct:
+    """Ragged products of grouped MXFP8 rows with one stack of expert weights.
+
+    fmt="mxfp8": w uint8 [E, N, K]; fmt="mxfp4": w uint8 [E, N, K/2]; w_scales
+    uint8 [E, N, K/32]. With silu_mul the N = 2I rows of an expert are I gate
+    rows and I up rows, and the product is finished to MXFP8(SiLU(g) * u).
+    The weights are borrowed (kept alive by this object); the scales are
+    copied once into the order in which the tensor cores take them.
+    """
+
+    def __init__(self, w, w_scales, *, fmt: str = "mxfp8", silu_mul: bool = False, stream=None):
+        if fmt not in ("mxfp8", "mxfp4"):
+            raise ValueError(f"fmt must be 'mxfp8' or 'mxfp4', got {fmt!r}")
+        per = 2 if fmt == "mxfp4" else 1
+        if not isinstance(w, torch.Tensor):
+            raise TypeError("w must be a torch.Tensor")
+        if w.dim() != 3:
+            raise ValueError(f"w: expected three dimensions, got {w.dim()}")
+        E, N, RB = w.shape
+        K = RB * per
+        _need(w, torch.uint8, (E, N, RB), "w")
+        _need(w_scales, torch.uint8, (E, N, K // 32), "w_scales")
+        self.E, self.N, self.K, self.fmt, self.silu_mul = E, N, K, fmt, silu_mul
+        self._weights = (w, w_scales)
+        flags = (MOE_FLAG_MXFP4 if fmt == "mxfp4" else 0) | (MOE_PRODUCT_SILU_MUL if silu_mul else 0)
+        h = ctypes.c_void_p()
+        check(lib.moe_product_create(ctypes.byref(MoEProductConfig(E, N, K, flags)), _ptr(w),
+                                     _ptr(w_scales), ctypes.byref(h), _stream(stream)),
+              "moe_product_create")
+        self._h = h
+
+    def close(self) -> None:
+        if getattr(self, "_h", None):
+            lib.moe_product_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    @property
+    def handle(self) -> ctypes.c_void_p:
+        return self._h
+
+    def __call__(self, a, a_scales, offsets, rows=None, *, out=None, out_scales=None, stream=None):
+        """For every expert e, rows offsets[e] .. offsets[e + 1] - 1 of the
+        result from the MXFP8 rows a[rows[q]] (a[q] without `rows`) uint8
+        [A, K] with scales uint8 [A, K/32]: bf16 [R, N], or with silu_mul the
+        pair codes uint8 [R, I], scales uint8 [R, I/32]. R is the length of
+        `rows`, or A. Rows outside every group are left as they are."""
+        A = a.shape[0]
+        _need(a, torch.uint8, (A, self.K), "a")
+        _need(a_scales, torch.uint8, (A, self.K // 32), "a_scales")
+        _need(offsets, torch.int32, (self.E + 1,), "offsets")
+        R = A
+        if rows is not None:
+            R = rows.shape[0]
+            _need(rows, torch.int32, (R,), "rows")
+        if self.silu_mul:
+            I = self.N // 2
+            codes = _out(out, torch.uint8, (R, I), "out", a)
+            scales = _out(out_scales, torch.uint8, (R, I // 32), "out_scales", a)
+            check(lib.moe_product_run(self._h, R, A, _ptr(a), _ptr(a_scales), _ptr(offsets),
+                                      _ptr(rows), 0, _ptr(codes), _ptr(scales), _stream(stream)),
+                  "moe_product_run")
+            return codes, scales
+        y = _out(out, torch.bfloat16, (R, self.N), "out", a)
+        check(lib.moe_product_run(self._h, R, A, _ptr(a), _ptr(a_scales), _ptr(offsets), _ptr(rows),
+                                  _ptr(y), 0, 0, _stream(stream)), "moe_product_run")
+        return y
+
+    def get_error(self, stream=None) -> int:
+        """Read and clear the handle's device error bits, after waiting for the
+        stream."""
+        flags = ctypes.c_uint32(0)
+        st = lib.moe_product_get_error(self._h, _stream(stream), ctypes.byref(flags))
+        if st not in (0, 5):
+            check(st, "moe_product_get_error")
+        return int(flags.value)
