@@ -4,18 +4,22 @@
 // along K, and the tensor cores apply the scales.
 //
 // Operands are swapped: an expert's weight rows are the MMA's M dimension
-// (128 a tile, always full) and the rows of its group the N dimension (16 to
-// kProdCols a tile, in steps of 16), so a ragged group wastes at most 15
-// columns where the other way round it would waste up to 127 rows.
+// (256 a tile over the two SMs of a CTA pair) and the rows of its group the N
+// dimension (32 to kProdCols a tile, in steps of 32), so a ragged group
+// wastes at most 31 columns where the other way round it would waste up to
+// 255 rows.
 //
-// One persistent CTA an SM walks the tiles (token tile of a group, 128 weight
-// rows), found from the offsets on the device. Roles:
-//   warp 0       weights, their scales and the group's rows by TMA (gathered
-//                rows with the four-row gather form), per stage of 128 K
-//   warp 1       scales to tensor memory (tcgen05.cp) and the MMAs
+// One persistent pair of CTAs (a cluster of 2, cta_group::2) a pair of SMs
+// walks the tiles (token tile of a group, 256 weight rows), found from the
+// offsets on the device. Each CTA holds 128 of the weight rows and half of the
+// group's rows in shared memory, per stage of 128 K, and its 128 rows of the
+// accumulator in tensor memory; the first CTA issues the MMAs of both. Roles:
+//   warp 0       weights by TMA
+//   warp 1       (first CTA) scales to tensor memory (tcgen05.cp) and the MMAs
+//   warp 2       the group's rows by TMA, where they are contiguous
 //   warps 4-7    epilogue, one per lane quarter of tensor memory
-//   warps 8-11   the rows' scales: gathered words to shared memory in the
-//                order tcgen05.cp takes
+//   warps 8-11   scales, four stages at a time, into shared memory in the order
+//                tcgen05.cp takes; and the group's rows where they are gathered
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
 // the next tile's MMAs.
 #pragma once
@@ -30,29 +34,38 @@
 
 namespace moe {
 
-constexpr int kProdRows = 128;     // weight rows a tile (M)
-// Rows of a group a tile (N). Two accumulators of 224 columns and four
-// stages' scales (12 columns each) share the 512 columns of tensor memory.
-constexpr int kProdCols = 224;
+constexpr int kProdRows = 128;     // weight rows a CTA (half of the MMA's M)
+// Rows of a group a tile (N). Two accumulators of 192 columns and two batches
+// of four stages' scales (12 columns a stage) share the 512 columns of tensor
+// memory.
+constexpr int kProdCols = 192;
 constexpr int kProdK = 128;        // K elements a stage: one 128-byte swizzle row
-constexpr int kProdStages = 4;
-constexpr int kProdBox = 32;       // rows of a TMA box when rows are contiguous
+constexpr int kProdStages = 6;
+constexpr int kProdSfStages = 4;   // stages a batch of scales covers
 constexpr int kProdThreads = 384;
 constexpr int kProdMaxE = 1024;
 constexpr int kProdABytes = kProdRows * kProdK;
-constexpr int kProdBBytes = kProdCols * kProdK;
-constexpr int kProdSfaBytes = 512;
-constexpr int kProdSfbBytes = 1024;
+constexpr int kProdBBytes = kProdCols / 2 * kProdK;
+constexpr int kProdSfaBytes = 512;    // a stage's weight scales of one CTA
+constexpr int kProdSfbBytes = 1024;   // a stage's row scales (up to 256 rows)
+constexpr int kProdSfBytes = kProdSfStages * (kProdSfaBytes + kProdSfbBytes);
+constexpr int kProdGatherLag = 4;     // gathered stages in flight behind the newest
 // tensor-memory columns
 constexpr uint32_t kProdTmemCols = 512;
 constexpr uint32_t kProdSfCol = 2 * kProdCols;
-constexpr uint32_t kProdSfCols = 12;   // 4 of the weights' scales, 8 of the rows'
-static_assert(2 * kProdCols + kProdStages * kProdSfCols <= kProdTmemCols, "tensor memory");
-static_assert(kProdCols % kProdBox == 0 && kProdCols <= 256, "token tile");
+constexpr uint32_t kProdSfCols = 12;   // a stage's: 4 of the weights, 8 of the rows
+static_assert(2 * kProdCols + 2 * kProdSfStages * kProdSfCols <= kProdTmemCols, "tensor memory");
+static_assert(kProdCols % 32 == 0 && kProdCols <= 256, "token tile");
+static_assert(kProdGatherLag < kProdStages, "a stage is handed over before its slot is due again");
+// epilogue staging: a chunk of 32 columns as rows of 128 bf16 (16-byte pieces
+// swizzled by the row), or of 64 codes padded to 80 bytes, two chunks in turn
+constexpr int kProdStageOut = 32 * 256;
+constexpr int kProdCodePitch = 80;
 
 struct ProductParams {
   CUtensorMap tm_w;
-  CUtensorMap tm_a;        // boxes of kProdBox rows, or of one row to gather
+  CUtensorMap tm_a[3];     // boxes of 16, 32 and 64 contiguous rows
+  const uint8_t* a;        // [A, K]
   const uint8_t* sfa;      // weights' scales in tile order (moe_product_lay_scales)
   const uint8_t* a_scales; // [A, K/32]
   const int32_t* offsets;  // [E + 1]
@@ -62,105 +75,184 @@ struct ProductParams {
   uint8_t* scales;         // [R, N/64]
   uint32_t* err;
   int E, N, K, R, A;
-  int mt;                  // weight tiles of an expert
+  int mt;                  // tiles of kProdRows weight rows an expert has
   int sf_vec;              // scale bytes a load may take: 16, 4 or 1
-  uint32_t w_bytes;        // bytes a weight tile's copy completes
+  uint32_t w_bytes;        // bytes a CTA's weight copy completes
   uint32_t a_format;       // the MMA's code for the weights' element type
 };
 
 struct ProductSmem {
   static constexpr int a = 0;
   static constexpr int b = a + kProdStages * kProdABytes;
-  static constexpr int sfa = b + kProdStages * kProdBBytes;
-  static constexpr int sfb = sfa + kProdStages * kProdSfaBytes;
-  static constexpr int amax = sfb + kProdStages * kProdSfbBytes;   // [2][4][32] words
-  static constexpr int off = amax + 2 * 4 * 32 * 4;                // [E + 1] group starts
+  static constexpr int sf = b + kProdStages * kProdBBytes;         // 2 batches
+  static constexpr int out = sf + 2 * kProdSfBytes;                // 2 chunks
+  static constexpr int amax = out + 2 * kProdStageOut;             // [2][4][32] words
+  static constexpr int inv = amax + 2 * 4 * 32 * 4;                // [4][32] floats
+  static constexpr int off = inv + 4 * 32 * 4;                     // [E + 1] group starts
   static constexpr int tiles = off + (kProdMaxE + 4) * 4;          // [E + 1] token tiles before
   static constexpr int bars = tiles + (kProdMaxE + 4) * 4;
-  static constexpr int total = bars + (3 * kProdStages + 5) * 8 + 16;
+  static constexpr int total = bars + (2 * kProdStages + 9) * 8 + 16;
 };
 
 namespace tc {
 
-__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, int c0, int c1, int c2,
-                                            int c3, int c4, uint64_t* bar) {
+// True in one lane of a converged warp, always the same one. The tensor-memory
+// and TMA instructions take their operands in registers that the whole warp
+// shares; issued under this predicate in a loop that all lanes walk they cost
+// a few cycles each, where a loop walked by lane 0 alone cost 60 to 80 (the
+// pipeline then waited for them: 1024 cycles a stage at 384 of MMA).
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-      "%3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_addr(bar))
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
-// Four rows of a tensor map whose box is one row.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, const int4& r,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-      "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
-      "l"(tmap), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(smem_addr(bar))
-      : "memory");
+// The address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  return a;
+}
+// One arrival on an mbarrier of the cluster.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 512 bytes of scales (32 lanes of 16) -> 4 columns of tensor memory, repeated
-// in its four lane quarters.
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t desc =
-      (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                : "memory");
 }
 
-// D (+)= A * B^T with the operands' block scales.
+// Tensor-map tiles into this CTA's shared memory, completing on an mbarrier of
+// either CTA of the pair.
+__device__ __forceinline__ void tma2_load_2d(void* dst, const void* tmap, int x, int y,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_load_3d(void* dst, const void* tmap, int x, int y, int z,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma2_load_5d(void* dst, const void* tmap, int c0, int c1, int c2,
+                                             int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+
+// 16 bytes global -> shared in the issuing thread's copy group; `bytes` 0
+// fills with zeros and reads nothing.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// 512 bytes of scales (32 lanes of 16) at the same place of both CTAs' shared
+// memory -> 4 columns of their tensor memory, repeated in its four quarters.
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc =
+      (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+
+// D (+)= A * B^T with the operands' block scales, over both CTAs.
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
       "[%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
 }
 
 // Instruction descriptor of kind::mxf8f6f4: A of format `fa` (0 E4M3, 5 E2M1),
-// B E4M3, both K-major, M = 128, N = n, UE8M0 scales; the scale byte of the
-// K = 32 step is added by mx_scale_id.
+// B E4M3, both K-major, M = 256 over the pair, N = n, UE8M0 scales; the scale
+// byte of the K = 32 step is added by mx_scale_id.
 __device__ __forceinline__ uint32_t mx_idesc(uint32_t fa, int n) {
-  return (fa << 7) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kProdRows >> 4) << 24);
+  return (fa << 7) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+         ((uint32_t)(2 * kProdRows >> 4) << 24);
 }
 __device__ __forceinline__ uint32_t mx_scale_id(uint32_t j) { return (j << 4) | (j << 29); }
 
-// 32 consecutive columns of this warp's 32 lanes.
-__device__ __forceinline__ void ld32(uint32_t taddr, uint32_t (&v)[32]) {
+// Arrive once on the mbarrier at `bar` of both CTAs when every MMA and copy
+// this thread issued so far is done.
+__device__ __forceinline__ void commit2(uint64_t* bar) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// 32 columns of lanes 0-15 of this warp's quarter (16-31 from taddr + 16
+// lanes): register 4b + 2i + j of thread t holds lane 8i + t / 4, column
+// 8b + 2 (t % 4) + j.
+__device__ __forceinline__ void ld_16x32(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]),
         "=r"(v[7]), "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]),
-        "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]),
-        "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]),
-        "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        "=r"(v[14]), "=r"(v[15])
       : "r"(taddr)
       : "memory");
+}
+
+// Four transposed 8x8 matrices of 16-bit values: thread t's register m holds
+// rows 2 (t % 4) + {0, 1}, column t / 4 of matrix m, whose row r goes to the
+// 16 bytes at the address of lane 8m + r.
+__device__ __forceinline__ void stm4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
 }
 
 }  // namespace tc
 
 // ---------------------------------------------------------------------------
 // moe_product_lay_scales: the weights' scales in the order tcgen05.cp takes
-// them, once per handle: for (expert, weight tile, stage) 512 bytes, lane l's
+// them, once per handle: for (expert, 128-row tile, stage) 512 bytes, lane l's
 // 16 holding four scale bytes of each of the MMA rows l, l + 32, l + 64,
 // l + 96. Places past N or K get 1 (their codes arrive as zeros).
 // ---------------------------------------------------------------------------
-// Weight row of an expert that MMA row `r` of tile m stands for. With SILU_MUL
-// a tile is 64 gate rows and their 64 up rows in turns of 16, so that a gate
-// and its up value meet in one warp of the epilogue; valid while the row's
-// neuron is below I.
+// Weight row of an expert that MMA row `r` of 128-row tile m stands for. With
+// SILU_MUL a tile is 64 neurons in four groups of 16: a group's 16 gate rows,
+// then its 16 up rows, even neurons before odd ones, so that one thread of the
+// epilogue holds the gates and ups of two neighbouring neurons. False past the
+// last row.
 __host__ __device__ __forceinline__ bool product_row(bool silu, int N, int m, int r, int& row) {
   if (!silu) {
     row = m * kProdRows + r;
     return row < N;
   }
-  const int I = N / 2, i = m * 64 + (r >> 5) * 16 + (r & 15);
+  const int I = N / 2, i = m * 64 + (r >> 5) * 16 + 2 * (r & 7) + ((r >> 3) & 1);
   row = ((r >> 4) & 1) * I + i;
   return i < I;
 }
@@ -186,11 +278,28 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
 // moe_product_tiles
 // ---------------------------------------------------------------------------
 
-// Bounded wait; a timeout marks the CTA dead (every role winds down).
+// Bounded wait on a phase of this CTA's mbarrier that either CTA's arrivals
+// complete; a timeout marks the CTA dead (every role winds down).
+__device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                           volatile int* dead) {
-  if (*dead) return false;
-  if (mbar_wait(bar, parity, err)) return true;
+  if (prod_poll(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t it = 0; it < kMbarPolls; ++it) {
+    if (*dead) return false;
+    if (prod_poll(bar, parity)) return true;
+  }
+  atomicOr(err, kDeviceTimeout);
   *dead = 1;
   return false;
 }
@@ -213,35 +322,44 @@ __device__ __forceinline__ bool named_all(int id, int nthreads, bool ok) {
   return r != 0;
 }
 
+// The value of lane 0, which all lanes hold already: tells the compiler that
+// it is the same in the whole warp, so that what follows from it (loop bounds,
+// descriptors, tensor-memory addresses) is computed once a warp and reaches
+// the tensor-memory instructions without a move per operand.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(kFull, v, 0); }
+
 struct ProductTile {
   int e, m;
   int r0, n;   // first row and rows (1..kProdCols) of the group's piece
+  // the MMA's N and each CTA's half of it
+  __device__ __forceinline__ int cols() const { return (n + 31) & ~31; }
+  __device__ __forceinline__ int half() const { return cols() >> 1; }
 };
 
-// Tile `i` of the walk: weight tiles of one token tile in turn, so that CTAs
-// working side by side share its rows in L2. A group of c rows is cut into
-// the fewest pieces, of equal size but for rounding to 16.
-__device__ __forceinline__ ProductTile product_tile(int i, int mt, int E, const int* off,
-                                                    const int* tiles) {
+// Tile `i` of the walk: the pairs of weight tiles of one token tile in turn,
+// so that pairs of CTAs working side by side share its rows in L2. A group of
+// c rows is cut into the fewest pieces, of equal size but for rounding to 32.
+__device__ __forceinline__ ProductTile product_tile(int i, int rank, int pairs, int E,
+                                                    const int* off, const int* tiles) {
   ProductTile t;
-  const int q = i / mt;
-  t.m = i - q * mt;
+  const int q = i / pairs;
+  t.m = 2 * (i - q * pairs) + rank;
   int lo = 0, hi = E;   // tiles[lo] <= q < tiles[hi]
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (tiles[mid] <= q) lo = mid; else hi = mid;
   }
-  t.e = lo;
   const int pieces = tiles[lo + 1] - tiles[lo], j = q - tiles[lo];
   const int c = off[lo + 1] - off[lo];
-  const int b = ((c + pieces - 1) / pieces + 15) & ~15;
-  t.r0 = off[lo] + j * b;
-  t.n = min(b, c - j * b);
+  const int b = ((c + pieces - 1) / pieces + 31) & ~31;
+  t.e = uniform(lo);
+  t.r0 = uniform(off[lo] + j * b);
+  t.n = uniform(min(b, c - j * b));
   return t;
 }
 
-// Four stages' scale bytes (16) of one row from stage kb on; bytes past the
-// row's end read as 127.
+// A batch's scale bytes (16, four stages) of one row from stage kb on; bytes
+// past the row's end read as 127.
 __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int ks, int vec) {
   if (vec == 16) return *reinterpret_cast<const uint4*>(row + kb * 4);
   uint32_t w[4];
@@ -260,6 +378,40 @@ __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What a thread of the scale warps holds of a tile: the two rows (r and
+// r + 128 of the tile) whose scales it brings, and with gathered rows the
+// rows of this CTA's half that it copies 16 bytes a stage of. load() only
+// issues the loads of gathered rows; settle() uses them, a tile later.
+struct ProductRows {
+  int scale_row[2];
+  int copy_row[kProdCols / 32];
+  ProductTile t;
+  __device__ __forceinline__ void load(const ProductParams& p, const ProductTile& tile, int rank,
+                                       int r) {
+    t = tile;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      scale_row[h] = t.r0 + min(r + 128 * h, t.n - 1);
+      if (p.rows) scale_row[h] = p.rows[scale_row[h]];
+    }
+    if (p.rows) {
+      const int half = t.half();
+#pragma unroll
+      for (int i = 0; i < kProdCols / 32; ++i)
+        if (16 * i < half)
+          copy_row[i] = p.rows[t.r0 + min(rank * half + (r >> 3) + 16 * i, t.n - 1)];
+    }
+  }
+  __device__ __forceinline__ void settle(const ProductParams& p) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) scale_row[h] = min(max(scale_row[h], 0), p.A - 1);
+    if (p.rows) {
+#pragma unroll
+      for (int i = 0; i < kProdCols / 32; ++i) copy_row[i] = min(max(copy_row[i], 0), p.A - 1);
+    }
+  }
+};
+
 template <bool SILU>
 __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     const __grid_constant__ ProductParams p) {
@@ -269,35 +421,41 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   using L = ProductSmem;
   int* off = reinterpret_cast<int*>(smem + L::off);
   int* tiles = reinterpret_cast<int*>(smem + L::tiles);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
-  uint64_t* sfb_full = full + kProdStages;
-  uint64_t* empty = sfb_full + kProdStages;
-  uint64_t* d_full = empty + kProdStages;
-  uint64_t* d_empty = d_full + 2;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
+  uint64_t* empty = full + kProdStages;
+  uint64_t* sf_full = empty + kProdStages;                        // used in the first CTA
+  uint64_t* sf_empty = sf_full + 2;
+  uint64_t* d_full = sf_empty + 2;
+  uint64_t* d_empty = d_full + 2;                                 // used in the first CTA
   uint64_t* drain = d_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;   // clusters are pairs of neighbours
   const int nk = (p.K + kProdK - 1) / kProdK;
+  const int pairs = (p.mt + 1) / 2;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
 
   if (warp == 0 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
-    tc::prefetch_tmap(&p.tm_a);
     for (int i = 0; i < kProdStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&sfb_full[i], 4);   // the scale warps
+      // the announcement of both CTAs' TMA bytes; gathered rows add the eight
+      // warps that copy them
+      mbar_init(&full[i], p.rows ? 9 : 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sf_full[i], 8);    // both CTAs' scale warps
+      mbar_init(&sf_empty[i], 1);
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 4);    // the epilogue warps
+      mbar_init(&d_empty[i], 8);    // both CTAs' epilogue warps
     }
     mbar_init(drain, 1);
     *dead = 0;
     mbar_init_fence();
   }
-  if (warp == 1) tc::tmem_alloc(tmem_slot, kProdTmemCols);
+  if (warp == 1) tc::tmem_alloc2(tmem_slot, kProdTmemCols);
   pdl_wait();
   if (warp == 2) {   // groups and the token tiles before each
     int carry = 0;
@@ -326,241 +484,356 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   }
   tc::fence_before();
   __syncthreads();
+  cluster_sync();   // the other CTA's barriers are ready too
   tc::fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int ntiles = tiles[p.E] * p.mt;
+  // all of tensor memory is this CTA's, so its columns start at 0
+  constexpr uint32_t tmem = 0;
+  const int ntiles = uniform(tiles[p.E] * pairs);
 
   if (warp == 0) {
-    // ------------------------------------------------------------ TMA copies
+    // --------------------------------------------------------------- weights
     RingPos rg(kProdStages);
+    const uint32_t full0 = tc::cluster_addr(full, 0);
     int g = 0;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < ntiles; i += gridDim.x) {
-      const ProductTile t = product_tile(i, p.mt, p.E, off, tiles);
-      const int n16 = (t.n + 15) & ~15;
-      int4 quad[2];   // gathered rows 4 lane .. + 3 and 4 (lane + 32) .. + 3
-      if (p.rows) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          int r[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int q = min(4 * (lane + 32 * h) + j, t.n - 1);
-            r[j] = min(max(p.rows[t.r0 + q], 0), p.A - 1);
-          }
-          quad[h] = make_int4(r[0], r[1], r[2], r[3]);
-        }
-      }
-      const int boxes = (n16 + kProdBox - 1) / kProdBox;
-      const uint32_t bytes =
-          p.w_bytes + kProdSfaBytes + (p.rows ? n16 : boxes * kProdBox) * kProdK;
-      const uint8_t* sfa = p.sfa + ((size_t)t.e * p.mt + t.m) * nk * kProdSfaBytes;
+    for (int i = first; ok && i < ntiles; i += step) {
+      const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
+      const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);
+      // the groups of 16 neurons of all experts' gate and up rows in one row
+      const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
       for (int kb = 0; kb < nk; ++kb, ++g) {
         const int s = rg.slot;
         if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
-        uint8_t* bdst = smem + L::b + s * kProdBBytes;
-        if (lane == 0) {
-          mbar_expect_tx(&full[s], bytes);
-          uint8_t* adst = smem + L::a + s * kProdABytes;
+        uint8_t* dst = smem + L::a + s * kProdABytes;
+        if (tc::elect()) {
+          if (rank == 0) mbar_expect_tx(&full[s], bytes);
           if (SILU)
-            tc::tma_load_5d(adst, &p.tm_w, kb * kProdK, 0, 0, t.m * 4, t.e, &full[s]);
+            tc::tma2_load_5d(dst, &p.tm_w, kb * kProdK, 0, 0, 0, grp, full0 + 8 * s);
           else
-            tma_load_3d(adst, &p.tm_w, kb * kProdK, t.m * kProdRows, t.e, &full[s]);
-          bulk_copy_g2s(smem + L::sfa + s * kProdSfaBytes, sfa + (size_t)kb * kProdSfaBytes,
-                        kProdSfaBytes, &full[s]);
+            tc::tma2_load_3d(dst, &p.tm_w, kb * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
         }
         __syncwarp();
-        if (p.rows) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int q = lane + 32 * h;
-            if (4 * q < n16) tc::tma_gather4(bdst + q * 4 * kProdK, &p.tm_a, kb * kProdK, quad[h], &full[s]);
-          }
-        } else if (lane < boxes) {
-          tma_load_2d(bdst + lane * kProdBox * kProdK, &p.tm_a, kb * kProdK, t.r0 + lane * kProdBox,
-                      &full[s]);
-        }
         rg.next();
       }
     }
-    // never leave with copies in flight
-    if (lane == 0)
+    // never leave with copies in flight (both CTAs' complete here)
+    if (rank == 0)
       for (int d = max(0, g - kProdStages); d < g; ++d)
-        mbar_wait(&full[d % kProdStages], (d / kProdStages) & 1, p.err);
+        prod_wait(&full[d % kProdStages], (d / kProdStages) & 1, p.err, dead);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      RingPos rg(kProdStages);
+    if (rank == 0) {
+      RingPos rg(kProdStages), rs(2);
       int lt = 0;
       bool ok = true;
-      for (int i = blockIdx.x; ok && i < ntiles; i += gridDim.x, ++lt) {
-        const ProductTile t = product_tile(i, p.mt, p.E, off, tiles);
-        const int n16 = (t.n + 15) & ~15;
-        const uint32_t idesc = tc::mx_idesc(p.a_format, n16);
+      for (int i = first; ok && i < ntiles; i += step, ++lt) {
+        const ProductTile t = product_tile(i, 0, pairs, p.E, off, tiles);
+        const int n = t.cols();
+        const uint32_t idesc = tc::mx_idesc(p.a_format, n);
         const int buf = lt & 1;
-        if (lt >= 2) ok = prod_wait(&d_empty[buf], ((lt >> 1) - 1) & 1, p.err, dead);
+        if (lt >= 2) ok = prod_wait_warp(&d_empty[buf], ((lt >> 1) - 1) & 1, p.err, dead);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kProdCols;
-        for (int kb = 0; kb < nk; ++kb) {
-          const int s = rg.slot;
-          ok = prod_wait(&full[s], rg.phase, p.err, dead) &&
-               prod_wait(&sfb_full[s], rg.phase, p.err, dead);
+        for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages) {
+          const int ns = min(kProdSfStages, nk - k0);
+          ok = prod_wait_warp(&sf_full[rs.slot], rs.phase, p.err, dead);
           if (!ok) break;
           tc::fence_after();
-          const uint32_t sfa = tmem + kProdSfCol + s * kProdSfCols, sfb = sfa + 4;
-          const uint32_t sb = smem_addr(smem + L::sfb + s * kProdSfbBytes);
-          tc::cp_scales(sfa, smem_addr(smem + L::sfa + s * kProdSfaBytes));
-          tc::cp_scales(sfb, sb);
-          if (n16 > 128) tc::cp_scales(sfb + 4, sb + 512);
-          const uint32_t aa = smem_addr(smem + L::a + s * kProdABytes);
-          const uint32_t ba = smem_addr(smem + L::b + s * kProdBBytes);
+          const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfStages * kProdSfCols;
+          const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
+          if (tc::elect()) {
+            for (int j = 0; j < ns; ++j) {
+              const uint32_t c = sfc + j * kProdSfCols;
+              const uint32_t sb = sfs + kProdSfStages * kProdSfaBytes + j * kProdSfbBytes;
+              tc::cp_scales(c, sfs + j * kProdSfaBytes);
+              tc::cp_scales(c + 4, sb);
+              if (n > 128) tc::cp_scales(c + 8, sb + 512);
+            }
+          }
+          __syncwarp();
+          for (int j = 0; j < ns; ++j) {
+            const int s = rg.slot;
+            ok = prod_wait_warp(&full[s], rg.phase, p.err, dead);
+            if (!ok) break;
+            tc::fence_after();
+            const uint64_t ad = tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdABytes));
+            const uint64_t bd = tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBBytes));
+            const uint32_t c = sfc + j * kProdSfCols;
+            if (tc::elect()) {
 #pragma unroll
-          for (int j = 0; j < kProdK / 32; ++j)
-            tc::mma_mx(d, tc::sdesc_sw128(aa + 32 * j), tc::sdesc_sw128(ba + 32 * j),
-                       idesc | tc::mx_scale_id(j), sfa, sfb, kb > 0 || j > 0 ? 1u : 0u);
-          tc::commit(&empty[s]);
-          rg.next();
+              for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
+                tc::mma_mx(d, ad + 2 * q, bd + 2 * q, idesc | tc::mx_scale_id(q), c, c + 4,
+                           k0 + j + q > 0 ? 1u : 0u);
+              tc::commit2(&empty[s]);
+            }
+            __syncwarp();
+            rg.next();
+          }
+          // the batch's places in shared and tensor memory are free when its
+          // MMAs are done
+          if (ok && tc::elect()) tc::commit2(&sf_empty[rs.slot]);
+          __syncwarp();
+          rs.next();
         }
-        if (ok) tc::commit(&d_full[buf]);
+        if (ok && tc::elect()) tc::commit2(&d_full[buf]);
+        __syncwarp();
       }
       // every MMA done before tensor memory is released
-      tc::commit(drain);
+      if (tc::elect()) tc::commit2(drain);
+      __syncwarp();
       mbar_wait(drain, 0, p.err);
     }
-  } else if (warp >= 8) {
-    // ------------------------------------------------------ the rows' scales
-    const int r = threadIdx.x - 256;   // this thread's rows of a tile: r and r + 128
-    const int ks = p.K / 32;
-    uint32_t* dst0 = reinterpret_cast<uint32_t*>(smem + L::sfb) + (r & 31) * 4 + (r >> 5);
-    RingPos rg(kProdStages);
-    int g = 0;
-    bool ok = true;
-    for (int i = blockIdx.x; ok && i < ntiles; i += gridDim.x) {
-      const ProductTile t = product_tile(i, p.mt, p.E, off, tiles);
-      const uint8_t* src[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int q = t.r0 + min(r + 128 * h, t.n - 1);
-        if (p.rows) q = min(max(p.rows[q], 0), p.A - 1);
-        src[h] = p.a_scales + (size_t)q * ks;
-      }
-      const bool two = t.n > 128;
-      uint4 w[2];
-      w[0] = load_row_scales(src[0], 0, ks, p.sf_vec);
-      w[1] = two ? load_row_scales(src[1], 0, ks, p.sf_vec) : w[0];
-      for (int k0 = 0; ok && k0 < nk; k0 += 4) {
-        const uint4 c[2] = {w[0], w[1]};
-        if (k0 + 4 < nk) {   // the next four stages' words while these are handed over
-          w[0] = load_row_scales(src[0], k0 + 4, ks, p.sf_vec);
-          if (two) w[1] = load_row_scales(src[1], k0 + 4, ks, p.sf_vec);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (k0 + j >= nk) break;
+  } else if (warp == 2) {
+    // ------------------------------------------------------- contiguous rows
+    if (!p.rows) {
+      RingPos rg(kProdStages);
+      const uint32_t full0 = tc::cluster_addr(full, 0);
+      int g = 0;
+      bool ok = true;
+      for (int i = first; ok && i < ntiles; i += step) {
+        const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
+        const int half = t.half(), r0 = t.r0 + rank * half;
+        for (int kb = 0; kb < nk; ++kb, ++g) {
           const int s = rg.slot;
           if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
-          uint32_t* dst = dst0 + s * (kProdSfbBytes / 4);
-          dst[0] = j == 0 ? c[0].x : j == 1 ? c[0].y : j == 2 ? c[0].z : c[0].w;
-          if (two) dst[128] = j == 0 ? c[1].x : j == 1 ? c[1].y : j == 2 ? c[1].z : c[1].w;
-          tc::fence_proxy_async();
+          uint8_t* dst = smem + L::b + s * kProdBBytes;
+          if (tc::elect()) {
+            int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
+#pragma unroll
+            for (int b = 2; b >= 0; --b)
+              if (half & (16 << b)) {
+                tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[b], kb * kProdK, r0 + r, full0 + 8 * s);
+                r += 16 << b;
+              }
+          }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sfb_full[s]);
-          ++g;
           rg.next();
         }
       }
     }
+  } else if (warp >= 8) {
+    // ---------------------------------------------- scales and gathered rows
+    const int r = threadIdx.x - 256;
+    const int ks = p.K / 32;
+    const uint32_t sf_full0 = tc::cluster_addr(sf_full, 0);
+    const uint32_t full0 = tc::cluster_addr(full, 0);
+    const bool gather = p.rows != nullptr;
+    // this thread's 16 bytes of the gathered rows (r / 8 + 16 i): piece r % 8,
+    // where the 128-byte swizzle puts it
+    const int piece = (r & 7) * 16;
+    const uint32_t copy_dst =
+        smem_addr(smem + L::b) + (r >> 3) * kProdK + (((r & 7) ^ ((r >> 3) & 7)) << 4);
+    RingPos rg(kProdStages), rs(2);
+    int g = 0, gb = 0;
+    bool ok = true;
+    ProductRows cur, nxt;
+    if (first < ntiles) {
+      cur.load(p, product_tile(first, rank, pairs, p.E, off, tiles), rank, r);
+      cur.settle(p);
+    }
+    // Gathered stages before `upto` go to the MMAs once their copies have
+    // landed: `handed` of the g issued have been so far.
+    int handed = 0;
+    RingPos ra(kProdStages);
+    auto hand_over = [&](int upto) {
+      switch (g - upto) {
+        case 0: tc::copy_wait<0>(); break;
+        case 1: tc::copy_wait<1>(); break;
+        case 2: tc::copy_wait<2>(); break;
+        case 3: tc::copy_wait<3>(); break;
+        default: tc::copy_wait<kProdGatherLag>();
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      for (; handed < upto; ++handed, ra.next())
+        if (lane == 0) tc::arrive_at(full0 + 8 * ra.slot);
+    };
+    int end1 = 0, end2 = 0;    // stages issued with the last batch, and with the one before
+    uint4 wsf = make_uint4(0, 0, 0, 0), rsf[2] = {wsf, wsf};
+    auto load_batch = [&](const ProductRows& pr, int k0) {
+      if (r < 32 * min(kProdSfStages, nk - k0))
+        wsf = *reinterpret_cast<const uint4*>(
+            p.sfa + (((size_t)pr.t.e * 2 * pairs + pr.t.m) * nk + k0) * kProdSfaBytes + r * 16);
+      rsf[0] = load_row_scales(p.a_scales + (size_t)pr.scale_row[0] * ks, k0, ks, p.sf_vec);
+      if (pr.t.n > 128)
+        rsf[1] = load_row_scales(p.a_scales + (size_t)pr.scale_row[1] * ks, k0, ks, p.sf_vec);
+    };
+    if (first < ntiles) load_batch(cur, 0);
+    for (int i = first; ok && i < ntiles; i += step) {
+      const bool more = i + step < ntiles;
+      if (more) nxt.load(p, product_tile(i + step, rank, pairs, p.E, off, tiles), rank, r);
+      const int half = cur.t.half();
+      for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages, ++gb) {
+        // the slot below frees when the MMAs of the batch before last are done:
+        // they need all of its stages, which a short batch since may hold back
+        if (gather && handed < end2) hand_over(end2);
+        if (gb >= 2 && !prod_wait_warp(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sf = smem + L::sf + rs.slot * kProdSfBytes;
+        *reinterpret_cast<uint4*>(sf + r * 16) = wsf;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(sf + kProdSfStages * kProdSfaBytes) +
+                        (r & 31) * 4 + (r >> 5);
+        dst[0] = rsf[0].x, dst[256] = rsf[0].y, dst[512] = rsf[0].z, dst[768] = rsf[0].w;
+        if (cur.t.n > 128)
+          dst[128] = rsf[1].x, dst[384] = rsf[1].y, dst[640] = rsf[1].z, dst[896] = rsf[1].w;
+        tc::fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) tc::arrive_at(sf_full0 + 8 * rs.slot);
+        rs.next();
+        // the next batch's loads run while this one is used
+        if (k0 + kProdSfStages < nk)
+          load_batch(cur, k0 + kProdSfStages);
+        else if (more) {
+          nxt.settle(p);
+          load_batch(nxt, 0);
+        }
+        if (!gather) continue;
+        const int ns = min(kProdSfStages, nk - k0);
+        for (int j = 0; j < ns; ++j) {
+          const int s = rg.slot, at = (k0 + j) * kProdK + piece;
+          if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = at < p.K ? 16u : 0u;
+          const uint8_t* src = p.a + (bytes ? at : 0);
+#pragma unroll
+          for (int c = 0; c < kProdCols / 32; ++c)
+            if (16 * c < half)
+              tc::copy16(copy_dst + s * kProdBBytes + c * 16 * kProdK,
+                         src + (size_t)cur.copy_row[c] * p.K, bytes);
+          tc::copy_commit();
+          rg.next();
+          ++g;
+          if (g - kProdGatherLag > handed) hand_over(g - kProdGatherLag);
+        }
+        end2 = end1, end1 = g;
+      }
+      cur = nxt;
+    }
+    if (gather) {
+      if (ok) hand_over(g);
+      tc::copy_wait<0>();
+    }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3;
+    const int q = warp & 3, et = threadIdx.x - 128;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
     uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::amax);
+    float* inv = reinterpret_cast<float*>(smem + L::inv) + q * 32;
     int lt = 0, chunk = 0;
-    for (int i = blockIdx.x; i < ntiles; i += gridDim.x, ++lt) {
-      const ProductTile t = product_tile(i, p.mt, p.E, off, tiles);
+    for (int i = first; i < ntiles; i += step, ++lt) {
+      const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
       const int buf = lt & 1;
       bool ok = prod_wait_warp(&d_full[buf], (lt >> 1) & 1, p.err, dead);
-      // the two warps of a block go on or leave together: the named barrier
-      // below never waits for a warp that gave up
-      if (SILU) ok = named_all(1 + (q >> 1), 64, ok);
+      // the four warps go on or leave together: no named barrier below waits
+      // for a warp that gave up
+      ok = named_all(1, 128, ok);
       if (!ok) break;
       tc::fence_after();
       for (int c0 = 0; c0 < t.n; c0 += 32, ++chunk) {
-        uint32_t v[32];
-        tc::ld32(lanes + buf * kProdCols + c0, v);
+        uint8_t* stage = smem + L::out + (chunk & 1) * kProdStageOut;
+        uint32_t lo[16], hi[16];
+        tc::ld_16x32(lanes + buf * kProdCols + c0, lo);
+        tc::ld_16x32(lanes + (16u << 16) + buf * kProdCols + c0, hi);
         tc::wait_ld();
         if constexpr (!SILU) {
-          // a lane holds one weight row of 32 columns (rows of the group):
-          // neighbouring lanes swap, so that each stores two weight rows' bf16
-          // values of every other column
-          const int n = t.m * kProdRows + 32 * q + (lane & ~1);
-          const int odd = lane & 1;
-          uint16_t* y = p.y + (size_t)(t.r0 + c0) * p.N + n;
+          // 32 rows of the group x this warp's 32 weight rows, transposed on
+          // the way to shared memory: 16-byte piece 4q + m of row r holds
+          // weight rows 8m.. and sits at piece ^ (r & 7)
+          const int m = lane >> 3, r = lane & 7;
+          const uint32_t dst = smem_addr(stage) + r * 256 + (((4 * q + m) ^ r) << 4);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const uint32_t give = odd ? v[j] : v[j + 1], keep = odd ? v[j + 1] : v[j];
-            const uint32_t got = __shfl_xor_sync(kFull, give, 1);
-            const float lo = __uint_as_float(odd ? got : keep);
-            const float hi = __uint_as_float(odd ? keep : got);
-            if (c0 + j + odd < t.n && n < p.N)
-              *reinterpret_cast<uint32_t*>(y + (size_t)(j + odd) * p.N) = RowVec<8>::pack(lo, hi);
+          for (int b = 0; b < 4; ++b) {
+            auto pack = [](uint32_t x, uint32_t y) {
+              return RowVec<8>::pack(__uint_as_float(x), __uint_as_float(y));
+            };
+            tc::stm4_trans(dst + b * 8 * 256, pack(lo[4 * b], lo[4 * b + 1]),
+                           pack(lo[4 * b + 2], lo[4 * b + 3]), pack(hi[4 * b], hi[4 * b + 1]),
+                           pack(hi[4 * b + 2], hi[4 * b + 3]));
+          }
+          named_sync(1, 128);
+          const int pc = et & 15, n = t.m * kProdRows + 8 * pc;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = (et >> 4) + 8 * k;
+            if (c0 + row < t.n && n < p.N)
+              *reinterpret_cast<uint4*>(p.y + (size_t)(t.r0 + c0 + row) * p.N + n) =
+                  *reinterpret_cast<const uint4*>(stage + row * 256 + ((pc ^ (row & 7)) << 4));
           }
         } else {
-          // lanes 0-15 hold gate rows, lanes 16-31 the same neurons' up rows:
-          // the halves swap, so that the low half finishes even columns and
-          // the high half odd ones
-          const int up = lane >> 4, I = p.N / 2;
-          const int n = t.m * 64 + 16 * q + (lane & 15);
+          // this thread's gates (lo) and ups (hi) of neurons 2 (lane / 4) + {0, 1}
+          // of the warp's 16, columns 8 b + 2 (lane % 4) + {0, 1}
           float h[16];
-          uint32_t mine = 0u;   // lane's column's largest magnitude among these 16 neurons
+          uint32_t mx[8];   // magnitudes of columns 2 b + j, over those two neurons
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t give = up ? v[2 * j] : v[2 * j + 1], keep = up ? v[2 * j + 1] : v[2 * j];
-            const uint32_t got = __shfl_xor_sync(kFull, give, 16);
-            const float gate = __uint_as_float(up ? got : keep);
-            const float u = __uint_as_float(up ? keep : got);
-            h[j] = gate / (1.0f + expf(-gate)) * u;
-            uint32_t a = __float_as_uint(h[j]) & 0x7fffffffu;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(kFull, a, o));
-            if ((lane & 15) == j) mine = a;
+          for (int x = 0; x < 16; ++x) {
+            const float gate = __uint_as_float(lo[x]), up = __uint_as_float(hi[x]);
+            h[x] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
           }
-          // lane l now holds column 2 (l & 15) + (l >> 4); the block's other 16
-          // neurons are in the neighbouring warp
-          const int col = 2 * (lane & 15) + up;
-          uint32_t* mx = amax + (chunk & 1) * 128;
-          mx[q * 32 + lane] = mine;
-          named_sync(1 + (q >> 1), 64);
-          mine = max(mine, mx[(q ^ 1) * 32 + lane]);
-          const uint32_t sc = mx_scale_code(mine);
-          if ((q & 1) == 0 && c0 + col < t.n && n < I)
-            p.scales[(size_t)(t.r0 + c0 + col) * (I / 32) + t.m * 2 + (q >> 1)] = (uint8_t)sc;
-          const float inv = mx_inverse(sc);
-          uint8_t* out = p.codes + (size_t)(t.r0 + c0) * I + n;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const float x = h[j] * __shfl_sync(kFull, inv, j + (lane & 16));
-            if (c0 + 2 * j + up < t.n && n < I)
-              out[(size_t)(2 * j + up) * I] = (uint8_t)e4m3x2(x, x);
+          for (int b = 0; b < 8; ++b) {
+            const int x = (b >> 1) * 4 + (b & 1);
+            mx[b] = max(__float_as_uint(h[x]) & 0x7fffffffu, __float_as_uint(h[x + 2]) & 0x7fffffffu);
           }
+          // over the warp's 16 neurons (lane bits 4, 3, 2), each lane keeping
+          // half of its columns a step and one in the end
+#pragma unroll
+          for (int w = 4; w > 0; w >>= 1) {
+            const bool high = (lane & (4 * w)) != 0;
+#pragma unroll
+            for (int b = 0; b < w; ++b) {
+              const uint32_t give = high ? mx[b] : mx[b + w], keep = high ? mx[b + w] : mx[b];
+              mx[b] = max(keep, __shfl_xor_sync(kFull, give, 4 * w));
+            }
+          }
+          const int v = lane >> 2, col = 8 * (v >> 1) + 2 * (lane & 3) + (v & 1);
+          // the block's other 16 neurons are in the neighbouring warp
+          uint32_t* am = amax + (chunk & 1) * 128;
+          am[q * 32 + col] = mx[0];
+          named_sync(2 + (q >> 1), 64);
+          const uint32_t sc = mx_scale_code(max(mx[0], am[(q ^ 1) * 32 + col]));
+          const int I = p.N / 2, nb = t.m * 2 + (q >> 1);   // block of 32 neurons
+          if ((q & 1) == 0 && c0 + col < t.n && nb * 32 < I)
+            p.scales[(size_t)(t.r0 + c0 + col) * (I / 32) + nb] = (uint8_t)sc;
+          inv[col] = mx_inverse(sc);
+          __syncwarp();
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const int cb = 8 * b + 2 * (lane & 3);
+            const float2 f = *reinterpret_cast<const float2*>(inv + cb);
+            uint16_t* dst = reinterpret_cast<uint16_t*>(stage + cb * kProdCodePitch + 16 * q) + v;
+            dst[0] = (uint16_t)e4m3x2(h[4 * b] * f.x, h[4 * b + 2] * f.x);
+            dst[kProdCodePitch / 2] = (uint16_t)e4m3x2(h[4 * b + 1] * f.y, h[4 * b + 3] * f.y);
+          }
+          named_sync(1, 128);
+          const int row = et >> 2, n = t.m * 64 + 16 * (et & 3);
+          if (c0 + row < t.n && n < I)
+            *reinterpret_cast<uint4*>(p.codes + (size_t)(t.r0 + c0 + row) * I + n) =
+                *reinterpret_cast<const uint4*>(stage + row * kProdCodePitch + 16 * (et & 3));
         }
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[buf]);
+      if (lane == 0) tc::arrive_at(d_empty0 + 8 * buf);
     }
   }
+  __syncwarp();
   tc::fence_before();
   __syncthreads();
+  cluster_sync();   // no CTA leaves while the other may still reach into it
   tc::fence_after();
-  if (warp == 1) tc::tmem_dealloc(tmem, kProdTmemCols);
+  if (warp == 1) tc::tmem_dealloc2(*tmem_slot, kProdTmemCols);
 }
 
 }  // namespace moe

@@ -94,8 +94,11 @@ bool is_fp4(const moe_product_config_t& c) { return (c.flags & MOE_FLAG_MXFP4) !
 bool is_silu(const moe_product_config_t& c) { return (c.flags & MOE_PRODUCT_SILU_MUL) != 0; }
 
 // The weights as [E][N][K] in boxes of 128 rows, or with SILU_MUL as
-// [E][I/16][gate, up][16][K] in boxes of four groups of 16 gate and 16 up
-// rows. MXFP4 codes are spread to a byte each on the way (16 codes and 8
+// [groups of 16 rows][gate, up][odd][8][K] in boxes of four groups' gate rows
+// and the up rows I further on, even neurons before odd ones. There the groups
+// of all experts lie in one row, and the last I/16 (up rows whose own up rows
+// would lie past the end) are left out: a tile that runs past its expert's
+// last neuron reads other rows or zeros, and its surplus is not stored. MXFP4 codes are spread to a byte each on the way (16 codes and 8
 // bytes of padding in 16 bytes of shared memory).
 bool encode_weights(moe_product* m, const uint8_t* w) {
   const moe_product_config_t& c = m->cfg;
@@ -103,10 +106,10 @@ bool encode_weights(moe_product* m, const uint8_t* w) {
       is_fp4(c) ? CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B : CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const cuuint64_t row = is_fp4(c) ? c.K / 2 : c.K, N = c.N, K = c.K, E = c.E;
   if (is_silu(c)) {
-    const cuuint64_t I = N / 2;
-    const cuuint64_t dims[5] = {K, 16, 2, I / 16, E};
-    const cuuint64_t strides[4] = {row, I * row, 16 * row, N * row};
-    const cuuint32_t box[5] = {moe::kProdK, 16, 2, 4, 1};
+    const cuuint64_t I = N / 2, groups = E * (N / 16) - I / 16;
+    const cuuint64_t dims[5] = {K, 8, 2, 2, groups};
+    const cuuint64_t strides[4] = {2 * row, row, I * row, 16 * row};
+    const cuuint32_t box[5] = {moe::kProdK, 8, 2, 2, 4};
     return encode(&m->tm_w, type, 5, w, dims, strides, box);
   }
   const cuuint64_t dims[3] = {K, N, E};
@@ -205,7 +208,8 @@ moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* 
   m->cfg = c;
   m->mt = is_silu(c) ? (c.N / 2 + 63) / 64 : (c.N + moe::kProdRows - 1) / moe::kProdRows;
   const int nk = (c.K + moe::kProdK - 1) / moe::kProdK;
-  const int64_t blocks = (int64_t)c.E * m->mt * nk;
+  const int mt2 = (m->mt + 1) / 2 * 2;   // a pair of CTAs takes two tiles
+  const int64_t blocks = (int64_t)c.E * mt2 * nk;
   int dev = 0;
   const bool ok =
       blocks <= 0x7fffffff && cudaGetDevice(&dev) == cudaSuccess &&
@@ -222,7 +226,7 @@ moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* 
                            (int)kProductSmem) == cudaSuccess;
   if (ok) {
     moe::moe_product_lay_scales<<<(unsigned)blocks, 128, 0, static_cast<cudaStream_t>(stream)>>>(
-        w_scales, m->sfa, c.N, c.K, m->mt, is_silu(c));
+        w_scales, m->sfa, c.N, c.K, mt2, is_silu(c));
   }
   // the scales are laid out once this returns: calls may come on any stream
   if (!ok || cudaGetLastError() != cudaSuccess ||
@@ -254,10 +258,16 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
     return MOE_ERR_MISALIGNED;
   moe::ProductParams p;
   p.tm_w = m->tm_w;
-  const cuuint64_t dims[2] = {(cuuint64_t)c.K, (cuuint64_t)A};
-  const cuuint64_t strides[1] = {(cuuint64_t)c.K};
-  const cuuint32_t box[2] = {moe::kProdK, rows ? 1u : (cuuint32_t)moe::kProdBox};
-  if (!encode(&p.tm_a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, dims, strides, box)) return MOE_ERR_CUDA;
+  if (!rows) {
+    const cuuint64_t dims[2] = {(cuuint64_t)c.K, (cuuint64_t)A};
+    const cuuint64_t strides[1] = {(cuuint64_t)c.K};
+    for (int b = 0; b < 3; ++b) {
+      const cuuint32_t box[2] = {moe::kProdK, 16u << b};
+      if (!encode(&p.tm_a[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a, dims, strides, box))
+        return MOE_ERR_CUDA;
+    }
+  }
+  p.a = a;
   p.sfa = m->sfa;
   p.a_scales = a_scales;
   p.offsets = offsets;
@@ -276,11 +286,11 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
   p.sf_vec = ks % 16 == 0 && aligned(a_scales, 16) ? 16 : ks % 4 == 0 && aligned(a_scales, 4) ? 4 : 1;
   p.w_bytes = is_fp4(c) ? moe::kProdABytes / 2 : moe::kProdABytes;
   p.a_format = is_fp4(c) ? 5 : 0;
-  // at most this many tiles can exist
-  const int64_t most = ((int64_t)std::min(c.E, R) + R / moe::kProdCols) * m->mt;
-  const unsigned grid = (unsigned)std::min<int64_t>(m->num_sms, most);
-  return silu ? launch(moe::moe_product_tiles<true>, grid, moe::kProdThreads, kProductSmem, stream, 1, p)
-              : launch(moe::moe_product_tiles<false>, grid, moe::kProdThreads, kProductSmem, stream, 1, p);
+  // one pair of CTAs a pair of SMs, and no more than there can be tiles
+  const int64_t most = ((int64_t)std::min(c.E, R) + R / moe::kProdCols) * ((m->mt + 1) / 2);
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(std::max(1, m->num_sms / 2), most);
+  return launch(silu ? moe::moe_product_tiles<true> : moe::moe_product_tiles<false>, grid,
+                moe::kProdThreads, kProductSmem, stream, 2, p);
 }
 
 moe_status_t moe_product_get_error(moe_product_t m, void* stream, uint32_t* device_flags) {
