@@ -17,6 +17,7 @@
 //   warp 0       weights by TMA
 //   warp 1       (first CTA) scales to tensor memory (tcgen05.cp) and the MMAs
 //   warp 2       the group's rows by TMA, where they are contiguous
+//   warp 3       where they are gathered, word to the MMAs that they landed
 //   warps 4-7    epilogue, one per lane quarter of tensor memory
 //   warps 8-11   scales, four stages at a time, into shared memory in the order
 //                tcgen05.cp takes; and the group's rows where they are gathered
@@ -49,14 +50,12 @@ constexpr int kProdBBytes = kProdCols / 2 * kProdK;
 constexpr int kProdSfaBytes = 512;    // a stage's weight scales of one CTA
 constexpr int kProdSfbBytes = 1024;   // a stage's row scales (up to 256 rows)
 constexpr int kProdSfBytes = kProdSfStages * (kProdSfaBytes + kProdSfbBytes);
-constexpr int kProdGatherLag = 4;     // gathered stages in flight behind the newest
 // tensor-memory columns
 constexpr uint32_t kProdTmemCols = 512;
 constexpr uint32_t kProdSfCol = 2 * kProdCols;
 constexpr uint32_t kProdSfCols = 12;   // a stage's: 4 of the weights, 8 of the rows
 static_assert(2 * kProdCols + 2 * kProdSfStages * kProdSfCols <= kProdTmemCols, "tensor memory");
 static_assert(kProdCols % 32 == 0 && kProdCols <= 256, "token tile");
-static_assert(kProdGatherLag < kProdStages, "a stage is handed over before its slot is due again");
 // epilogue staging: a chunk of 32 columns as rows of 128 bf16 (16-byte pieces
 // swizzled by the row), or of 64 codes padded to 80 bytes, two chunks in turn
 constexpr int kProdStageOut = 32 * 256;
@@ -90,8 +89,9 @@ struct ProductSmem {
   static constexpr int inv = amax + 2 * 4 * 32 * 4;                // [4][32] floats
   static constexpr int off = inv + 4 * 32 * 4;                     // [E + 1] group starts
   static constexpr int tiles = off + (kProdMaxE + 4) * 4;          // [E + 1] token tiles before
-  static constexpr int bars = tiles + (kProdMaxE + 4) * 4;
-  static constexpr int total = bars + (2 * kProdStages + 9) * 8 + 16;
+  static constexpr int piece = tiles + (kProdMaxE + 4) * 4;        // [E] rows of a group's pieces
+  static constexpr int bars = piece + kProdMaxE * 4;
+  static constexpr int total = bars + (3 * kProdStages + 9) * 8 + 16;
 };
 
 namespace tc {
@@ -159,16 +159,19 @@ __device__ __forceinline__ void tma2_load_5d(void* dst, const void* tmap, int c0
       : "memory");
 }
 
-// 16 bytes global -> shared in the issuing thread's copy group; `bytes` 0
-// fills with zeros and reads nothing.
+// 16 bytes global -> shared, asynchronously; `bytes` 0 fills with zeros and
+// reads nothing.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+// This thread's arrival on an mbarrier, once its copies so far have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void copy_wait_all() {
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // 512 bytes of scales (32 lanes of 16) at the same place of both CTAs' shared
@@ -336,27 +339,45 @@ struct ProductTile {
   __device__ __forceinline__ int half() const { return cols() >> 1; }
 };
 
-// Tile `i` of the walk: the pairs of weight tiles of one token tile in turn,
-// so that pairs of CTAs working side by side share its rows in L2. A group of
-// c rows is cut into the fewest pieces, of equal size but for rounding to 32.
-__device__ __forceinline__ ProductTile product_tile(int i, int rank, int pairs, int E,
-                                                    const int* off, const int* tiles) {
-  ProductTile t;
-  const int q = i / pairs;
-  t.m = 2 * (i - q * pairs) + rank;
-  int lo = 0, hi = E;   // tiles[lo] <= q < tiles[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tiles[mid] <= q) lo = mid; else hi = mid;
+// A CTA pair's walk over the tiles first, first + step, ...: the pairs of
+// weight tiles of one token tile in turn, so that pairs of CTAs working side
+// by side share its rows in L2. A group of c rows is cut into the fewest
+// pieces, of equal size but for rounding to 32. Every lane of the warp takes
+// part: the next token tile's expert is found 32 experts at a time (a search
+// and divisions cost each role a thousand cycles a tile).
+struct ProductWalk {
+  const int *off, *tiles, *piece;   // [E + 1], [E + 1], [E]
+  int rank, pairs, E, ntok;
+  int q, m, dq, dm;                 // token tile and pair of weight tiles, and a step's
+  int e;                            // expert of q, once found
+  __device__ __forceinline__ ProductWalk(const int* off_, const int* tiles_, const int* piece_,
+                                         int rank_, int pairs_, int E_, int first, int step)
+      : off(off_), tiles(tiles_), piece(piece_), rank(rank_), pairs(pairs_), E(E_),
+        ntok(uniform(tiles_[E_])), q(first / pairs_), m(first % pairs_), dq(step / pairs_),
+        dm(step % pairs_), e(0) {}
+  __device__ __forceinline__ bool valid() const { return q < ntok; }
+  __device__ __forceinline__ void next() {
+    q += dq;
+    m += dm;
+    if (m >= pairs) m -= pairs, ++q;
   }
-  const int pieces = tiles[lo + 1] - tiles[lo], j = q - tiles[lo];
-  const int c = off[lo + 1] - off[lo];
-  const int b = ((c + pieces - 1) / pieces + 31) & ~31;
-  t.e = uniform(lo);
-  t.r0 = uniform(off[lo] + j * b);
-  t.n = uniform(min(b, c - j * b));
-  return t;
-}
+  __device__ __forceinline__ ProductTile tile() {
+    const int lane = threadIdx.x & 31;
+    for (;;) {   // tiles[e] <= q < tiles[e + 1]; the last entry is above q
+      const int i = e + 1 + lane;
+      const unsigned past = __ballot_sync(kFull, i <= E && tiles[i] <= q);
+      e += __popc(past);
+      if (past != kFull) break;
+    }
+    ProductTile t;
+    const int b = piece[e], r0 = off[e] + (q - tiles[e]) * b;
+    t.e = uniform(e);
+    t.m = 2 * m + rank;
+    t.r0 = uniform(r0);
+    t.n = uniform(min(b, off[e + 1] - r0));
+    return t;
+  }
+};
 
 // A batch's scale bytes (16, four stages) of one row from stage kb on; bytes
 // past the row's end read as 127.
@@ -421,9 +442,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   using L = ProductSmem;
   int* off = reinterpret_cast<int*>(smem + L::off);
   int* tiles = reinterpret_cast<int*>(smem + L::tiles);
+  int* piece = reinterpret_cast<int*>(smem + L::piece);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
   uint64_t* empty = full + kProdStages;
-  uint64_t* sf_full = empty + kProdStages;                        // used in the first CTA
+  uint64_t* copied = empty + kProdStages;                         // gathered rows
+  uint64_t* sf_full = copied + kProdStages;                       // used in the first CTA
   uint64_t* sf_empty = sf_full + 2;
   uint64_t* d_full = sf_empty + 2;
   uint64_t* d_empty = d_full + 2;                                 // used in the first CTA
@@ -440,10 +463,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   if (warp == 0 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
     for (int i = 0; i < kProdStages; ++i) {
-      // the announcement of both CTAs' TMA bytes; gathered rows add the eight
-      // warps that copy them
-      mbar_init(&full[i], p.rows ? 9 : 1);
+      // the announcement of both CTAs' TMA bytes, and with gathered rows both
+      // CTAs' word that their copies have landed
+      mbar_init(&full[i], p.rows ? 3 : 1);
       mbar_init(&empty[i], 1);
+      mbar_init(&copied[i], 128);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sf_full[i], 8);    // both CTAs' scale warps
@@ -467,6 +491,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int hi = min(max(p.offsets[e + 1], 0), p.R);
         nt = hi > lo ? (hi - lo + kProdCols - 1) / kProdCols : 0;
         off[e] = lo;
+        piece[e] = nt ? ((hi - lo + nt - 1) / nt + 31) & ~31 : 0;
       }
       int incl = nt;
 #pragma unroll
@@ -488,7 +513,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   tc::fence_after();
   // all of tensor memory is this CTA's, so its columns start at 0
   constexpr uint32_t tmem = 0;
-  const int ntiles = uniform(tiles[p.E] * pairs);
+  ProductWalk walk(off, tiles, piece, rank, pairs, p.E, first, step);
 
   if (warp == 0) {
     // --------------------------------------------------------------- weights
@@ -496,8 +521,8 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     const uint32_t full0 = tc::cluster_addr(full, 0);
     int g = 0;
     bool ok = true;
-    for (int i = first; ok && i < ntiles; i += step) {
-      const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
+    for (; ok && walk.valid(); walk.next()) {
+      const ProductTile t = walk.tile();
       const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);
       // the groups of 16 neurons of all experts' gate and up rows in one row
       const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
@@ -528,9 +553,12 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     if (rank == 0) {
       RingPos rg(kProdStages), rs(2);
       int lt = 0;
-      bool ok = true;
-      for (int i = first; ok && i < ntiles; i += step, ++lt) {
-        const ProductTile t = product_tile(i, 0, pairs, p.E, off, tiles);
+      bool ok = true, ready = false;
+      ProductTile t, after;
+      bool more = walk.valid();
+      if (more) after = walk.tile();
+      for (; more; ++lt) {
+        t = after;
         const int n = t.cols();
         const uint32_t idesc = tc::mx_idesc(p.a_format, n);
         const int buf = lt & 1;
@@ -542,7 +570,6 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           const int ns = min(kProdSfStages, nk - k0);
           ok = prod_wait_warp(&sf_full[rs.slot], rs.phase, p.err, dead);
           if (!ok) break;
-          tc::fence_after();
           const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfStages * kProdSfCols;
           const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
           if (tc::elect()) {
@@ -557,9 +584,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           __syncwarp();
           for (int j = 0; j < ns; ++j) {
             const int s = rg.slot;
-            ok = prod_wait_warp(&full[s], rg.phase, p.err, dead);
+            ok = ready || prod_wait_warp(&full[s], rg.phase, p.err, dead);
             if (!ok) break;
-            tc::fence_after();
+            rg.next();
+            // the next stage's barrier is looked at while this one's MMAs issue
+            const bool next = mbar_test(&full[rg.slot], rg.phase);
             const uint64_t ad = tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdABytes));
             const uint64_t bd = tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBBytes));
             const uint32_t c = sfc + j * kProdSfCols;
@@ -570,16 +599,21 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
                            k0 + j + q > 0 ? 1u : 0u);
               tc::commit2(&empty[s]);
             }
-            __syncwarp();
-            rg.next();
+            ready = __all_sync(kFull, next);
           }
           // the batch's places in shared and tensor memory are free when its
           // MMAs are done
           if (ok && tc::elect()) tc::commit2(&sf_empty[rs.slot]);
           __syncwarp();
           rs.next();
+          if (k0 == 0) {   // find the next tile while MMAs are under way
+            walk.next();
+            more = walk.valid();
+            if (more) after = walk.tile();
+          }
         }
-        if (ok && tc::elect()) tc::commit2(&d_full[buf]);
+        if (!ok) break;
+        if (tc::elect()) tc::commit2(&d_full[buf]);
         __syncwarp();
       }
       // every MMA done before tensor memory is released
@@ -594,8 +628,8 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       const uint32_t full0 = tc::cluster_addr(full, 0);
       int g = 0;
       bool ok = true;
-      for (int i = first; ok && i < ntiles; i += step) {
-        const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
+      for (; ok && walk.valid(); walk.next()) {
+        const ProductTile t = walk.tile();
         const int half = t.half(), r0 = t.r0 + rank * half;
         for (int kb = 0; kb < nk; ++kb, ++g) {
           const int s = rg.slot;
@@ -618,44 +652,45 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         }
       }
     }
+  } else if (warp == 3) {
+    // ------------------------------------ word of gathered rows to the MMAs
+    // One warp waits for a stage's copies, makes them visible to the tensor
+    // cores and tells the first CTA, so that the copying warps never wait for
+    // what they issued.
+    if (p.rows) {
+      RingPos rg(kProdStages);
+      const uint32_t full0 = tc::cluster_addr(full, 0);
+      bool ok = true;
+      for (; ok && walk.valid(); walk.next())
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!prod_wait_warp(&copied[rg.slot], rg.phase, p.err, dead)) {
+            ok = false;
+            break;
+          }
+          tc::fence_proxy_async();
+          if (lane == 0) tc::arrive_at(full0 + 8 * rg.slot);
+          rg.next();
+        }
+    }
   } else if (warp >= 8) {
     // ---------------------------------------------- scales and gathered rows
     const int r = threadIdx.x - 256;
     const int ks = p.K / 32;
     const uint32_t sf_full0 = tc::cluster_addr(sf_full, 0);
-    const uint32_t full0 = tc::cluster_addr(full, 0);
     const bool gather = p.rows != nullptr;
     // this thread's 16 bytes of the gathered rows (r / 8 + 16 i): piece r % 8,
     // where the 128-byte swizzle puts it
-    const int piece = (r & 7) * 16;
+    const int within = (r & 7) * 16;
     const uint32_t copy_dst =
         smem_addr(smem + L::b) + (r >> 3) * kProdK + (((r & 7) ^ ((r >> 3) & 7)) << 4);
     RingPos rg(kProdStages), rs(2);
     int g = 0, gb = 0;
-    bool ok = true;
     ProductRows cur, nxt;
-    if (first < ntiles) {
-      cur.load(p, product_tile(first, rank, pairs, p.E, off, tiles), rank, r);
+    bool ok = true, more = walk.valid();
+    if (more) {
+      cur.load(p, walk.tile(), rank, r);
       cur.settle(p);
     }
-    // Gathered stages before `upto` go to the MMAs once their copies have
-    // landed: `handed` of the g issued have been so far.
-    int handed = 0;
-    RingPos ra(kProdStages);
-    auto hand_over = [&](int upto) {
-      switch (g - upto) {
-        case 0: tc::copy_wait<0>(); break;
-        case 1: tc::copy_wait<1>(); break;
-        case 2: tc::copy_wait<2>(); break;
-        case 3: tc::copy_wait<3>(); break;
-        default: tc::copy_wait<kProdGatherLag>();
-      }
-      tc::fence_proxy_async();
-      __syncwarp();
-      for (; handed < upto; ++handed, ra.next())
-        if (lane == 0) tc::arrive_at(full0 + 8 * ra.slot);
-    };
-    int end1 = 0, end2 = 0;    // stages issued with the last batch, and with the one before
     uint4 wsf = make_uint4(0, 0, 0, 0), rsf[2] = {wsf, wsf};
     auto load_batch = [&](const ProductRows& pr, int k0) {
       if (r < 32 * min(kProdSfStages, nk - k0))
@@ -665,15 +700,13 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       if (pr.t.n > 128)
         rsf[1] = load_row_scales(p.a_scales + (size_t)pr.scale_row[1] * ks, k0, ks, p.sf_vec);
     };
-    if (first < ntiles) load_batch(cur, 0);
-    for (int i = first; ok && i < ntiles; i += step) {
-      const bool more = i + step < ntiles;
-      if (more) nxt.load(p, product_tile(i + step, rank, pairs, p.E, off, tiles), rank, r);
+    if (more) load_batch(cur, 0);
+    while (ok && more) {
+      walk.next();
+      more = walk.valid();
+      if (more) nxt.load(p, walk.tile(), rank, r);
       const int half = cur.t.half();
       for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages, ++gb) {
-        // the slot below frees when the MMAs of the batch before last are done:
-        // they need all of its stages, which a short batch since may hold back
-        if (gather && handed < end2) hand_over(end2);
         if (gb >= 2 && !prod_wait_warp(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
@@ -699,7 +732,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (!gather) continue;
         const int ns = min(kProdSfStages, nk - k0);
         for (int j = 0; j < ns; ++j) {
-          const int s = rg.slot, at = (k0 + j) * kProdK + piece;
+          const int s = rg.slot, at = (k0 + j) * kProdK + within;
           if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
@@ -711,19 +744,14 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
             if (16 * c < half)
               tc::copy16(copy_dst + s * kProdBBytes + c * 16 * kProdK,
                          src + (size_t)cur.copy_row[c] * p.K, bytes);
-          tc::copy_commit();
+          tc::copy_arrive(&copied[s]);
           rg.next();
           ++g;
-          if (g - kProdGatherLag > handed) hand_over(g - kProdGatherLag);
         }
-        end2 = end1, end1 = g;
       }
       cur = nxt;
     }
-    if (gather) {
-      if (ok) hand_over(g);
-      tc::copy_wait<0>();
-    }
+    if (gather) tc::copy_wait_all();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, et = threadIdx.x - 128;
@@ -732,8 +760,8 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::amax);
     float* inv = reinterpret_cast<float*>(smem + L::inv) + q * 32;
     int lt = 0, chunk = 0;
-    for (int i = first; i < ntiles; i += step, ++lt) {
-      const ProductTile t = product_tile(i, rank, pairs, p.E, off, tiles);
+    for (; walk.valid(); walk.next(), ++lt) {
+      const ProductTile t = walk.tile();
       const int buf = lt & 1;
       bool ok = prod_wait_warp(&d_full[buf], (lt >> 1) & 1, p.err, dead);
       // the four warps go on or leave together: no named barrier below waits
