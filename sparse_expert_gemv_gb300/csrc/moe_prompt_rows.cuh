@@ -49,8 +49,14 @@ struct RowVec;
 
 template <>
 struct RowVec<8> {
+  using Raw = uint4;   // as stored: half the registers of the values
+  __device__ __forceinline__ static Raw raw(const uint16_t* p) {
+    return *reinterpret_cast<const uint4*>(p);
+  }
   __device__ __forceinline__ static void load(const uint16_t* p, float (&f)[8]) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    values(raw(p), f);
+  }
+  __device__ __forceinline__ static void values(const uint4& v, float (&f)[8]) {
     f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
   }
@@ -69,8 +75,13 @@ struct RowVec<8> {
 
 template <>
 struct RowVec<1> {
+  using Raw = uint16_t;
+  __device__ __forceinline__ static Raw raw(const uint16_t* p) { return *p; }
   __device__ __forceinline__ static void load(const uint16_t* p, float (&f)[1]) {
-    f[0] = __uint_as_float((uint32_t)*p << 16);
+    values(raw(p), f);
+  }
+  __device__ __forceinline__ static void values(uint16_t v, float (&f)[1]) {
+    f[0] = __uint_as_float((uint32_t)v << 16);
   }
   __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[1]) {
     *p = f32_to_bf16_rn(f[0]);
@@ -168,15 +179,15 @@ __global__ void __launch_bounds__(1024) moe_add_rms_norm_rows(const NormParams p
 
 // ---------------------------------------------------------------------------
 // moe_group_slots: stable counting sort of S = T * k slots by expert, one
-// cluster of C CTAs (1 or kGroupCluster). The slots are cut into one
+// cluster of C CTAs (1 to 16). The slots are cut into one
 // contiguous range per warp of the cluster. Each warp counts its range into a
-// table of its own (lanes of equal id find one another with a match, so no
-// atomics and a fixed order); the CTAs exchange their totals through
-// distributed shared memory; each warp then walks its range again and hands
-// out places.
+// table of its own (lanes of equal id find one another by ballots over the id's
+// bits, so no atomics and a fixed order) and notes each slot's rank there in `slots`; the
+// CTAs exchange their totals through distributed shared memory; each slot's
+// place is then its expert's start, what lower warps hold of it, and its rank.
 // ---------------------------------------------------------------------------
-constexpr int kGroupCluster = 8;
 constexpr int kGroupThreads = 1024;
+constexpr int kGroupBatch = 8;
 
 struct GroupParams {
   const int32_t* ids;
@@ -207,6 +218,21 @@ __device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
   return v;
 }
 
+// The lanes whose value (of BITS bits) is this lane's, where `in` holds.
+template <int BITS>
+__device__ __forceinline__ unsigned same_value(unsigned v, bool in) {
+  unsigned same = __ballot_sync(kFull, in);
+#pragma unroll
+  for (int b = 0; b < BITS; ++b) {
+    const bool one = (v >> b) & 1u;
+    const unsigned ones = __ballot_sync(kFull, one);
+    same &= one ? ones : ~ones;
+  }
+  return same;
+}
+
+// BITS: of the largest expert id, E - 1.
+template <int BITS>
 __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupParams p) {
   extern __shared__ int sm_group[];
   const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,16 +247,30 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
   const long long w0 = (long long)(rank * warps + warp) * p.per_warp;
   const int lo = (int)min((long long)p.S, w0), hi = (int)min((long long)p.S, w0 + p.per_warp);
   const unsigned below = (1u << lane) - 1u;
-  for (int s = lo; s < hi; s += 32) {
-    int e = s + lane < hi ? p.ids[s + lane] : -1;
-    if (e < 0 || e >= E) e = -1;
-    const unsigned same = __match_any_sync(kFull, e);
-    if (e >= 0 && (same & below) == 0u) cnt[e] += __popc(same);
-    __syncwarp();
+  for (int s0 = lo; s0 < hi; s0 += 32 * kGroupBatch) {
+    int id[kGroupBatch];   // a batch of loads in flight at once
+#pragma unroll
+    for (int i = 0; i < kGroupBatch; ++i) {
+      const int s = s0 + 32 * i + lane;
+      id[i] = s < hi ? p.ids[s] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroupBatch; ++i) {
+      if (s0 + 32 * i >= hi) break;
+      const int s = s0 + 32 * i + lane, e = id[i];
+      const bool in = e >= 0 && e < E;
+      const unsigned same = same_value<BITS>(e, in);
+      const int before = in ? cnt[e] : 0;
+      __syncwarp();
+      if (in && (same & below) == 0u) cnt[e] = before + __popc(same);
+      __syncwarp();
+      if (s < hi) p.slots[s] = before + __popc(same & below);
+    }
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     int sum = 0;
+#pragma unroll 8
     for (int w = 0; w < warps; ++w) {
       const int c = tab[w * E + e];
       tab[w * E + e] = sum;
@@ -248,6 +288,7 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
       total += v;
     }
     start[e] = total;
+#pragma unroll 8
     for (int w = 0; w < warps; ++w) tab[w * E + e] += before;
   }
   // no CTA leaves (or changes `mine`) while another still reads it
@@ -274,18 +315,23 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
     }
   }
   __syncthreads();
-  for (int s = lo; s < hi; s += 32) {
-    const bool in = s + lane < hi;
-    int e = in ? p.ids[s + lane] : -1;
-    if (e < 0 || e >= E) e = -1;
-    const unsigned same = __match_any_sync(kFull, e);
-    int q = -1;
-    if (e >= 0) q = start[e] + cnt[e] + __popc(same & below);
-    __syncwarp();
-    if (e >= 0 && (same & below) == 0u) cnt[e] += __popc(same);
-    __syncwarp();
-    if (in) p.slots[s + lane] = q;
-    if (q >= 0) p.rows[q] = (s + lane) / p.k;
+  for (int s0 = lo; s0 < hi; s0 += 32 * kGroupBatch) {
+    int id[kGroupBatch], rank_in[kGroupBatch];
+#pragma unroll
+    for (int i = 0; i < kGroupBatch; ++i) {
+      const int s = s0 + 32 * i + lane;
+      id[i] = s < hi ? p.ids[s] : -1;
+      rank_in[i] = s < hi ? p.slots[s] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kGroupBatch; ++i) {
+      const int s = s0 + 32 * i + lane, e = id[i];
+      if (s >= hi) continue;
+      const bool in = e >= 0 && e < E;
+      const int q = in ? start[e] + cnt[e] + rank_in[i] : -1;
+      p.slots[s] = q;
+      if (in) p.rows[q] = s / p.k;
+    }
   }
   // rows past the last group
   const int used = mine[0];
@@ -309,6 +355,7 @@ struct CombineParams {
 };
 
 constexpr int kCombineThreads = 256;
+constexpr int kCombineBatch = 8;
 
 template <int V>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_rows(const CombineParams p) {
@@ -321,23 +368,36 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_rows(const Combin
   for (int j = 0; j < V; ++j) acc[j] = 0.f;
   const int32_t* slots = p.slots + (size_t)t * p.k;
   const float* w = p.w + (size_t)t * p.k;
-#pragma unroll 4
-  for (int j = 0; j < p.k; ++j) {
-    const int q = slots[j];
-    if (q < 0 || q >= p.R) continue;
-    const float wj = w[j];
-    float f[V];
-    RowVec<V>::load(p.y + (size_t)q * p.H + (size_t)v * V, f);
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, f[i], acc[i]);
-  }
   const size_t at = (size_t)t * p.H + (size_t)v * V;
-  if (p.residual) {
-    float f[V];
-    RowVec<V>::load(p.residual + at, f);
+  typename RowVec<V>::Raw res{};
+  if (p.residual) res = RowVec<V>::raw(p.residual + at);
+  for (int j0 = 0; j0 < p.k; j0 += kCombineBatch) {
+    // a batch of rows in flight at once; absent ones weigh nothing
+    int q[kCombineBatch];
+    float wj[kCombineBatch];
+    typename RowVec<V>::Raw y[kCombineBatch];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] += f[i];
+    for (int j = 0; j < kCombineBatch; ++j) {
+      q[j] = j0 + j < p.k ? slots[j0 + j] : -1;
+      if (q[j] >= p.R) q[j] = -1;
+      wj[j] = q[j] >= 0 ? w[j0 + j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j)
+      if (q[j] >= 0) y[j] = RowVec<V>::raw(p.y + (size_t)q[j] * p.H + (size_t)v * V);
+#pragma unroll
+    for (int j = 0; j < kCombineBatch; ++j)
+      if (q[j] >= 0) {
+        float f[V];
+        RowVec<V>::values(y[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(wj[j], f[i], acc[i]);
+      }
   }
+  float r[V];
+  RowVec<V>::values(res, r);
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] += r[i];
   RowVec<V>::store(p.out + at, acc);
 }
 

@@ -26,6 +26,10 @@ from ._lib import MOE_FLAG_MXFP4, MOE_PRODUCT_SILU_MUL, MoEProductConfig, check,
 from ._tensors import _need, _ptr, _stream
 
 
+_add_rms_norm, _group, _combine = lib.moe_add_rms_norm, lib.moe_group, lib.moe_combine
+_product_run = lib.moe_product_run
+
+
 class RmsNorm(NamedTuple):
     """What add_rms_norm returns; outputs that were not asked for are None."""
     sum: torch.Tensor | None      # bf16 [T, H]: the new residual stream
@@ -34,20 +38,17 @@ class RmsNorm(NamedTuple):
     scales: torch.Tensor | None   # uint8 [T, H/32]: and UE8M0 scale codes
 
 
+_BF16, _U8, _I32, _F32 = torch.bfloat16, torch.uint8, torch.int32, torch.float32
+_empty = torch.empty
+
+
 def _matrix(t, dtype, name) -> tuple:
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
+    """The shape of a contiguous CUDA matrix of `dtype`."""
+    if isinstance(t, torch.Tensor) and t.dim() != 2:
         raise ValueError(f"{name}: expected two dimensions, got {t.dim()}")
-    _need(t, dtype, t.shape, name)
-    return t.shape
-
-
-def _out(t, dtype, shape, name, like):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
     _need(t, dtype, shape, name)
-    return t
+    return shape
 
 
 def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = True,
@@ -61,23 +62,44 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = Tr
     buffers sum, y, codes and scales may be passed in; sum may be x or
     residual, which is then updated in place.
     """
-    T, H = _matrix(x, torch.bfloat16, "x")
-    _need(weight, torch.bfloat16, (H,), "weight")
+    shape = T, H = _matrix(x, _BF16, "x")
+    _need(weight, _BF16, (H,), "weight")
+    dev = x.device
+    ps = py = pc = pz = pr = 0
     if residual is not None:
-        _need(residual, torch.bfloat16, (T, H), "residual")
-    if not (bf16 or mxfp8):
+        _need(residual, _BF16, shape, "residual")
+        pr = residual.data_ptr()
+        if sum is None:
+            sum = _empty(shape, dtype=_BF16, device=dev)
+    if sum is not None:
+        _need(sum, _BF16, shape, "sum")
+        ps = sum.data_ptr()
+    if bf16:
+        if y is None:
+            y = _empty(shape, dtype=_BF16, device=dev)
+        else:
+            _need(y, _BF16, shape, "y")
+        py = y.data_ptr()
+    elif mxfp8:
+        y = None
+    else:
         raise ValueError("add_rms_norm: ask for bf16 rows, mxfp8 rows or both")
-    if sum is not None or residual is not None:
-        sum = _out(sum, torch.bfloat16, (T, H), "sum", x)
-    y = _out(y, torch.bfloat16, (T, H), "y", x) if bf16 else None
     if mxfp8:
-        codes = _out(codes, torch.uint8, (T, H), "codes", x)
-        scales = _out(scales, torch.uint8, (T, H // 32), "scales", x)
+        if codes is None:
+            codes = _empty(shape, dtype=_U8, device=dev)
+        else:
+            _need(codes, _U8, shape, "codes")
+        if scales is None:
+            scales = _empty((T, H // 32), dtype=_U8, device=dev)
+        else:
+            _need(scales, _U8, (T, H // 32), "scales")
+        pc, pz = codes.data_ptr(), scales.data_ptr()
     else:
         codes = scales = None
-    check(lib.moe_add_rms_norm(T, H, _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(sum),
-                               _ptr(y), _ptr(codes), _ptr(scales), _stream(stream)),
-          "moe_add_rms_norm")
+    st = _add_rms_norm(T, H, x.data_ptr(), pr, weight.data_ptr(), eps, ps, py, pc, pz,
+                       _stream(stream))
+    if st:
+        check(st, "moe_add_rms_norm")
     return RmsNorm(sum, y, codes, scales)
 
 
@@ -87,12 +109,24 @@ def group_by_expert(ids, E: int, *, offsets=None, rows=None, slots=None, stream=
     rows[q] is the token of grouped row q (-1 past the last group) and
     slots[t, j] the grouped row of a slot (-1 for an id outside [0, E), which
     joins no group)."""
-    T, k = _matrix(ids, torch.int32, "ids")
-    offsets = _out(offsets, torch.int32, (E + 1,), "offsets", ids)
-    rows = _out(rows, torch.int32, (T * k,), "rows", ids)
-    slots = _out(slots, torch.int32, (T, k), "slots", ids)
-    check(lib.moe_group(T, k, E, _ptr(ids), _ptr(offsets), _ptr(rows), _ptr(slots),
-                        _stream(stream)), "moe_group")
+    T, k = _matrix(ids, _I32, "ids")
+    dev = ids.device
+    if offsets is None:
+        offsets = _empty((E + 1,), dtype=_I32, device=dev)
+    else:
+        _need(offsets, _I32, (E + 1,), "offsets")
+    if rows is None:
+        rows = _empty((T * k,), dtype=_I32, device=dev)
+    else:
+        _need(rows, _I32, (T * k,), "rows")
+    if slots is None:
+        slots = _empty((T, k), dtype=_I32, device=dev)
+    else:
+        _need(slots, _I32, (T, k), "slots")
+    st = _group(T, k, E, ids.data_ptr(), offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+                _stream(stream))
+    if st:
+        check(st, "moe_group")
     return offsets, rows, slots
 
 
@@ -100,14 +134,19 @@ def combine(y, slots, w, *, residual=None, out=None, stream=None):
     """out[t] = bf16(residual[t] + sum_j w[t, j] * y[slots[t, j]]) over expert
     rows y bf16 [R, H], slots int32 [T, k] (outside [0, R): nothing) and w
     float32 [T, k]; residual bf16 [T, H] is optional and may be `out`."""
-    R, H = _matrix(y, torch.bfloat16, "y")
-    T, k = _matrix(slots, torch.int32, "slots")
-    _need(w, torch.float32, (T, k), "w")
+    R, H = _matrix(y, _BF16, "y")
+    T, k = _matrix(slots, _I32, "slots")
+    _need(w, _F32, (T, k), "w")
     if residual is not None:
-        _need(residual, torch.bfloat16, (T, H), "residual")
-    out = _out(out, torch.bfloat16, (T, H), "out", y)
-    check(lib.moe_combine(T, k, H, R, _ptr(y), _ptr(slots), _ptr(w), _ptr(residual), _ptr(out),
-                          _stream(stream)), "moe_combine")
+        _need(residual, _BF16, (T, H), "residual")
+    if out is None:
+        out = _empty((T, H), dtype=_BF16, device=y.device)
+    else:
+        _need(out, _BF16, (T, H), "out")
+    st = _combine(T, k, H, R, y.data_ptr(), slots.data_ptr(), w.data_ptr(), _ptr(residual),
+                  out.data_ptr(), _stream(stream))
+    if st:
+        check(st, "moe_combine")
     return out
 
 
@@ -164,25 +203,33 @@ class GroupedProduct:
         pair codes uint8 [R, I], scales uint8 [R, I/32]. R is the length of
         `rows`, or A. Rows outside every group are left as they are."""
         A = a.shape[0]
-        _need(a, torch.uint8, (A, self.K), "a")
-        _need(a_scales, torch.uint8, (A, self.K // 32), "a_scales")
-        _need(offsets, torch.int32, (self.E + 1,), "offsets")
-        R = A
+        _need(a, _U8, (A, self.K), "a")
+        _need(a_scales, _U8, (A, self.K // 32), "a_scales")
+        _need(offsets, _I32, (self.E + 1,), "offsets")
+        R, pr = A, 0
         if rows is not None:
-            R = rows.shape[0]
-            _need(rows, torch.int32, (R,), "rows")
+            R, pr = rows.shape[0], rows.data_ptr()
+            _need(rows, _I32, (R,), "rows")
+        shape = (R, self.N // 2) if self.silu_mul else (R, self.N)
+        dtype = _U8 if self.silu_mul else _BF16
+        if out is None:
+            out = _empty(shape, dtype=dtype, device=a.device)
+        else:
+            _need(out, dtype, shape, "out")
+        py, pc, pz = out.data_ptr(), 0, 0
         if self.silu_mul:
-            I = self.N // 2
-            codes = _out(out, torch.uint8, (R, I), "out", a)
-            scales = _out(out_scales, torch.uint8, (R, I // 32), "out_scales", a)
-            check(lib.moe_product_run(self._h, R, A, _ptr(a), _ptr(a_scales), _ptr(offsets),
-                                      _ptr(rows), 0, _ptr(codes), _ptr(scales), _stream(stream)),
-                  "moe_product_run")
-            return codes, scales
-        y = _out(out, torch.bfloat16, (R, self.N), "out", a)
-        check(lib.moe_product_run(self._h, R, A, _ptr(a), _ptr(a_scales), _ptr(offsets), _ptr(rows),
-                                  _ptr(y), 0, 0, _stream(stream)), "moe_product_run")
-        return y
+            if out_scales is None:
+                out_scales = _empty((R, self.N // 64), dtype=_U8, device=a.device)
+            else:
+                _need(out_scales, _U8, (R, self.N // 64), "out_scales")
+            py, pc, pz = 0, py, out_scales.data_ptr()
+        elif out_scales is not None:
+            raise ValueError("out_scales: only a product with silu_mul has scales")
+        st = _product_run(self._h, R, A, a.data_ptr(), a_scales.data_ptr(), offsets.data_ptr(), pr,
+                          py, pc, pz, _stream(stream))
+        if st:
+            check(st, "moe_product_run")
+        return (out, out_scales) if self.silu_mul else out
 
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits, after waiting for the
