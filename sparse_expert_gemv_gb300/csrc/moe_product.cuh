@@ -12,14 +12,14 @@
 // One persistent pair of CTAs (a cluster of 2, cta_group::2) a pair of SMs
 // walks the tiles (token tile of a group, 256 weight rows), found from the
 // offsets on the device. Each CTA holds 128 of the weight rows and half of the
-// group's rows in shared memory, per stage of 128 K, and its 128 rows of the
+// group's rows in shared memory, per stage of 256 K, and its 128 rows of the
 // accumulator in tensor memory; the first CTA issues the MMAs of both. Roles:
 //   warp 0       weights by TMA
 //   warp 1       (first CTA) scales to tensor memory (tcgen05.cp) and the MMAs
 //   warp 2       the group's rows by TMA, where they are contiguous
 //   warp 3       where they are gathered, word to the MMAs that they landed
 //   warps 4-7    epilogue, one per lane quarter of tensor memory
-//   warps 8-11   scales, four stages at a time, into shared memory in the order
+//   warps 8-11   scales, 512 K at a time, into shared memory in the order
 //                tcgen05.cp takes; and the group's rows where they are gathered
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
 // the next tile's MMAs.
@@ -37,24 +37,28 @@ namespace moe {
 
 constexpr int kProdRows = 128;     // weight rows a CTA (half of the MMA's M)
 // Rows of a group a tile (N). Two accumulators of 192 columns and two batches
-// of four stages' scales (12 columns a stage) share the 512 columns of tensor
+// of four blocks' scales (12 columns a block) share the 512 columns of tensor
 // memory.
 constexpr int kProdCols = 192;
-constexpr int kProdK = 128;        // K elements a stage: one 128-byte swizzle row
-constexpr int kProdStages = 6;
-constexpr int kProdSfStages = 4;   // stages a batch of scales covers
+constexpr int kProdK = 128;        // K elements a block: one 128-byte swizzle row
+// Blocks a stage: the MMA warp spends some 250 cycles a stage on barriers and
+// loop, which two blocks share (STAGEFIG).
+constexpr int kProdBlocks = 2;
+constexpr int kProdStages = 3;
+constexpr int kProdSfBlocks = 4;   // blocks a batch of scales covers
 constexpr int kProdThreads = 384;
 constexpr int kProdMaxE = 1024;
 constexpr int kProdABytes = kProdRows * kProdK;
 constexpr int kProdBBytes = kProdCols / 2 * kProdK;
-constexpr int kProdSfaBytes = 512;    // a stage's weight scales of one CTA
-constexpr int kProdSfbBytes = 1024;   // a stage's row scales (up to 256 rows)
-constexpr int kProdSfBytes = kProdSfStages * (kProdSfaBytes + kProdSfbBytes);
+constexpr int kProdSfaBytes = 512;    // a block's weight scales of one CTA
+constexpr int kProdSfbBytes = 1024;   // a block's row scales (up to 256 rows)
+constexpr int kProdSfBytes = kProdSfBlocks * (kProdSfaBytes + kProdSfbBytes);
 // tensor-memory columns
 constexpr uint32_t kProdTmemCols = 512;
 constexpr uint32_t kProdSfCol = 2 * kProdCols;
-constexpr uint32_t kProdSfCols = 12;   // a stage's: 4 of the weights, 8 of the rows
-static_assert(2 * kProdCols + 2 * kProdSfStages * kProdSfCols <= kProdTmemCols, "tensor memory");
+constexpr uint32_t kProdSfCols = 12;   // a block's: 4 of the weights, 8 of the rows
+static_assert(2 * kProdCols + 2 * kProdSfBlocks * kProdSfCols <= kProdTmemCols, "tensor memory");
+static_assert(kProdSfBlocks % kProdBlocks == 0, "a batch of scales covers whole stages");
 static_assert(kProdCols % 32 == 0 && kProdCols <= 256, "token tile");
 // epilogue staging: a chunk of 32 columns as rows of 128 bf16 (16-byte pieces
 // swizzled by the row), or of 64 codes padded to 80 bytes, two chunks in turn
@@ -82,8 +86,8 @@ struct ProductParams {
 
 struct ProductSmem {
   static constexpr int a = 0;
-  static constexpr int b = a + kProdStages * kProdABytes;
-  static constexpr int sf = b + kProdStages * kProdBBytes;         // 2 batches
+  static constexpr int b = a + kProdStages * kProdBlocks * kProdABytes;
+  static constexpr int sf = b + kProdStages * kProdBlocks * kProdBBytes;         // 2 batches
   static constexpr int out = sf + 2 * kProdSfBytes;                // 2 chunks
   static constexpr int amax = out + 2 * kProdStageOut;             // [2][4][32] words
   static constexpr int inv = amax + 2 * 4 * 32 * 4;                // [4][32] floats
@@ -241,7 +245,7 @@ __device__ __forceinline__ void stm4_trans(uint32_t addr, uint32_t a, uint32_t b
 
 // ---------------------------------------------------------------------------
 // moe_product_lay_scales: the weights' scales in the order tcgen05.cp takes
-// them, once per handle: for (expert, 128-row tile, stage) 512 bytes, lane l's
+// them, once per handle: for (expert, 128-row tile, block) 512 bytes, lane l's
 // 16 holding four scale bytes of each of the MMA rows l, l + 32, l + 64,
 // l + 96. Places past N or K get 1 (their codes arrive as zeros).
 // ---------------------------------------------------------------------------
@@ -379,7 +383,7 @@ struct ProductWalk {
   }
 };
 
-// A batch's scale bytes (16, four stages) of one row from stage kb on; bytes
+// A batch's scale bytes (16, four blocks) of one row from block kb on; bytes
 // past the row's end read as 127.
 __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int ks, int vec) {
   if (vec == 16) return *reinterpret_cast<const uint4*>(row + kb * 4);
@@ -401,7 +405,7 @@ __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int
 
 // What a thread of the scale warps holds of a tile: the two rows (r and
 // r + 128 of the tile) whose scales it brings, and with gathered rows the
-// rows of this CTA's half that it copies 16 bytes a stage of. load() only
+// rows of this CTA's half that it copies 16 bytes a block of. load() only
 // issues the loads of gathered rows; settle() uses them, a tile later.
 struct ProductRows {
   int scale_row[2];
@@ -523,22 +527,24 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     bool ok = true;
     for (; ok && walk.valid(); walk.next()) {
       const ProductTile t = walk.tile();
-      const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);
+      const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);   // a block
       // the groups of 16 neurons of all experts' gate and up rows in one row
       const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
-      for (int kb = 0; kb < nk; ++kb, ++g) {
-        const int s = rg.slot;
+      for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
+        const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
         if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
-        uint8_t* dst = smem + L::a + s * kProdABytes;
+        uint8_t* dst = smem + L::a + s * kProdBlocks * kProdABytes;
         if (tc::elect()) {
-          if (rank == 0) mbar_expect_tx(&full[s], bytes);
-          if (SILU)
-            tc::tma2_load_5d(dst, &p.tm_w, kb * kProdK, 0, 0, 0, grp, full0 + 8 * s);
-          else
-            tc::tma2_load_3d(dst, &p.tm_w, kb * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
+          if (rank == 0) mbar_expect_tx(&full[s], nb * bytes);
+          for (int b = 0; b < nb; ++b, dst += kProdABytes) {
+            if (SILU)
+              tc::tma2_load_5d(dst, &p.tm_w, (kb + b) * kProdK, 0, 0, 0, grp, full0 + 8 * s);
+            else
+              tc::tma2_load_3d(dst, &p.tm_w, (kb + b) * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
+          }
         }
         __syncwarp();
         rg.next();
@@ -566,37 +572,44 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kProdCols;
-        for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages) {
-          const int ns = min(kProdSfStages, nk - k0);
+        for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks) {
+          const int ns = min(kProdSfBlocks, nk - k0);
           ok = prod_wait_warp(&sf_full[rs.slot], rs.phase, p.err, dead);
           if (!ok) break;
-          const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfStages * kProdSfCols;
+          const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfBlocks * kProdSfCols;
           const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
           if (tc::elect()) {
             for (int j = 0; j < ns; ++j) {
               const uint32_t c = sfc + j * kProdSfCols;
-              const uint32_t sb = sfs + kProdSfStages * kProdSfaBytes + j * kProdSfbBytes;
+              const uint32_t sb = sfs + kProdSfBlocks * kProdSfaBytes + j * kProdSfbBytes;
               tc::cp_scales(c, sfs + j * kProdSfaBytes);
               tc::cp_scales(c + 4, sb);
               if (n > 128) tc::cp_scales(c + 8, sb + 512);
             }
           }
           __syncwarp();
-          for (int j = 0; j < ns; ++j) {
+          for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
             const int s = rg.slot;
             ok = ready || prod_wait_warp(&full[s], rg.phase, p.err, dead);
             if (!ok) break;
             rg.next();
             // the next stage's barrier is looked at while this one's MMAs issue
             const bool next = mbar_test(&full[rg.slot], rg.phase);
-            const uint64_t ad = tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdABytes));
-            const uint64_t bd = tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBBytes));
-            const uint32_t c = sfc + j * kProdSfCols;
+            const uint64_t ad =
+                tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdBlocks * kProdABytes));
+            const uint64_t bd =
+                tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBlocks * kProdBBytes));
             if (tc::elect()) {
 #pragma unroll
-              for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
-                tc::mma_mx(d, ad + 2 * q, bd + 2 * q, idesc | tc::mx_scale_id(q), c, c + 4,
-                           k0 + j + q > 0 ? 1u : 0u);
+              for (int b = 0; b < kProdBlocks; ++b) {
+                if (j0 + b >= ns) break;
+                const uint32_t c = sfc + (j0 + b) * kProdSfCols;
+#pragma unroll
+                for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
+                  tc::mma_mx(d, ad + b * (kProdABytes >> 4) + 2 * q,
+                             bd + b * (kProdBBytes >> 4) + 2 * q, idesc | tc::mx_scale_id(q), c,
+                             c + 4, k0 + j0 + b + q > 0 ? 1u : 0u);
+              }
               tc::commit2(&empty[s]);
             }
             ready = __all_sync(kFull, next);
@@ -631,21 +644,24 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       for (; ok && walk.valid(); walk.next()) {
         const ProductTile t = walk.tile();
         const int half = t.half(), r0 = t.r0 + rank * half;
-        for (int kb = 0; kb < nk; ++kb, ++g) {
-          const int s = rg.slot;
+        for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
+          const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
           if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
-          uint8_t* dst = smem + L::b + s * kProdBBytes;
+          uint8_t* dst = smem + L::b + s * kProdBlocks * kProdBBytes;
           if (tc::elect()) {
-            int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
+            for (int b = 0; b < nb; ++b, dst += kProdBBytes) {
+              int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
 #pragma unroll
-            for (int b = 2; b >= 0; --b)
-              if (half & (16 << b)) {
-                tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[b], kb * kProdK, r0 + r, full0 + 8 * s);
-                r += 16 << b;
-              }
+              for (int x = 2; x >= 0; --x)
+                if (half & (16 << x)) {
+                  tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[x], (kb + b) * kProdK, r0 + r,
+                                   full0 + 8 * s);
+                  r += 16 << x;
+                }
+            }
           }
           __syncwarp();
           rg.next();
@@ -662,7 +678,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       const uint32_t full0 = tc::cluster_addr(full, 0);
       bool ok = true;
       for (; ok && walk.valid(); walk.next())
-        for (int kb = 0; kb < nk; ++kb) {
+        for (int kb = 0; kb < nk; kb += kProdBlocks) {
           if (!prod_wait_warp(&copied[rg.slot], rg.phase, p.err, dead)) {
             ok = false;
             break;
@@ -693,7 +709,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     }
     uint4 wsf = make_uint4(0, 0, 0, 0), rsf[2] = {wsf, wsf};
     auto load_batch = [&](const ProductRows& pr, int k0) {
-      if (r < 32 * min(kProdSfStages, nk - k0))
+      if (r < 32 * min(kProdSfBlocks, nk - k0))
         wsf = *reinterpret_cast<const uint4*>(
             p.sfa + (((size_t)pr.t.e * 2 * pairs + pr.t.m) * nk + k0) * kProdSfaBytes + r * 16);
       rsf[0] = load_row_scales(p.a_scales + (size_t)pr.scale_row[0] * ks, k0, ks, p.sf_vec);
@@ -706,14 +722,14 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       more = walk.valid();
       if (more) nxt.load(p, walk.tile(), rank, r);
       const int half = cur.t.half();
-      for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages, ++gb) {
+      for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks, ++gb) {
         if (gb >= 2 && !prod_wait_warp(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
         uint8_t* sf = smem + L::sf + rs.slot * kProdSfBytes;
         *reinterpret_cast<uint4*>(sf + r * 16) = wsf;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(sf + kProdSfStages * kProdSfaBytes) +
+        uint32_t* dst = reinterpret_cast<uint32_t*>(sf + kProdSfBlocks * kProdSfaBytes) +
                         (r & 31) * 4 + (r >> 5);
         dst[0] = rsf[0].x, dst[256] = rsf[0].y, dst[512] = rsf[0].z, dst[768] = rsf[0].w;
         if (cur.t.n > 128)
@@ -723,27 +739,32 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (lane == 0) tc::arrive_at(sf_full0 + 8 * rs.slot);
         rs.next();
         // the next batch's loads run while this one is used
-        if (k0 + kProdSfStages < nk)
-          load_batch(cur, k0 + kProdSfStages);
+        if (k0 + kProdSfBlocks < nk)
+          load_batch(cur, k0 + kProdSfBlocks);
         else if (more) {
           nxt.settle(p);
           load_batch(nxt, 0);
         }
         if (!gather) continue;
-        const int ns = min(kProdSfStages, nk - k0);
-        for (int j = 0; j < ns; ++j) {
-          const int s = rg.slot, at = (k0 + j) * kProdK + within;
+        const int ns = min(kProdSfBlocks, nk - k0);
+        for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
+          const int s = rg.slot;
           if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
-          const uint32_t bytes = at < p.K ? 16u : 0u;
-          const uint8_t* src = p.a + (bytes ? at : 0);
 #pragma unroll
-          for (int c = 0; c < kProdCols / 32; ++c)
-            if (16 * c < half)
-              tc::copy16(copy_dst + s * kProdBBytes + c * 16 * kProdK,
-                         src + (size_t)cur.copy_row[c] * p.K, bytes);
+          for (int b = 0; b < kProdBlocks; ++b) {
+            if (j0 + b >= ns) break;
+            const int at = (k0 + j0 + b) * kProdK + within;
+            const uint32_t bytes = at < p.K ? 16u : 0u;
+            const uint8_t* src = p.a + (bytes ? at : 0);
+#pragma unroll
+            for (int c = 0; c < kProdCols / 32; ++c)
+              if (16 * c < half)
+                tc::copy16(copy_dst + (s * kProdBlocks + b) * kProdBBytes + c * 16 * kProdK,
+                           src + (size_t)cur.copy_row[c] * p.K, bytes);
+          }
           tc::copy_arrive(&copied[s]);
           rg.next();
           ++g;
