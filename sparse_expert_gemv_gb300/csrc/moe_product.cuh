@@ -18,7 +18,8 @@
 //   warp 1       (first CTA) scales to tensor memory (tcgen05.cp) and the MMAs
 //   warp 2       the group's rows by TMA, where they are contiguous
 //   warp 3       where they are gathered, word to the MMAs that they landed
-//   warps 4-7    epilogue, one per lane quarter of tensor memory
+//   warps 4-7    epilogue, one per lane quarter of tensor memory, and
+//   warps 12-15  the same for every other chunk of 32 columns
 //   warps 8-11   scales, 512 K at a time, into shared memory in the order
 //                tcgen05.cp takes; and the group's rows where they are gathered
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
@@ -46,7 +47,7 @@ constexpr int kProdK = 128;        // K elements a block: one 128-byte swizzle r
 constexpr int kProdBlocks = 2;
 constexpr int kProdStages = 3;
 constexpr int kProdSfBlocks = 4;   // blocks a batch of scales covers
-constexpr int kProdThreads = 384;
+constexpr int kProdThreads = 512;
 constexpr int kProdMaxE = 1024;
 constexpr int kProdABytes = kProdRows * kProdK;
 constexpr int kProdBBytes = kProdCols / 2 * kProdK;
@@ -60,8 +61,9 @@ constexpr uint32_t kProdSfCols = 12;   // a block's: 4 of the weights, 8 of the 
 static_assert(2 * kProdCols + 2 * kProdSfBlocks * kProdSfCols <= kProdTmemCols, "tensor memory");
 static_assert(kProdSfBlocks % kProdBlocks == 0, "a batch of scales covers whole stages");
 static_assert(kProdCols % 32 == 0 && kProdCols <= 256, "token tile");
-// epilogue staging: a chunk of 32 columns as rows of 128 bf16 (16-byte pieces
-// swizzled by the row), or of 64 codes padded to 80 bytes, two chunks in turn
+// epilogue staging, two in turn for each of its two groups of four warps: a
+// chunk of 32 columns as rows of 128 bf16 (16-byte pieces swizzled by the row),
+// or of 64 codes padded to 80 bytes
 constexpr int kProdStageOut = 32 * 256;
 constexpr int kProdCodePitch = 80;
 
@@ -88,30 +90,25 @@ struct ProductSmem {
   static constexpr int a = 0;
   static constexpr int b = a + kProdStages * kProdBlocks * kProdABytes;
   static constexpr int sf = b + kProdStages * kProdBlocks * kProdBBytes;         // 2 batches
-  static constexpr int out = sf + 2 * kProdSfBytes;                // 2 chunks
-  static constexpr int amax = out + 2 * kProdStageOut;             // [2][4][32] words
-  static constexpr int inv = amax + 2 * 4 * 32 * 4;                // [4][32] floats
-  static constexpr int off = inv + 4 * 32 * 4;                     // [E + 1] group starts
+  static constexpr int out = sf + 2 * kProdSfBytes;                // [2][2] chunks
+  static constexpr int amax = out + 4 * kProdStageOut;             // [2][2][4][32] words
+  static constexpr int inv = amax + 2 * 2 * 4 * 32 * 4;            // [2][4][32] floats
+  static constexpr int off = inv + 2 * 4 * 32 * 4;                 // [E + 1] group starts
   static constexpr int tiles = off + (kProdMaxE + 4) * 4;          // [E + 1] token tiles before
   static constexpr int piece = tiles + (kProdMaxE + 4) * 4;        // [E] rows of a group's pieces
-  static constexpr int bars = piece + kProdMaxE * 4;
+  static constexpr int bars = piece + kProdMaxE * 2;
   static constexpr int total = bars + (3 * kProdStages + 9) * 8 + 16;
 };
 
 namespace tc {
 
-// True in one lane of a converged warp, always the same one. The tensor-memory
-// and TMA instructions take their operands in registers that the whole warp
-// shares; issued under this predicate in a loop that all lanes walk they cost
-// a few cycles each, where a loop walked by lane 0 alone cost 60 to 80 (the
-// pipeline then waited for them: 1024 cycles a stage at 384 of MMA).
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
+// The wrappers below are called by whole, converged warps and act in one lane,
+// always the same one, chosen inside the instruction sequence and by predicate.
+// No branch on a lane appears in a role's loop: with a loop walked by lane 0
+// alone a tensor-memory instruction cost 60 to 80 cycles and a wait on a
+// barrier that had long completed over 200, and the MMA pipe idled for more
+// than half of the time.
+#define MOE_ELECT ".reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
 
 // The address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -121,7 +118,15 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 }
 // One arrival on an mbarrier of the cluster.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("{\n\t" MOE_ELECT "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+               : "memory");
+}
+// One arrival on this CTA's mbarrier that announces `bytes` of copies.
+__device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("{\n\t" MOE_ELECT
+               "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(smem_addr(bar)),
+               "r"(bytes)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t ncols) {
@@ -141,24 +146,27 @@ __device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
 __device__ __forceinline__ void tma2_load_2d(void* dst, const void* tmap, int x, int y,
                                              uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma2_load_3d(void* dst, const void* tmap, int x, int y, int z,
                                              uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(smem_addr(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma2_load_5d(void* dst, const void* tmap, int c0, int c1, int c2,
                                              int c3, int c4, uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_addr(dst)),
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(smem_addr(dst)),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
       : "memory");
 }
@@ -183,7 +191,9 @@ __device__ __forceinline__ void copy_wait_all() {
 __device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
   const uint64_t desc =
       (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+  asm volatile("{\n\t" MOE_ELECT "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(
+                   taddr),
+               "l"(desc)
                : "memory");
 }
 
@@ -191,8 +201,9 @@ __device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+      "{\n\t" MOE_ELECT
+      ".reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
       "[%5], p;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
       : "memory");
@@ -208,11 +219,12 @@ __device__ __forceinline__ uint32_t mx_idesc(uint32_t fa, int n) {
 __device__ __forceinline__ uint32_t mx_scale_id(uint32_t j) { return (j << 4) | (j << 29); }
 
 // Arrive once on the mbarrier at `bar` of both CTAs when every MMA and copy
-// this thread issued so far is done.
+// issued so far is done.
 __device__ __forceinline__ void commit2(uint64_t* bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "{\n\t" MOE_ELECT
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;\n\t}" ::"r"(smem_addr(bar)),
       "h"((uint16_t)3)
       : "memory");
 }
@@ -285,8 +297,6 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
 // moe_product_tiles
 // ---------------------------------------------------------------------------
 
-// Bounded wait on a phase of this CTA's mbarrier that either CTA's arrivals
-// complete; a timeout marks the CTA dead (every role winds down).
 __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -298,22 +308,19 @@ __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
       : "memory");
   return done != 0;
 }
+// A whole warp's bounded wait on a phase of this CTA's mbarrier; a timeout
+// marks the CTA dead (every role winds down).
 __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                           volatile int* dead) {
-  if (prod_poll(bar, parity)) return true;
+  if (__all_sync(kFull, prod_poll(bar, parity))) return true;
 #pragma unroll 1
   for (uint32_t it = 0; it < kMbarPolls; ++it) {
-    if (*dead) return false;
-    if (prod_poll(bar, parity)) return true;
+    if (__any_sync(kFull, *dead)) return false;
+    if (__all_sync(kFull, prod_poll(bar, parity))) return true;
   }
   atomicOr(err, kDeviceTimeout);
   *dead = 1;
   return false;
-}
-__device__ __forceinline__ bool prod_wait_warp(uint64_t* bar, uint32_t parity, uint32_t* err,
-                                               volatile int* dead) {
-  const bool ok = prod_wait(bar, parity, err, dead);
-  return __all_sync(kFull, ok);
 }
 
 // Barrier over `nthreads` threads on named barrier `id`: whether `ok` holds
@@ -350,12 +357,13 @@ struct ProductTile {
 // part: the next token tile's expert is found 32 experts at a time (a search
 // and divisions cost each role a thousand cycles a tile).
 struct ProductWalk {
-  const int *off, *tiles, *piece;   // [E + 1], [E + 1], [E]
+  const int *off, *tiles;           // [E + 1]
+  const uint16_t* piece;            // [E]
   int rank, pairs, E, ntok;
   int q, m, dq, dm;                 // token tile and pair of weight tiles, and a step's
   int e;                            // expert of q, once found
-  __device__ __forceinline__ ProductWalk(const int* off_, const int* tiles_, const int* piece_,
-                                         int rank_, int pairs_, int E_, int first, int step)
+  __device__ __forceinline__ ProductWalk(const int* off_, const int* tiles_,
+                                         const uint16_t* piece_, int rank_, int pairs_, int E_, int first, int step)
       : off(off_), tiles(tiles_), piece(piece_), rank(rank_), pairs(pairs_), E(E_),
         ntok(uniform(tiles_[E_])), q(first / pairs_), m(first % pairs_), dq(step / pairs_),
         dm(step % pairs_), e(0) {}
@@ -446,7 +454,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   using L = ProductSmem;
   int* off = reinterpret_cast<int*>(smem + L::off);
   int* tiles = reinterpret_cast<int*>(smem + L::tiles);
-  int* piece = reinterpret_cast<int*>(smem + L::piece);
+  uint16_t* piece = reinterpret_cast<uint16_t*>(smem + L::piece);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
   uint64_t* empty = full + kProdStages;
   uint64_t* copied = empty + kProdStages;                         // gathered rows
@@ -477,7 +485,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       mbar_init(&sf_full[i], 8);    // both CTAs' scale warps
       mbar_init(&sf_empty[i], 1);
       mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 8);    // both CTAs' epilogue warps
+      mbar_init(&d_empty[i], 16);   // both CTAs' epilogue warps
     }
     mbar_init(drain, 1);
     *dead = 0;
@@ -495,7 +503,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int hi = min(max(p.offsets[e + 1], 0), p.R);
         nt = hi > lo ? (hi - lo + kProdCols - 1) / kProdCols : 0;
         off[e] = lo;
-        piece[e] = nt ? ((hi - lo + nt - 1) / nt + 31) & ~31 : 0;
+        piece[e] = (uint16_t)(nt ? ((hi - lo + nt - 1) / nt + 31) & ~31 : 0);
       }
       int incl = nt;
 #pragma unroll
@@ -532,21 +540,18 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
       for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
         const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
-        if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+        if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
         uint8_t* dst = smem + L::a + s * kProdBlocks * kProdABytes;
-        if (tc::elect()) {
-          if (rank == 0) mbar_expect_tx(&full[s], nb * bytes);
-          for (int b = 0; b < nb; ++b, dst += kProdABytes) {
-            if (SILU)
-              tc::tma2_load_5d(dst, &p.tm_w, (kb + b) * kProdK, 0, 0, 0, grp, full0 + 8 * s);
-            else
-              tc::tma2_load_3d(dst, &p.tm_w, (kb + b) * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
-          }
+        if (rank == 0) tc::expect(&full[s], nb * bytes);
+        for (int b = 0; b < nb; ++b, dst += kProdABytes) {
+          if (SILU)
+            tc::tma2_load_5d(dst, &p.tm_w, (kb + b) * kProdK, 0, 0, 0, grp, full0 + 8 * s);
+          else
+            tc::tma2_load_3d(dst, &p.tm_w, (kb + b) * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
         }
-        __syncwarp();
         rg.next();
       }
     }
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     if (rank == 0) {
       RingPos rg(kProdStages), rs(2);
       int lt = 0;
-      bool ok = true, ready = false;
+      bool ok = true;
       ProductTile t, after;
       bool more = walk.valid();
       if (more) after = walk.tile();
@@ -568,56 +573,48 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int n = t.cols();
         const uint32_t idesc = tc::mx_idesc(p.a_format, n);
         const int buf = lt & 1;
-        if (lt >= 2) ok = prod_wait_warp(&d_empty[buf], ((lt >> 1) - 1) & 1, p.err, dead);
+        if (lt >= 2) ok = prod_wait(&d_empty[buf], ((lt >> 1) - 1) & 1, p.err, dead);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kProdCols;
         for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks) {
           const int ns = min(kProdSfBlocks, nk - k0);
-          ok = prod_wait_warp(&sf_full[rs.slot], rs.phase, p.err, dead);
+          ok = prod_wait(&sf_full[rs.slot], rs.phase, p.err, dead);
           if (!ok) break;
           const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfBlocks * kProdSfCols;
           const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
-          if (tc::elect()) {
-            for (int j = 0; j < ns; ++j) {
-              const uint32_t c = sfc + j * kProdSfCols;
-              const uint32_t sb = sfs + kProdSfBlocks * kProdSfaBytes + j * kProdSfbBytes;
-              tc::cp_scales(c, sfs + j * kProdSfaBytes);
-              tc::cp_scales(c + 4, sb);
-              if (n > 128) tc::cp_scales(c + 8, sb + 512);
-            }
+          for (int j = 0; j < ns; ++j) {
+            const uint32_t c = sfc + j * kProdSfCols;
+            const uint32_t sb = sfs + kProdSfBlocks * kProdSfaBytes + j * kProdSfbBytes;
+            tc::cp_scales(c, sfs + j * kProdSfaBytes);
+            tc::cp_scales(c + 4, sb);
+            if (n > 128) tc::cp_scales(c + 8, sb + 512);
           }
-          __syncwarp();
           for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
             const int s = rg.slot;
-            ok = ready || prod_wait_warp(&full[s], rg.phase, p.err, dead);
+            ok = prod_wait(&full[s], rg.phase, p.err, dead);
             if (!ok) break;
-            rg.next();
-            // the next stage's barrier is looked at while this one's MMAs issue
-            const bool next = mbar_test(&full[rg.slot], rg.phase);
             const uint64_t ad =
                 tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdBlocks * kProdABytes));
             const uint64_t bd =
                 tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBlocks * kProdBBytes));
-            if (tc::elect()) {
 #pragma unroll
-              for (int b = 0; b < kProdBlocks; ++b) {
-                if (j0 + b >= ns) break;
-                const uint32_t c = sfc + (j0 + b) * kProdSfCols;
+            for (int b = 0; b < kProdBlocks; ++b) {
+              if (j0 + b >= ns) break;
+              const uint32_t c = sfc + (j0 + b) * kProdSfCols;
 #pragma unroll
-                for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
-                  tc::mma_mx(d, ad + b * (kProdABytes >> 4) + 2 * q,
-                             bd + b * (kProdBBytes >> 4) + 2 * q, idesc | tc::mx_scale_id(q), c,
-                             c + 4, k0 + j0 + b + q > 0 ? 1u : 0u);
-              }
-              tc::commit2(&empty[s]);
+              for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
+                tc::mma_mx(d, ad + b * (kProdABytes >> 4) + 2 * q,
+                           bd + b * (kProdBBytes >> 4) + 2 * q, idesc | tc::mx_scale_id(q), c,
+                           c + 4, k0 + j0 + b + q > 0 ? 1u : 0u);
             }
-            ready = __all_sync(kFull, next);
+            tc::commit2(&empty[s]);
+            rg.next();
           }
           // the batch's places in shared and tensor memory are free when its
           // MMAs are done
-          if (ok && tc::elect()) tc::commit2(&sf_empty[rs.slot]);
-          __syncwarp();
+          if (!ok) break;
+          tc::commit2(&sf_empty[rs.slot]);
           rs.next();
           if (k0 == 0) {   // find the next tile while MMAs are under way
             walk.next();
@@ -626,12 +623,10 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           }
         }
         if (!ok) break;
-        if (tc::elect()) tc::commit2(&d_full[buf]);
-        __syncwarp();
+        tc::commit2(&d_full[buf]);
       }
       // every MMA done before tensor memory is released
-      if (tc::elect()) tc::commit2(drain);
-      __syncwarp();
+      tc::commit2(drain);
       mbar_wait(drain, 0, p.err);
     }
   } else if (warp == 2) {
@@ -646,24 +641,21 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int half = t.half(), r0 = t.r0 + rank * half;
         for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
           const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
-          if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
           uint8_t* dst = smem + L::b + s * kProdBlocks * kProdBBytes;
-          if (tc::elect()) {
-            for (int b = 0; b < nb; ++b, dst += kProdBBytes) {
-              int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
+          for (int b = 0; b < nb; ++b, dst += kProdBBytes) {
+            int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
 #pragma unroll
-              for (int x = 2; x >= 0; --x)
-                if (half & (16 << x)) {
-                  tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[x], (kb + b) * kProdK, r0 + r,
-                                   full0 + 8 * s);
-                  r += 16 << x;
-                }
-            }
+            for (int x = 2; x >= 0; --x)
+              if (half & (16 << x)) {
+                tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[x], (kb + b) * kProdK, r0 + r,
+                                 full0 + 8 * s);
+                r += 16 << x;
+              }
           }
-          __syncwarp();
           rg.next();
         }
       }
@@ -679,16 +671,17 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       bool ok = true;
       for (; ok && walk.valid(); walk.next())
         for (int kb = 0; kb < nk; kb += kProdBlocks) {
-          if (!prod_wait_warp(&copied[rg.slot], rg.phase, p.err, dead)) {
+          if (!prod_wait(&copied[rg.slot], rg.phase, p.err, dead)) {
             ok = false;
             break;
           }
           tc::fence_proxy_async();
-          if (lane == 0) tc::arrive_at(full0 + 8 * rg.slot);
+          __syncwarp();
+          tc::arrive_at(full0 + 8 * rg.slot);
           rg.next();
         }
     }
-  } else if (warp >= 8) {
+  } else if ((warp >> 2) == 2) {
     // ---------------------------------------------- scales and gathered rows
     const int r = threadIdx.x - 256;
     const int ks = p.K / 32;
@@ -722,8 +715,12 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       more = walk.valid();
       if (more) nxt.load(p, walk.tile(), rank, r);
       const int half = cur.t.half();
+      const uint8_t* src[kProdCols / 32];
+#pragma unroll
+      for (int c = 0; c < kProdCols / 32; ++c)
+        src[c] = p.a + (gather && 16 * c < half ? (size_t)cur.copy_row[c] * p.K : 0);
       for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks, ++gb) {
-        if (gb >= 2 && !prod_wait_warp(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
+        if (gb >= 2 && !prod_wait(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
@@ -736,7 +733,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           dst[128] = rsf[1].x, dst[384] = rsf[1].y, dst[640] = rsf[1].z, dst[896] = rsf[1].w;
         tc::fence_proxy_async();
         __syncwarp();
-        if (lane == 0) tc::arrive_at(sf_full0 + 8 * rs.slot);
+        tc::arrive_at(sf_full0 + 8 * rs.slot);
         rs.next();
         // the next batch's loads run while this one is used
         if (k0 + kProdSfBlocks < nk)
@@ -749,7 +746,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int ns = min(kProdSfBlocks, nk - k0);
         for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
           const int s = rg.slot;
-          if (g >= kProdStages && !prod_wait_warp(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
@@ -758,12 +755,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
             if (j0 + b >= ns) break;
             const int at = (k0 + j0 + b) * kProdK + within;
             const uint32_t bytes = at < p.K ? 16u : 0u;
-            const uint8_t* src = p.a + (bytes ? at : 0);
+            const int from = bytes ? at : 0;
+            const uint32_t to = copy_dst + (s * kProdBlocks + b) * kProdBBytes;
 #pragma unroll
             for (int c = 0; c < kProdCols / 32; ++c)
-              if (16 * c < half)
-                tc::copy16(copy_dst + (s * kProdBlocks + b) * kProdBBytes + c * 16 * kProdK,
-                           src + (size_t)cur.copy_row[c] * p.K, bytes);
+              if (16 * c < half) tc::copy16(to + c * 16 * kProdK, src[c] + from, bytes);
           }
           tc::copy_arrive(&copied[s]);
           rg.next();
@@ -775,23 +771,25 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     if (gather) tc::copy_wait_all();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
-    const int q = warp & 3, et = threadIdx.x - 128;
+    const int q = warp & 3, et = threadIdx.x & 127;
+    const int grp = warp >> 3;   // chunks of 32 columns go to the two groups in turn
+    const int bar = 1 + 3 * grp;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
-    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::amax);
-    float* inv = reinterpret_cast<float*>(smem + L::inv) + q * 32;
+    uint32_t* amax = reinterpret_cast<uint32_t*>(smem + L::amax) + grp * 256;
+    float* inv = reinterpret_cast<float*>(smem + L::inv) + (grp * 4 + q) * 32;
     int lt = 0, chunk = 0;
     for (; walk.valid(); walk.next(), ++lt) {
       const ProductTile t = walk.tile();
       const int buf = lt & 1;
-      bool ok = prod_wait_warp(&d_full[buf], (lt >> 1) & 1, p.err, dead);
-      // the four warps go on or leave together: no named barrier below waits
+      bool ok = prod_wait(&d_full[buf], (lt >> 1) & 1, p.err, dead);
+      // a group's warps go on or leave together: no named barrier below waits
       // for a warp that gave up
-      ok = named_all(1, 128, ok);
+      ok = named_all(bar, 128, ok);
       if (!ok) break;
       tc::fence_after();
-      for (int c0 = 0; c0 < t.n; c0 += 32, ++chunk) {
-        uint8_t* stage = smem + L::out + (chunk & 1) * kProdStageOut;
+      for (int c0 = 32 * grp; c0 < t.n; c0 += 64, ++chunk) {
+        uint8_t* stage = smem + L::out + (2 * grp + (chunk & 1)) * kProdStageOut;
         uint32_t lo[16], hi[16];
         tc::ld_16x32(lanes + buf * kProdCols + c0, lo);
         tc::ld_16x32(lanes + (16u << 16) + buf * kProdCols + c0, hi);
@@ -811,7 +809,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
                            pack(lo[4 * b + 2], lo[4 * b + 3]), pack(hi[4 * b], hi[4 * b + 1]),
                            pack(hi[4 * b + 2], hi[4 * b + 3]));
           }
-          named_sync(1, 128);
+          named_sync(bar, 128);
           const int pc = et & 15, n = t.m * kProdRows + 8 * pc;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -850,7 +848,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           // the block's other 16 neurons are in the neighbouring warp
           uint32_t* am = amax + (chunk & 1) * 128;
           am[q * 32 + col] = mx[0];
-          named_sync(2 + (q >> 1), 64);
+          named_sync(bar + 1 + (q >> 1), 64);
           const uint32_t sc = mx_scale_code(max(mx[0], am[(q ^ 1) * 32 + col]));
           const int I = p.N / 2, nb = t.m * 2 + (q >> 1);   // block of 32 neurons
           if ((q & 1) == 0 && c0 + col < t.n && nb * 32 < I)
@@ -865,7 +863,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
             dst[0] = (uint16_t)e4m3x2(h[4 * b] * f.x, h[4 * b + 2] * f.x);
             dst[kProdCodePitch / 2] = (uint16_t)e4m3x2(h[4 * b + 1] * f.y, h[4 * b + 3] * f.y);
           }
-          named_sync(1, 128);
+          named_sync(bar, 128);
           const int row = et >> 2, n = t.m * 64 + 16 * (et & 3);
           if (c0 + row < t.n && n < I)
             *reinterpret_cast<uint4*>(p.codes + (size_t)(t.r0 + c0 + row) * I + n) =
@@ -874,7 +872,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       }
       tc::fence_before();
       __syncwarp();
-      if (lane == 0) tc::arrive_at(d_empty0 + 8 * buf);
+      tc::arrive_at(d_empty0 + 8 * buf);
     }
   }
   __syncwarp();
