@@ -12,7 +12,7 @@
 // One persistent pair of CTAs (a cluster of 2, cta_group::2) a pair of SMs
 // walks the tiles (token tile of a group, 256 weight rows), found from the
 // offsets on the device. Each CTA holds 128 of the weight rows and half of the
-// group's rows in shared memory, per stage of 256 K, and its 128 rows of the
+// group's rows in shared memory, per stage of 128 K, and its 128 rows of the
 // accumulator in tensor memory; the first CTA issues the MMAs of both. Roles:
 //   warp 0       weights by TMA
 //   warp 1       (first CTA) scales to tensor memory (tcgen05.cp) and the MMAs
@@ -21,7 +21,8 @@
 //   warps 4-7    epilogue, one per lane quarter of tensor memory, and
 //   warps 12-15  the same for every other chunk of 32 columns
 //   warps 8-11   scales, 512 K at a time, into shared memory in the order
-//                tcgen05.cp takes; and the group's rows where they are gathered
+//                tcgen05.cp takes
+//   warps 16-19  the group's rows where they are gathered
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
 // the next tile's MMAs.
 #pragma once
@@ -38,28 +39,27 @@ namespace moe {
 
 constexpr int kProdRows = 128;     // weight rows a CTA (half of the MMA's M)
 // Rows of a group a tile (N). Two accumulators of 192 columns and two batches
-// of four blocks' scales (12 columns a block) share the 512 columns of tensor
+// of four stages' scales (12 columns a stage) share the 512 columns of tensor
 // memory.
 constexpr int kProdCols = 192;
-constexpr int kProdK = 128;        // K elements a block: one 128-byte swizzle row
-// Blocks a stage: the MMA warp spends some 250 cycles a stage on barriers and
-// loop, which two blocks share (STAGEFIG).
-constexpr int kProdBlocks = 2;
-constexpr int kProdStages = 3;
-constexpr int kProdSfBlocks = 4;   // blocks a batch of scales covers
-constexpr int kProdThreads = 512;
+constexpr int kProdK = 128;        // K elements a stage: one 128-byte swizzle row
+// A slot's way from the MMA's release through a copy from L2 back to the MMA
+// takes some 2000 cycles: six stages of one row each hide it better than three
+// of two (down projection of 32768 rows, E32 H7168 I2048: 317 and 329 us).
+constexpr int kProdStages = 6;
+constexpr int kProdSfStages = 4;   // stages a batch of scales covers
+constexpr int kProdThreads = 640;
 constexpr int kProdMaxE = 1024;
 constexpr int kProdABytes = kProdRows * kProdK;
 constexpr int kProdBBytes = kProdCols / 2 * kProdK;
-constexpr int kProdSfaBytes = 512;    // a block's weight scales of one CTA
-constexpr int kProdSfbBytes = 1024;   // a block's row scales (up to 256 rows)
-constexpr int kProdSfBytes = kProdSfBlocks * (kProdSfaBytes + kProdSfbBytes);
+constexpr int kProdSfaBytes = 512;    // a stage's weight scales of one CTA
+constexpr int kProdSfbBytes = 1024;   // a stage's row scales (up to 256 rows)
+constexpr int kProdSfBytes = kProdSfStages * (kProdSfaBytes + kProdSfbBytes);
 // tensor-memory columns
 constexpr uint32_t kProdTmemCols = 512;
 constexpr uint32_t kProdSfCol = 2 * kProdCols;
-constexpr uint32_t kProdSfCols = 12;   // a block's: 4 of the weights, 8 of the rows
-static_assert(2 * kProdCols + 2 * kProdSfBlocks * kProdSfCols <= kProdTmemCols, "tensor memory");
-static_assert(kProdSfBlocks % kProdBlocks == 0, "a batch of scales covers whole stages");
+constexpr uint32_t kProdSfCols = 12;   // a stage's: 4 of the weights, 8 of the rows
+static_assert(2 * kProdCols + 2 * kProdSfStages * kProdSfCols <= kProdTmemCols, "tensor memory");
 static_assert(kProdCols % 32 == 0 && kProdCols <= 256, "token tile");
 // epilogue staging, two in turn for each of its two groups of four warps: a
 // chunk of 32 columns as rows of 128 bf16 (16-byte pieces swizzled by the row),
@@ -88,8 +88,8 @@ struct ProductParams {
 
 struct ProductSmem {
   static constexpr int a = 0;
-  static constexpr int b = a + kProdStages * kProdBlocks * kProdABytes;
-  static constexpr int sf = b + kProdStages * kProdBlocks * kProdBBytes;         // 2 batches
+  static constexpr int b = a + kProdStages * kProdABytes;
+  static constexpr int sf = b + kProdStages * kProdBBytes;         // 2 batches
   static constexpr int out = sf + 2 * kProdSfBytes;                // [2][2] chunks
   static constexpr int amax = out + 4 * kProdStageOut;             // [2][2][4][32] words
   static constexpr int inv = amax + 2 * 2 * 4 * 32 * 4;            // [2][4][32] floats
@@ -257,7 +257,7 @@ __device__ __forceinline__ void stm4_trans(uint32_t addr, uint32_t a, uint32_t b
 
 // ---------------------------------------------------------------------------
 // moe_product_lay_scales: the weights' scales in the order tcgen05.cp takes
-// them, once per handle: for (expert, 128-row tile, block) 512 bytes, lane l's
+// them, once per handle: for (expert, 128-row tile, stage) 512 bytes, lane l's
 // 16 holding four scale bytes of each of the MMA rows l, l + 32, l + 64,
 // l + 96. Places past N or K get 1 (their codes arrive as zeros).
 // ---------------------------------------------------------------------------
@@ -297,11 +297,22 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
 // moe_product_tiles
 // ---------------------------------------------------------------------------
 
+// One look at a barrier's phase: without a time the instruction returns after
+// the hardware's own short wait, with one it may sleep that long.
+__device__ __forceinline__ bool prod_look(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
 __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(done)
       : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
@@ -312,7 +323,7 @@ __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
 // marks the CTA dead (every role winds down).
 __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                           volatile int* dead) {
-  if (__all_sync(kFull, prod_poll(bar, parity))) return true;
+  if (__all_sync(kFull, prod_look(bar, parity))) return true;
 #pragma unroll 1
   for (uint32_t it = 0; it < kMbarPolls; ++it) {
     if (__any_sync(kFull, *dead)) return false;
@@ -391,7 +402,7 @@ struct ProductWalk {
   }
 };
 
-// A batch's scale bytes (16, four blocks) of one row from block kb on; bytes
+// A batch's scale bytes (16, four stages) of one row from stage kb on; bytes
 // past the row's end read as 127.
 __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int ks, int vec) {
   if (vec == 16) return *reinterpret_cast<const uint4*>(row + kb * 4);
@@ -412,35 +423,37 @@ __device__ __forceinline__ uint4 load_row_scales(const uint8_t* row, int kb, int
 }
 
 // What a thread of the scale warps holds of a tile: the two rows (r and
-// r + 128 of the tile) whose scales it brings, and with gathered rows the
-// rows of this CTA's half that it copies 16 bytes a block of. load() only
-// issues the loads of gathered rows; settle() uses them, a tile later.
-struct ProductRows {
-  int scale_row[2];
-  int copy_row[kProdCols / 32];
+// r + 128 of the tile) whose scales it brings. load() only issues the loads of
+// gathered rows; settle() uses them, a tile later.
+struct ScaleRows {
+  int row[2];
   ProductTile t;
-  __device__ __forceinline__ void load(const ProductParams& p, const ProductTile& tile, int rank,
-                                       int r) {
+  __device__ __forceinline__ void load(const ProductParams& p, const ProductTile& tile, int r) {
     t = tile;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      scale_row[h] = t.r0 + min(r + 128 * h, t.n - 1);
-      if (p.rows) scale_row[h] = p.rows[scale_row[h]];
-    }
-    if (p.rows) {
-      const int half = t.half();
-#pragma unroll
-      for (int i = 0; i < kProdCols / 32; ++i)
-        if (16 * i < half)
-          copy_row[i] = p.rows[t.r0 + min(rank * half + (r >> 3) + 16 * i, t.n - 1)];
+      row[h] = t.r0 + min(r + 128 * h, t.n - 1);
+      if (p.rows) row[h] = p.rows[row[h]];
     }
   }
   __device__ __forceinline__ void settle(const ProductParams& p) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) scale_row[h] = min(max(scale_row[h], 0), p.A - 1);
-    if (p.rows) {
+    for (int h = 0; h < 2; ++h) row[h] = min(max(row[h], 0), p.A - 1);
+  }
+};
+
+// What a thread of the copying warps holds of a tile: the gathered rows
+// (r / 8 + 16 c of this CTA's half) of which it copies 16 bytes a stage.
+struct CopyRows {
+  int row[kProdCols / 32];
+  int half;
+  __device__ __forceinline__ void load(const ProductParams& p, const ProductTile& t, int rank,
+                                       int r) {
+    half = t.half();
 #pragma unroll
-      for (int i = 0; i < kProdCols / 32; ++i) copy_row[i] = min(max(copy_row[i], 0), p.A - 1);
+    for (int c = 0; c < kProdCols / 32; ++c) {
+      row[c] = 0;
+      if (16 * c < half) row[c] = p.rows[t.r0 + min(rank * half + (r >> 3) + 16 * c, t.n - 1)];
     }
   }
 };
@@ -535,23 +548,21 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     bool ok = true;
     for (; ok && walk.valid(); walk.next()) {
       const ProductTile t = walk.tile();
-      const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);   // a block
+      const uint32_t bytes = 2 * p.w_bytes + (p.rows ? 0 : t.cols() * kProdK);
       // the groups of 16 neurons of all experts' gate and up rows in one row
       const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
-      for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
-        const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
+      for (int kb = 0; kb < nk; ++kb, ++g) {
+        const int s = rg.slot;
         if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
-        uint8_t* dst = smem + L::a + s * kProdBlocks * kProdABytes;
-        if (rank == 0) tc::expect(&full[s], nb * bytes);
-        for (int b = 0; b < nb; ++b, dst += kProdABytes) {
-          if (SILU)
-            tc::tma2_load_5d(dst, &p.tm_w, (kb + b) * kProdK, 0, 0, 0, grp, full0 + 8 * s);
-          else
-            tc::tma2_load_3d(dst, &p.tm_w, (kb + b) * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
-        }
+        uint8_t* dst = smem + L::a + s * kProdABytes;
+        if (rank == 0) tc::expect(&full[s], bytes);
+        if (SILU)
+          tc::tma2_load_5d(dst, &p.tm_w, kb * kProdK, 0, 0, 0, grp, full0 + 8 * s);
+        else
+          tc::tma2_load_3d(dst, &p.tm_w, kb * kProdK, t.m * kProdRows, t.e, full0 + 8 * s);
         rg.next();
       }
     }
@@ -577,37 +588,30 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kProdCols;
-        for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks) {
-          const int ns = min(kProdSfBlocks, nk - k0);
+        for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages) {
+          const int ns = min(kProdSfStages, nk - k0);
           ok = prod_wait(&sf_full[rs.slot], rs.phase, p.err, dead);
           if (!ok) break;
-          const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfBlocks * kProdSfCols;
+          const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfStages * kProdSfCols;
           const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
           for (int j = 0; j < ns; ++j) {
             const uint32_t c = sfc + j * kProdSfCols;
-            const uint32_t sb = sfs + kProdSfBlocks * kProdSfaBytes + j * kProdSfbBytes;
+            const uint32_t sb = sfs + kProdSfStages * kProdSfaBytes + j * kProdSfbBytes;
             tc::cp_scales(c, sfs + j * kProdSfaBytes);
             tc::cp_scales(c + 4, sb);
             if (n > 128) tc::cp_scales(c + 8, sb + 512);
           }
-          for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
+          for (int j = 0; j < ns; ++j) {
             const int s = rg.slot;
             ok = prod_wait(&full[s], rg.phase, p.err, dead);
             if (!ok) break;
-            const uint64_t ad =
-                tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdBlocks * kProdABytes));
-            const uint64_t bd =
-                tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBlocks * kProdBBytes));
+            const uint64_t ad = tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdABytes));
+            const uint64_t bd = tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBBytes));
+            const uint32_t c = sfc + j * kProdSfCols;
 #pragma unroll
-            for (int b = 0; b < kProdBlocks; ++b) {
-              if (j0 + b >= ns) break;
-              const uint32_t c = sfc + (j0 + b) * kProdSfCols;
-#pragma unroll
-              for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
-                tc::mma_mx(d, ad + b * (kProdABytes >> 4) + 2 * q,
-                           bd + b * (kProdBBytes >> 4) + 2 * q, idesc | tc::mx_scale_id(q), c,
-                           c + 4, k0 + j0 + b + q > 0 ? 1u : 0u);
-            }
+            for (int q = 0; q < kProdK / 32; ++q)   // 32 bytes further in the swizzled rows
+              tc::mma_mx(d, ad + 2 * q, bd + 2 * q, idesc | tc::mx_scale_id(q), c, c + 4,
+                         k0 + j + q > 0 ? 1u : 0u);
             tc::commit2(&empty[s]);
             rg.next();
           }
@@ -639,23 +643,20 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       for (; ok && walk.valid(); walk.next()) {
         const ProductTile t = walk.tile();
         const int half = t.half(), r0 = t.r0 + rank * half;
-        for (int kb = 0; kb < nk; kb += kProdBlocks, ++g) {
-          const int s = rg.slot, nb = min(kProdBlocks, nk - kb);
+        for (int kb = 0; kb < nk; ++kb, ++g) {
+          const int s = rg.slot;
           if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
             ok = false;
             break;
           }
-          uint8_t* dst = smem + L::b + s * kProdBlocks * kProdBBytes;
-          for (int b = 0; b < nb; ++b, dst += kProdBBytes) {
-            int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
+          uint8_t* dst = smem + L::b + s * kProdBBytes;
+          int r = 0;   // half = 64 + 32 + 16 where those bits are set (at most two boxes)
 #pragma unroll
-            for (int x = 2; x >= 0; --x)
-              if (half & (16 << x)) {
-                tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[x], (kb + b) * kProdK, r0 + r,
-                                 full0 + 8 * s);
-                r += 16 << x;
-              }
-          }
+          for (int b = 2; b >= 0; --b)
+            if (half & (16 << b)) {
+              tc::tma2_load_2d(dst + r * kProdK, &p.tm_a[b], kb * kProdK, r0 + r, full0 + 8 * s);
+              r += 16 << b;
+            }
           rg.next();
         }
       }
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       const uint32_t full0 = tc::cluster_addr(full, 0);
       bool ok = true;
       for (; ok && walk.valid(); walk.next())
-        for (int kb = 0; kb < nk; kb += kProdBlocks) {
+        for (int kb = 0; kb < nk; ++kb) {
           if (!prod_wait(&copied[rg.slot], rg.phase, p.err, dead)) {
             ok = false;
             break;
@@ -681,52 +682,82 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           rg.next();
         }
     }
+  } else if (warp >= 16) {
+    // --------------------------------------------------------- gathered rows
+    if (p.rows) {
+      const int r = threadIdx.x - 512;
+      // this thread's 16 bytes of each row: piece r % 8, where the 128-byte
+      // swizzle puts it
+      const int within = (r & 7) * 16;
+      const uint32_t dst =
+          smem_addr(smem + L::b) + (r >> 3) * kProdK + (((r & 7) ^ ((r >> 3) & 7)) << 4);
+      RingPos rg(kProdStages);
+      int g = 0;
+      CopyRows cur, nxt;
+      bool ok = true, more = walk.valid();
+      if (more) nxt.load(p, walk.tile(), rank, r);
+      while (ok && more) {
+        cur = nxt;
+        const uint8_t* src[kProdCols / 32];
+#pragma unroll
+        for (int c = 0; c < kProdCols / 32; ++c)
+          src[c] = p.a + (size_t)min(max(cur.row[c], 0), p.A - 1) * p.K;
+        walk.next();
+        more = walk.valid();
+        if (more) nxt.load(p, walk.tile(), rank, r);   // used a tile later
+        for (int kb = 0; kb < nk; ++kb, ++g) {
+          const int s = rg.slot, at = kb * kProdK + within;
+          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bytes = at < p.K ? 16u : 0u;
+          const int from = bytes ? at : 0;
+#pragma unroll
+          for (int c = 0; c < kProdCols / 32; ++c)
+            if (16 * c < cur.half)
+              tc::copy16(dst + s * kProdBBytes + c * 16 * kProdK, src[c] + from, bytes);
+          tc::copy_arrive(&copied[s]);
+          rg.next();
+        }
+      }
+      tc::copy_wait_all();
+    }
   } else if ((warp >> 2) == 2) {
-    // ---------------------------------------------- scales and gathered rows
+    // ---------------------------------------------------------------- scales
     const int r = threadIdx.x - 256;
     const int ks = p.K / 32;
     const uint32_t sf_full0 = tc::cluster_addr(sf_full, 0);
-    const bool gather = p.rows != nullptr;
-    // this thread's 16 bytes of the gathered rows (r / 8 + 16 i): piece r % 8,
-    // where the 128-byte swizzle puts it
-    const int within = (r & 7) * 16;
-    const uint32_t copy_dst =
-        smem_addr(smem + L::b) + (r >> 3) * kProdK + (((r & 7) ^ ((r >> 3) & 7)) << 4);
-    RingPos rg(kProdStages), rs(2);
-    int g = 0, gb = 0;
-    ProductRows cur, nxt;
+    RingPos rs(2);
+    int gb = 0;
+    ScaleRows cur, nxt;
     bool ok = true, more = walk.valid();
-    if (more) {
-      cur.load(p, walk.tile(), rank, r);
-      cur.settle(p);
-    }
     uint4 wsf = make_uint4(0, 0, 0, 0), rsf[2] = {wsf, wsf};
-    auto load_batch = [&](const ProductRows& pr, int k0) {
-      if (r < 32 * min(kProdSfBlocks, nk - k0))
+    auto load_batch = [&](const ScaleRows& sr, int k0) {
+      if (r < 32 * min(kProdSfStages, nk - k0))
         wsf = *reinterpret_cast<const uint4*>(
-            p.sfa + (((size_t)pr.t.e * 2 * pairs + pr.t.m) * nk + k0) * kProdSfaBytes + r * 16);
-      rsf[0] = load_row_scales(p.a_scales + (size_t)pr.scale_row[0] * ks, k0, ks, p.sf_vec);
-      if (pr.t.n > 128)
-        rsf[1] = load_row_scales(p.a_scales + (size_t)pr.scale_row[1] * ks, k0, ks, p.sf_vec);
+            p.sfa + (((size_t)sr.t.e * 2 * pairs + sr.t.m) * nk + k0) * kProdSfaBytes + r * 16);
+      rsf[0] = load_row_scales(p.a_scales + (size_t)sr.row[0] * ks, k0, ks, p.sf_vec);
+      if (sr.t.n > 128)
+        rsf[1] = load_row_scales(p.a_scales + (size_t)sr.row[1] * ks, k0, ks, p.sf_vec);
     };
-    if (more) load_batch(cur, 0);
+    if (more) {
+      cur.load(p, walk.tile(), r);
+      cur.settle(p);
+      load_batch(cur, 0);
+    }
     while (ok && more) {
       walk.next();
       more = walk.valid();
-      if (more) nxt.load(p, walk.tile(), rank, r);
-      const int half = cur.t.half();
-      const uint8_t* src[kProdCols / 32];
-#pragma unroll
-      for (int c = 0; c < kProdCols / 32; ++c)
-        src[c] = p.a + (gather && 16 * c < half ? (size_t)cur.copy_row[c] * p.K : 0);
-      for (int k0 = 0; ok && k0 < nk; k0 += kProdSfBlocks, ++gb) {
+      if (more) nxt.load(p, walk.tile(), r);
+      for (int k0 = 0; k0 < nk; k0 += kProdSfStages, ++gb) {
         if (gb >= 2 && !prod_wait(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
           ok = false;
           break;
         }
         uint8_t* sf = smem + L::sf + rs.slot * kProdSfBytes;
         *reinterpret_cast<uint4*>(sf + r * 16) = wsf;
-        uint32_t* dst = reinterpret_cast<uint32_t*>(sf + kProdSfBlocks * kProdSfaBytes) +
+        uint32_t* dst = reinterpret_cast<uint32_t*>(sf + kProdSfStages * kProdSfaBytes) +
                         (r & 31) * 4 + (r >> 5);
         dst[0] = rsf[0].x, dst[256] = rsf[0].y, dst[512] = rsf[0].z, dst[768] = rsf[0].w;
         if (cur.t.n > 128)
@@ -736,39 +767,15 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         tc::arrive_at(sf_full0 + 8 * rs.slot);
         rs.next();
         // the next batch's loads run while this one is used
-        if (k0 + kProdSfBlocks < nk)
-          load_batch(cur, k0 + kProdSfBlocks);
-        else if (more) {
+        if (k0 + kProdSfStages < nk) {
+          load_batch(cur, k0 + kProdSfStages);
+        } else if (more) {
           nxt.settle(p);
           load_batch(nxt, 0);
-        }
-        if (!gather) continue;
-        const int ns = min(kProdSfBlocks, nk - k0);
-        for (int j0 = 0; j0 < ns; j0 += kProdBlocks) {
-          const int s = rg.slot;
-          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int b = 0; b < kProdBlocks; ++b) {
-            if (j0 + b >= ns) break;
-            const int at = (k0 + j0 + b) * kProdK + within;
-            const uint32_t bytes = at < p.K ? 16u : 0u;
-            const int from = bytes ? at : 0;
-            const uint32_t to = copy_dst + (s * kProdBlocks + b) * kProdBBytes;
-#pragma unroll
-            for (int c = 0; c < kProdCols / 32; ++c)
-              if (16 * c < half) tc::copy16(to + c * 16 * kProdK, src[c] + from, bytes);
-          }
-          tc::copy_arrive(&copied[s]);
-          rg.next();
-          ++g;
         }
       }
       cur = nxt;
     }
-    if (gather) tc::copy_wait_all();
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, et = threadIdx.x & 127;
