@@ -289,6 +289,21 @@ def test_mxfp4_product(dev, silu, counts, N, K, gather):
     assert p.get_error() == 0
 
 
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("counts", [
+    # wide pieces one after another on the same SMs, whose accumulators overlap
+    # in tensor memory, with narrow ones and splits between them
+    [256, 255, 256, 250, 225, 256, 31, 256, 224, 300, 256, 1, 256],
+    # few tiles: the groups are cut finer
+    [200, 0, 190], [33, 64, 65]])
+def test_wide_and_cut_pieces(dev, counts, silu):
+    c = Products(dev, "mxfp8", 3200, 288, counts, 9, gather=silu)
+    a, s, off, rows = c.args()
+    p = c.handle(silu)
+    c.check(silu, p(a, s, off, rows))
+    assert p.get_error() == 0
+
+
 def test_every_e2m1_and_e4m3_code_through_one_hot_rows(dev):
     # a one-hot row picks one weight column: exact products, so exact bf16
     from sparse_expert_gemv_gb300 import GroupedProduct
@@ -486,3 +501,30 @@ def test_refusals_of_the_python_calls(dev):
         p(z(4, 64, t=u8), z(4, 2, t=u8), z(3, t=i32), out=z(4, 64, t=u8))
     empty = p(z(0, 64, t=u8), z(0, 2, t=u8), z(3, t=i32))
     assert empty[0].shape == (0, 32) and empty[1].shape == (0, 1)
+
+
+def test_example_block(dev, capsys):
+    """The example runs, and its block is its operators: the stream after it is
+    the sum of the norm's stream and the routed experts."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "prompt_block.py")
+    spec = importlib.util.spec_from_file_location("prompt_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    assert ex.main(["--tokens", "70", "--experts", "8", "--topk", "2", "--hidden", "256",
+                    "--intermediate", "128"]) > 0
+    assert "tokens a us" in capsys.readouterr().out
+    from sparse_expert_gemv_gb300 import add_rms_norm
+    layer = ex.random_layer(8, 2, 256, 128, "mxfp4", max_T=40)
+    x, res, nw = norm_case(40, 256, 20)
+    r = bf16(rng(21).standard_normal((8, 256)) / 16, dev)
+    block = ex.PromptBlock(layer, bf16(nw, dev), r)
+    n = add_rms_norm(bf16(x, dev), bf16(nw, dev), bf16(res, dev), mxfp8=True)
+    ids, w = layer.route((n.y @ r.T).float())
+    want = layer.prompt(n.codes, n.scales, ids, w, residual=n.sum)
+    assert torch.equal(block(bf16(x, dev), bf16(res, dev)), want)
+    # a stream of zeros before the block: the same without a residual
+    zeros = torch.zeros(40, 256, dtype=torch.bfloat16, device=dev)
+    assert torch.equal(block(bf16(x, dev), None), block(bf16(x, dev), zeros))
