@@ -1,15 +1,18 @@
 """Build libmoe_decode.so in-tree with nvcc for sm_103a (no cmake; the decode
 layer and the prompt operators are one translation unit each, compiled side by
-side).
+side), and with g++ the extension module _moe_torch.so, which passes torch
+tensors to the prompt operators.
 
     python -m sparse_expert_gemv_gb300.build
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +23,8 @@ OUT = os.path.join(HERE, "libmoe_decode.so")
 # caller-supplied buffer by moe_decode_layer_timeline); never loaded by the
 # package itself
 OUT_TIMELINE = os.path.join(HERE, "libmoe_decode_timeline.so")
+BINDING_SRC = os.path.join(HERE, "csrc", "moe_torch.cpp")
+BINDING_OUT = os.path.join(HERE, "_moe_torch.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -37,18 +42,46 @@ def command(out: str = OUT, extra=()) -> list[str]:
             f"-Xlinker", f"-rpath,{cuda_lib}", "--threads", "0", *extra, *SRCS, "-o", out]
 
 
+def binding_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
+    """Compile and link commands of the extension module (linked against the
+    library beside it)."""
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cxx = shutil.which("g++") or "c++"
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj,
+                f"-I{os.path.join(ROOT, 'include')}", f"-I{sysconfig.get_paths()['include']}",
+                f"-I{os.path.join(torch, 'include')}", f"-I{os.path.join(cuda, 'include')}"]
+    link = [cxx, "-shared", obj, "-o", out, f"-L{os.path.join(torch, 'lib')}", "-ltorch_python",
+            "-ltorch", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", f"-L{HERE}",
+            "-lmoe_decode", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
+def _finish(cmd: list[str], out: str, p: subprocess.Popen | None = None) -> str:
+    p = p or subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    text = p.communicate()[0]
+    if p.returncode != 0:
+        sys.stderr.write(text)
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed building {os.path.basename(out)}")
+    return text
+
+
 def build(verbose: bool = False, timeline: bool = False) -> str:
     out = OUT_TIMELINE if timeline else OUT
-    tmp = out + ".tmp"
+    tmp, obj, tmp_binding = out + ".tmp", BINDING_OUT[:-3] + ".o", BINDING_OUT + ".tmp"
     extra = (["-Xptxas", "-v"] if verbose else []) + (["-DMOE_TIMELINE"] if timeline else [])
-    cmd = command(tmp, extra)
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"nvcc failed building {os.path.basename(out)}")
+    compile_, link = binding_commands(obj, tmp_binding)
+    cxx = None if timeline else subprocess.Popen(compile_, stdout=subprocess.PIPE,
+                                                 stderr=subprocess.STDOUT, text=True)
+    text = _finish(command(tmp, extra), out)
     if verbose:
-        sys.stderr.write(r.stderr)
+        sys.stderr.write(text)
     os.replace(tmp, out)
+    if not timeline:
+        _finish(compile_, BINDING_OUT, cxx)
+        _finish(link, BINDING_OUT)
+        os.remove(obj)
+        os.replace(tmp_binding, BINDING_OUT)
     return out
 
 
