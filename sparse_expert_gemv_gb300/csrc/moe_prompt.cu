@@ -84,7 +84,8 @@ int group_cluster_limit() {
     return known[dev].load(std::memory_order_relaxed);
   int limit = 16;
   for (GroupKernel k : kGroupKernels) {
-    const size_t smem = moe::group_smem(moe::kGroupThreads / 32, moe::kProdMaxE);
+    const size_t smem = moe::group_smem(moe::kGroupThreads / 32, moe::kProdMaxE,
+                                        moe::kGroupThreads * moe::kGroupBatch);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(16);
     cfg.blockDim = dim3(moe::kGroupThreads);
@@ -215,9 +216,18 @@ moe_status_t moe_group(int32_t T, int32_t k, int32_t E, const int32_t* topk_ids,
   while (C < limit && S > 512 * C) C *= 2;
   const int warps = std::min(moe::kGroupThreads / 32, (S + 32 * C - 1) / (32 * C));
   const int per = ((S + C * warps - 1) / (C * warps) + 31) / 32 * 32;
-  const moe::GroupParams p{topk_ids, offsets, rows, slots, S, k, E, per};
+  // division by k: 2^(31 + l) / k rounded up, 2^l the power of two at or above
+  // k, is off by less than 2^-(l + 31) of a quotient, too little to reach the
+  // next whole number for any s <= 2^30
+  int l = 0;
+  while ((int64_t)1 << l < k) ++l;
+  const unsigned inverse = (unsigned)((((uint64_t)1 << (31 + l)) + k - 1) / k);
+  // from 2048 slots a CTA on, while a warp's range is one batch (131072 slots
+  // of 256 experts: 12.8 us staged, 14.9 stored directly)
+  const int staged = per <= 32 * moe::kGroupBatch && warps * per >= 2048 ? warps * per : 0;
+  const moe::GroupParams p{topk_ids, offsets, rows, slots, S, E, per, inverse, l, staged};
   return launch(kGroupKernels[E <= 128 ? 0 : E <= 256 ? 1 : 2], C, warps * 32,
-                moe::group_smem(warps, E), stream, C, p);
+                moe::group_smem(warps, E, staged), stream, C, p);
 }
 
 moe_status_t moe_combine(int32_t T, int32_t k, int32_t H, int32_t R, const uint16_t* y,

@@ -194,12 +194,20 @@ struct GroupParams {
   int32_t* offsets;
   int32_t* rows;
   int32_t* slots;
-  int S, k, E;
+  int S, E;
   int per_warp;   // slots a warp takes, a multiple of 32
+  // s / k = (2 s * k_inverse) >> (32 + k_shift) for s <= 2^30
+  unsigned k_inverse;
+  int k_shift;
+  // slots of a CTA that go to `rows` through shared memory, in the order of
+  // their places there, so that a warp's stores are a few runs and not 32
+  // single words; 0 to store directly
+  int staged;
 };
 
-__host__ __device__ constexpr size_t group_smem(int warps, int E) {
-  return (size_t)(warps + 2) * E * sizeof(int);
+// `staged`: places of the CTA's slots before they are written (see below).
+__host__ __device__ constexpr size_t group_smem(int warps, int E, int staged) {
+  return (size_t)((warps + 3) * E + 1 + 2 * staged) * sizeof(int);
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -239,7 +247,9 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
   const int E = p.E, C = gridDim.x, rank = blockIdx.x;
   int* mine = sm_group;              // [E] this CTA's slots of each expert
   int* start = mine + E;             // [E] all CTAs' slots, then the groups' starts
-  int* tab = start + E;              // [warps][E] each warp's count, then its next place
+  int* local = start + E;            // [E] starts of the experts among this CTA's slots
+  int* tab = local + E;              // [warps][E] each warp's count, then its next place
+  int* stage = tab + warps * E + 1;  // [staged] tokens, then [staged] places
   int* cnt = tab + warp * E;
   pdl_wait();
   for (int e = lane; e < E; e += 32) cnt[e] = 0;
@@ -247,24 +257,29 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
   const long long w0 = (long long)(rank * warps + warp) * p.per_warp;
   const int lo = (int)min((long long)p.S, w0), hi = (int)min((long long)p.S, w0 + p.per_warp);
   const unsigned below = (1u << lane) - 1u;
+  // A warp's range is one batch up to kGroupBatch * 32 slots: its ids and
+  // ranks then stay in registers, else the ranks wait in `slots`.
+  const bool one = p.per_warp <= 32 * kGroupBatch;
+  int id[kGroupBatch], rank_in[kGroupBatch];
   for (int s0 = lo; s0 < hi; s0 += 32 * kGroupBatch) {
-    int id[kGroupBatch];   // a batch of loads in flight at once
 #pragma unroll
     for (int i = 0; i < kGroupBatch; ++i) {
       const int s = s0 + 32 * i + lane;
       id[i] = s < hi ? p.ids[s] : -1;
+      if (id[i] >= E) id[i] = -1;
     }
 #pragma unroll
     for (int i = 0; i < kGroupBatch; ++i) {
       if (s0 + 32 * i >= hi) break;
       const int s = s0 + 32 * i + lane, e = id[i];
-      const bool in = e >= 0 && e < E;
+      const bool in = e >= 0;
       const unsigned same = same_value<BITS>(e, in);
       const int before = in ? cnt[e] : 0;
       __syncwarp();
       if (in && (same & below) == 0u) cnt[e] = before + __popc(same);
       __syncwarp();
-      if (s < hi) p.slots[s] = before + __popc(same & below);
+      rank_in[i] = before + __popc(same & below);
+      if (!one && s < hi) p.slots[s] = rank_in[i];
     }
   }
   __syncthreads();
@@ -288,53 +303,71 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
       total += v;
     }
     start[e] = total;
-#pragma unroll 8
-    for (int w = 0; w < warps; ++w) tab[w * E + e] += before;
+    local[e] = before;
   }
   // no CTA leaves (or changes `mine`) while another still reads it
   if (C > 1) cluster_sync(); else __syncthreads();
-  if (warp == 0) {   // exclusive prefix over the experts
-    int carry = 0;
+  // exclusive prefixes over the experts: where a group starts (then where this
+  // CTA's part of it does), and where an expert starts among this CTA's slots
+  if (warp == 0) {
+    int carry = 0, mine_carry = 0;
     for (int e0 = 0; e0 < E; e0 += 32) {
-      const int v = e0 + lane < E ? start[e0 + lane] : 0;
-      int incl = v;
+      const int e = e0 + lane;
+      const int v = e < E ? start[e] : 0, m = e < E ? mine[e] : 0;
+      int incl = v, mi = m;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += u;
+        const int u = __shfl_up_sync(kFull, incl, o), w = __shfl_up_sync(kFull, mi, o);
+        if (lane >= o) incl += u, mi += w;
       }
-      if (e0 + lane < E) {
-        start[e0 + lane] = carry + incl - v;
-        if (rank == 0) p.offsets[e0 + lane] = carry + incl - v;
+      if (e < E) {
+        start[e] = carry + incl - v + local[e];
+        if (rank == 0) p.offsets[e] = carry + incl - v;
+        local[e] = mine_carry + mi - m;
       }
       carry += __shfl_sync(kFull, incl, 31);
+      mine_carry += __shfl_sync(kFull, mi, 31);
     }
     if (lane == 0) {
-      mine[0] = carry;   // rows in all groups
+      stage[-1] = carry;   // rows in all groups
       if (rank == 0) p.offsets[E] = carry;
     }
+    mine[0] = mine_carry;  // this CTA's slots that join a group
   }
   __syncthreads();
   for (int s0 = lo; s0 < hi; s0 += 32 * kGroupBatch) {
-    int id[kGroupBatch], rank_in[kGroupBatch];
+    if (!one) {
 #pragma unroll
-    for (int i = 0; i < kGroupBatch; ++i) {
-      const int s = s0 + 32 * i + lane;
-      id[i] = s < hi ? p.ids[s] : -1;
-      rank_in[i] = s < hi ? p.slots[s] : 0;
+      for (int i = 0; i < kGroupBatch; ++i) {
+        const int s = s0 + 32 * i + lane;
+        id[i] = s < hi ? p.ids[s] : -1;
+        if (id[i] >= E) id[i] = -1;
+        rank_in[i] = s < hi ? p.slots[s] : 0;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kGroupBatch; ++i) {
       const int s = s0 + 32 * i + lane, e = id[i];
-      if (s >= hi) continue;
-      const bool in = e >= 0 && e < E;
-      const int q = in ? start[e] + cnt[e] + rank_in[i] : -1;
+      if (s >= hi) break;
+      const int in_cta = e >= 0 ? cnt[e] + rank_in[i] : 0;
+      const int q = e >= 0 ? start[e] + in_cta : -1;
       p.slots[s] = q;
-      if (in) p.rows[q] = s / p.k;
+      if (e < 0) continue;
+      const int token = (int)(__umulhi(2u * s, p.k_inverse) >> p.k_shift);
+      if (p.staged) {
+        stage[local[e] + in_cta] = token;
+        stage[p.staged + local[e] + in_cta] = q;
+      } else {
+        p.rows[q] = token;
+      }
     }
   }
+  if (p.staged) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < mine[0]; i += blockDim.x) p.rows[stage[p.staged + i]] = stage[i];
+  }
   // rows past the last group
-  const int used = mine[0];
+  const int used = stage[-1];
   for (long long r = (long long)used + rank * blockDim.x + threadIdx.x; r < p.S;
        r += (long long)C * blockDim.x)
     p.rows[r] = -1;

@@ -178,7 +178,7 @@ def test_norm_tiny_and_huge_scales(dev):
 @pytest.mark.parametrize("T,k,E,bad", [
     (1, 1, 1, 0.0), (1, 8, 128, 0.0), (3, 2, 5, 0.3), (32, 8, 128, 0.0), (33, 4, 60, 0.2),
     (200, 8, 1024, 0.1), (257, 8, 8, 0.0), (1000, 6, 160, 0.05), (5000, 8, 256, 0.0),
-    (40, 3, 7, 1.0)])
+    (40, 3, 7, 1.0), (20000, 6, 300, 0.1), (40000, 8, 128, 0.02)])
 def test_group(dev, T, k, E, bad):
     from sparse_expert_gemv_gb300 import group_by_expert
     r = rng(5, T, k, E)
