@@ -116,7 +116,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
 }
-// One arrival on an mbarrier of the cluster.
+// One arrival on an mbarrier of the cluster. What it announces is read by this
+// SM's own tensor cores (scales and rows in this CTA's shared memory, columns of
+// its tensor memory) and made ready for them by a proxy or tcgen05 fence before
+// it, so it orders no data between the CTAs; a release at cluster scope waits
+// for every store of the warp and cost some 500 cycles an arrival.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("{\n\t" MOE_ELECT "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
                : "memory");
@@ -374,7 +378,8 @@ struct ProductWalk {
   int q, m, dq, dm;                 // token tile and pair of weight tiles, and a step's
   int e;                            // expert of q, once found
   __device__ __forceinline__ ProductWalk(const int* off_, const int* tiles_,
-                                         const uint16_t* piece_, int rank_, int pairs_, int E_, int first, int step)
+                                         const uint16_t* piece_, int rank_, int pairs_, int E_,
+                                         int first, int step)
       : off(off_), tiles(tiles_), piece(piece_), rank(rank_), pairs(pairs_), E(E_),
         ntok(uniform(tiles_[E_])), q(first / pairs_), m(first % pairs_), dq(step / pairs_),
         dm(step % pairs_), e(0) {}

@@ -175,8 +175,10 @@ class MoEDecode:
         scales uint8 [T, H/32], e.g. add_rms_norm's): grouping, both products
         on the tensor cores with h in MXFP8, and the weighted sum with
         `residual` (bf16 [T, H], optional) added; bf16 [T, H]. T is not bound
-        by max_T. The first call lays out the weights' scales for the two
-        products (see GroupedProduct), which the layer then keeps."""
+        by max_T; an id outside [0, E) adds nothing. The first call lays out
+        the weights' scales for the two products (see GroupedProduct), which
+        the layer then keeps: make it before a stream is captured. With MXFP4
+        weights H and I must be multiples of 128."""
         if stream is not None:      # the intermediates belong to that stream too
             with torch.cuda.stream(stream):
                 return self.prompt(codes, scales, ids, w, residual, out)
