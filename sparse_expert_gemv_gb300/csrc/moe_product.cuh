@@ -511,17 +511,18 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   }
   if (warp == 1) tc::tmem_alloc2(tmem_slot, kProdTmemCols);
   pdl_wait();
-  if (warp == 2) {   // groups and the token tiles before each
+  for (int e = threadIdx.x; e <= p.E; e += kProdThreads)
+    off[e] = min(max(p.offsets[e], 0), p.R);
+  __syncthreads();
+  if (warp == 2) {   // the token tiles before each group
     int carry = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int lo = 0, nt = 0;
+      int nt = 0;
       if (e < p.E) {
-        lo = min(max(p.offsets[e], 0), p.R);
-        const int hi = min(max(p.offsets[e + 1], 0), p.R);
-        nt = hi > lo ? (hi - lo + kProdCols - 1) / kProdCols : 0;
-        off[e] = lo;
-        piece[e] = (uint16_t)(nt ? ((hi - lo + nt - 1) / nt + 31) & ~31 : 0);
+        const int c = off[e + 1] - off[e];
+        nt = c > 0 ? (c + kProdCols - 1) / kProdCols : 0;
+        piece[e] = (uint16_t)(nt ? ((c + nt - 1) / nt + 31) & ~31 : 0);
       }
       int incl = nt;
 #pragma unroll
@@ -532,10 +533,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       if (e < p.E) tiles[e] = carry + incl - nt;
       carry += __shfl_sync(kFull, incl, 31);
     }
-    if (lane == 0) {
-      off[p.E] = min(max(p.offsets[p.E], 0), p.R);
-      tiles[p.E] = carry;
-    }
+    if (lane == 0) tiles[p.E] = carry;
   }
   tc::fence_before();
   __syncthreads();

@@ -55,10 +55,12 @@ moe_status_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, siz
 template <int V>
 moe_status_t norm_launch(const moe::NormParams& p, int T, void* stream) {
   const int nv = p.H / V;
-  // Up to 512 threads a row with one vector each, then two, then up to 1024
-  // threads with as many as the row needs (8191 rows of 7168: 448 threads x 2
-  // 68 us, 224 x 4 78 us, 896 x 1 91 us).
-  const int threads = nv <= 1024 ? ((nv + (nv > 512)) / (nv > 512 ? 2 : 1) + 31) / 32 * 32 : 1024;
+  // One vector a thread while few rows are under way, two from 2048 rows or 512
+  // vectors on (smaller blocks, more rows an SM), up to four on 1024 threads
+  // (us with one and with two: 1 row of 2048 1.9 / 2.3, 1024 rows 3.3 / 3.5, 4096
+  // rows of 4096 20.1 / 16.7, 16384 of 2048 39.7 / 37.2, MXFP8 rows out).
+  const bool two = nv > 512 || (nv > 128 && T >= 2048);
+  const int threads = nv > 1024 ? 1024 : ((two ? (nv + 1) / 2 : nv) + 31) / 32 * 32;
   const int per = (nv + threads - 1) / threads;
   if (per <= 1) return launch(moe::moe_add_rms_norm_rows<V, 1>, T, threads, 0, stream, 1, p);
   if (per <= 2) return launch(moe::moe_add_rms_norm_rows<V, 2>, T, threads, 0, stream, 1, p);
