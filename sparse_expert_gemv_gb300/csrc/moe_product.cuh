@@ -511,6 +511,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   }
   if (warp == 1) tc::tmem_alloc2(tmem_slot, kProdTmemCols);
   pdl_wait();
+  pdl_trigger();   // the next kernel's prologue may run beside this one
   for (int e = threadIdx.x; e <= p.E; e += kProdThreads)
     off[e] = min(max(p.offsets[e], 0), p.R);
   __syncthreads();

@@ -200,12 +200,14 @@ __global__ void __launch_bounds__(1024) moe_add_rms_norm_rows(const NormParams p
 
 // ---------------------------------------------------------------------------
 // moe_group_slots: stable counting sort of S = T * k slots by expert, one
-// cluster of C CTAs (1 to 16). The slots are cut into one
-// contiguous range per warp of the cluster. Each warp counts its range into a
-// table of its own (lanes of equal id find one another by ballots over the id's
-// bits, so no atomics and a fixed order) and notes each slot's rank there in `slots`; the
-// CTAs exchange their totals through distributed shared memory; each slot's
-// place is then its expert's start, what lower warps hold of it, and its rank.
+// cluster of C CTAs (1 to 16). The slots are cut into one contiguous range per
+// warp of the cluster. Each warp counts its range into a table of its own
+// (lanes of equal id find one another by ballots over the id's bits, so no
+// atomics and a fixed order) and keeps each slot's rank there; the CTAs
+// exchange their totals through distributed shared memory; each slot's place is
+// then its expert's start, what lower warps hold of it, and its rank. Bound by
+// latency up to some 8192 slots (2.7 us for 256 of them, 5.5 for 8192), by the
+// ballots and counts of 16 SMs beyond (12.9 for 131072).
 // ---------------------------------------------------------------------------
 constexpr int kGroupThreads = 1024;
 constexpr int kGroupBatch = 8;
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
   int* stage = tab + warps * E + 1;  // [staged] tokens, then [staged] places
   int* cnt = tab + warp * E;
   pdl_wait();
+  pdl_trigger();   // the next kernel's prologue may run beside this one
   for (int e = lane; e < E; e += 32) cnt[e] = 0;
   __syncwarp();
   const long long w0 = (long long)(rank * warps + warp) * p.per_warp;
@@ -399,7 +402,8 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
 // and adds that token's rows in slot order (no atomics, a fixed order). Bound
 // by HBM: eight rows' loads in flight, as loads of what is read once (8192
 // tokens of 8 rows of 2048: 58 us row by row, 49.9 with eight in flight, 46.0
-// with read-once loads, 7.3 TB/s).
+// with read-once loads, 7.3 TB/s). It lets no dependent launch start early: the
+// next one's CTAs would take this one's places (49.9 us then).
 // ---------------------------------------------------------------------------
 struct CombineParams {
   const uint16_t* y;
