@@ -25,6 +25,13 @@
 //   warps 16-19  the group's rows where they are gathered
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
 // the next tile's MMAs.
+//
+// What bounds it, measured (us a call, E=128 k=8 H=2048 I=768 unless noted): few
+// rows an expert, HBM (gate/up of 8 tokens 31, 5.4 TB/s; of 256 tokens 68, 6.1
+// TB/s); hundreds of rows an expert, the board's power limit, which takes the
+// clock from 2070 MHz to 1820 (gate/up of 2048 tokens, MXFP4, 52 to 55), 1520
+// (4096 tokens 97 to 108) and 1275 (down of 32768 rows, E=32 H=7168 I=2048, 318
+// to 367, 3.0 PFLOP/s): shorter figures from runs too short to reach the limit.
 #pragma once
 
 #include <cuda.h>
