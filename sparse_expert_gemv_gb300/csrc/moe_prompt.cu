@@ -68,6 +68,17 @@ moe_status_t norm_launch(const moe::NormParams& p, int T, void* stream) {
   return launch(moe::moe_add_rms_norm_rows<1, 16>, T, threads, 0, stream, 1, p);
 }
 
+// ---- combine -----------------------------------------------------------------
+
+template <int V>
+moe_status_t combine_launch(const moe::CombineParams& p, unsigned grid, unsigned threads,
+                            void* stream) {
+  if (p.k == 1) return launch(moe::moe_combine_rows<V, 1>, grid, threads, 0, stream, 1, p);
+  if (p.k == 2) return launch(moe::moe_combine_rows<V, 2>, grid, threads, 0, stream, 1, p);
+  if (p.k <= 4) return launch(moe::moe_combine_rows<V, 4>, grid, threads, 0, stream, 1, p);
+  return launch(moe::moe_combine_rows<V, moe::kCombineBatch>, grid, threads, 0, stream, 1, p);
+}
+
 // ---- group -------------------------------------------------------------------
 
 using GroupKernel = void (*)(const moe::GroupParams);
@@ -246,9 +257,10 @@ moe_status_t moe_combine(int32_t T, int32_t k, int32_t H, int32_t R, const uint1
   const int nb = (nv + moe::kCombineThreads - 1) / moe::kCombineThreads;
   if ((int64_t)T * nb > 0x7fffffff) return MOE_ERR_UNSUPPORTED_SHAPE;
   const moe::CombineParams p{y, slots, w, residual, out, k, H, R, nb};
-  const unsigned threads = nb > 1 ? moe::kCombineThreads : (nv + 31) / 32 * 32;
-  return vec ? launch(moe::moe_combine_rows<8>, T * nb, threads, 0, stream, 1, p)
-             : launch(moe::moe_combine_rows<1>, T * nb, threads, 0, stream, 1, p);
+  // a token's vectors in equal parts over its CTAs
+  const unsigned threads = ((nv + nb - 1) / nb + 31) / 32 * 32;
+  return vec ? combine_launch<8>(p, T * nb, threads, stream)
+             : combine_launch<1>(p, T * nb, threads, stream);
 }
 
 moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* w,

@@ -403,7 +403,10 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
 // by HBM: eight rows' loads in flight, as loads of what is read once (8192
 // tokens of 8 rows of 2048: 58 us row by row, 49.9 with eight in flight, 46.0
 // with read-once loads, 7.3 TB/s). It lets no dependent launch start early: the
-// next one's CTAs would take this one's places (49.9 us then).
+// next one's CTAs would take this one's places (49.9 us then). With few rows a
+// token the writes and the residual are most of the traffic: 16384 tokens of one
+// row of 2592 50 to 57 us, 5 TB/s (83 with registers for eight rows and an uneven
+// second CTA); two or four tokens a thread are no faster (50, 53).
 // ---------------------------------------------------------------------------
 struct CombineParams {
   const uint16_t* y;
@@ -418,7 +421,10 @@ struct CombineParams {
 constexpr int kCombineThreads = 256;
 constexpr int kCombineBatch = 8;
 
-template <int V>
+// B: rows in flight at once, the power of two at or above k up to
+// kCombineBatch: few rows then take few registers (64 at B = 8, 40 at 1) and
+// more threads share an SM.
+template <int V, int B>
 __global__ void __launch_bounds__(kCombineThreads) moe_combine_rows(const CombineParams p) {
   const int t = blockIdx.x / p.nb;
   const int v = (blockIdx.x % p.nb) * blockDim.x + threadIdx.x;
@@ -432,22 +438,22 @@ __global__ void __launch_bounds__(kCombineThreads) moe_combine_rows(const Combin
   const size_t at = (size_t)t * p.H + (size_t)v * V;
   typename RowVec<V>::Raw res{};
   if (p.residual) res = RowVec<V>::once(p.residual + at);
-  for (int j0 = 0; j0 < p.k; j0 += kCombineBatch) {
+  for (int j0 = 0; j0 < p.k; j0 += B) {
     // a batch of rows in flight at once; absent ones weigh nothing
-    int q[kCombineBatch];
-    float wj[kCombineBatch];
-    typename RowVec<V>::Raw y[kCombineBatch];
+    int q[B];
+    float wj[B];
+    typename RowVec<V>::Raw y[B];
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j) {
+    for (int j = 0; j < B; ++j) {
       q[j] = j0 + j < p.k ? slots[j0 + j] : -1;
       if (q[j] >= p.R) q[j] = -1;
       wj[j] = q[j] >= 0 ? w[j0 + j] : 0.f;
     }
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
+    for (int j = 0; j < B; ++j)
       if (q[j] >= 0) y[j] = RowVec<V>::once(p.y + (size_t)q[j] * p.H + (size_t)v * V);
 #pragma unroll
-    for (int j = 0; j < kCombineBatch; ++j)
+    for (int j = 0; j < B; ++j)
       if (q[j] >= 0) {
         float f[V];
         RowVec<V>::values(y[j], f);
