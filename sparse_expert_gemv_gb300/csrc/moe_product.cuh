@@ -844,7 +844,12 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
             const float gate = __uint_as_float(lo[x]), up = __uint_as_float(hi[x]);
-            h[x] = __fdividef(gate, 1.0f + __expf(-gate)) * up;
+            // SiLU with e = exp(-|gate|) <= 1: nothing overflows, and the divisor
+            // stays where the short division is good to two units. The short
+            // exp is off by 2 + 1.2 |gate| units, far below the 2^-4 that E4M3
+            // keeps; expf costs 1.5% at 2048 tokens, exact division 7%.
+            const float e = __expf(-fabsf(gate));
+            h[x] = __fdividef(gate < 0.f ? gate * e : gate, 1.0f + e) * up;
           }
 #pragma unroll
           for (int b = 0; b < 8; ++b) {

@@ -324,6 +324,27 @@ def test_every_e2m1_and_e4m3_code_through_one_hot_rows(dev):
     assert np.array_equal(tensor_to_f64(y), oracle.dequantize_mxfp4(w4[0], sw[0]).T)
 
 
+def test_silu_of_far_gates_under_large_ups(dev):
+    # one-hot weights: every neuron's gate and up are a row's two values, exactly.
+    # exp(-gate) overflows or comes near it while the product is a normal number.
+    from sparse_expert_gemv_gb300 import GroupedProduct
+    gates = np.array([-72.0, -80.0, -88.0, -96.0, -104.0, 72.0, 104.0, -0.0])
+    K, N, R = 64, 64, gates.size
+    w = np.zeros((1, N, K), dtype=np.uint8)
+    w[0, :32, 0] = w[0, 32:, 32] = 0x38                  # E4M3 1.0
+    a, s = np.zeros((R, K), dtype=np.uint8), np.full((R, 2), 127, dtype=np.uint8)
+    unit = [int(np.flatnonzero(oracle.E4M3 == g)[0]) for g in gates]
+    a[:, 0], a[:, 32], s[:, 1] = unit, 0x38, 127 + 40    # ups 2^40
+    p = GroupedProduct(on(w, dev), on(np.full((1, N, 2), 127, dtype=np.uint8), dev), silu_mul=True)
+    got = p(on(a, dev), on(s, dev), on(np.array([0, R], dtype=np.int32), dev))
+    Y = np.concatenate([np.repeat(gates[:, None], 32, 1), np.full((R, 32), 2.0 ** 40)], 1)
+    h = ref.silu_mul(Y)
+    g = np.abs(Y[:, :32])
+    # the usual error and, where exp or its product is subnormal, a unit of each
+    delta = (2.0 ** -20 + 2.0 ** -23 * (2 + g)) * np.abs(h) + 2.0 ** 40 * 2.0 ** -149 * (g + 3)
+    assert_mxfp8(got[0], got[1], h, delta, "h")
+
+
 def test_rows_outside_the_groups_stay_as_they_are(dev):
     c = Products(dev, "mxfp8", 128, 256, [10, 0, 30], 4, lead=5, tail=50)
     # what lies outside the groups is poison: NaN codes and NaN scales
