@@ -123,14 +123,21 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
 }
-// One arrival on an mbarrier of the cluster. What it announces is read by this
-// SM's own tensor cores (scales and rows in this CTA's shared memory, columns of
-// its tensor memory) and made ready for them by a proxy or tcgen05 fence before
-// it, so it orders no data between the CTAs; a release at cluster scope waits
-// for every store of the warp and cost some 500 cycles an arrival.
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("{\n\t" MOE_ELECT "@e mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
-               : "memory");
+// One arrival on an mbarrier of the first CTA, by this CTA or (`remote`) by the
+// other one. What a remote one announces, scales and rows in this CTA's shared
+// memory and columns of its tensor memory, is used by MMAs that the first CTA
+// issues, so it is a release at cluster scope, of shared memory alone: that fence
+// waits for no global load or store (gate/up of 4096 tokens 97 us, 264 with a
+// release of all memory; down projection of 32768 rows 312 and 454).
+__device__ __forceinline__ void arrive_at(uint32_t bar, bool remote) {
+  if (remote)
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t{\n\t" MOE_ELECT
+                 "@e mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+                 : "memory");
+  else
+    asm volatile("{\n\t" MOE_ELECT
+                 "@e mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar)
+                 : "memory");
 }
 // One arrival on this CTA's mbarrier that announces `bytes` of copies.
 __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes) {
@@ -308,37 +315,61 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
 // moe_product_tiles
 // ---------------------------------------------------------------------------
 
+// Whose arrivals a wait is for: kPair, an mbarrier on which the other CTA or the
+// MMAs of both arrive, acquired at cluster scope (1% of the gathered gate/up's
+// time), or kOwn, one of this CTA alone.
+enum class Arrivals { kOwn, kPair };
+
 // One look at a barrier's phase: without a time the instruction returns after
 // the hardware's own short wait, with one it may sleep that long.
+template <Arrivals A>
 __device__ __forceinline__ bool prod_look(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
+  if constexpr (A == Arrivals::kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+        "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], "
+        "%2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
   return done != 0;
 }
+template <Arrivals A>
 __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
   uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
-      : "memory");
+  if constexpr (A == Arrivals::kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], "
+        "%2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], "
+        "%2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kWaitSuspendNs)
+        : "memory");
   return done != 0;
 }
 // A whole warp's bounded wait on a phase of this CTA's mbarrier; a timeout
 // marks the CTA dead (every role winds down).
+template <Arrivals A = Arrivals::kPair>
 __device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
                                           volatile int* dead) {
-  if (__all_sync(kFull, prod_look(bar, parity))) return true;
+  if (__all_sync(kFull, prod_look<A>(bar, parity))) return true;
 #pragma unroll 1
   for (uint32_t it = 0; it < kMbarPolls; ++it) {
     if (__any_sync(kFull, *dead)) return false;
-    if (__all_sync(kFull, prod_poll(bar, parity))) return true;
+    if (__all_sync(kFull, prod_poll<A>(bar, parity))) return true;
   }
   atomicOr(err, kDeviceTimeout);
   *dead = 1;
@@ -683,13 +714,13 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       bool ok = true;
       for (; ok && walk.valid(); walk.next())
         for (int kb = 0; kb < nk; ++kb) {
-          if (!prod_wait(&copied[rg.slot], rg.phase, p.err, dead)) {
+          if (!prod_wait<Arrivals::kOwn>(&copied[rg.slot], rg.phase, p.err, dead)) {
             ok = false;
             break;
           }
           tc::fence_proxy_async();
           __syncwarp();
-          tc::arrive_at(full0 + 8 * rg.slot);
+          tc::arrive_at(full0 + 8 * rg.slot, rank != 0);
           rg.next();
         }
     }
@@ -775,7 +806,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           dst[128] = rsf[1].x, dst[384] = rsf[1].y, dst[640] = rsf[1].z, dst[896] = rsf[1].w;
         tc::fence_proxy_async();
         __syncwarp();
-        tc::arrive_at(sf_full0 + 8 * rs.slot);
+        tc::arrive_at(sf_full0 + 8 * rs.slot, rank != 0);
         rs.next();
         // the next batch's loads run while this one is used
         if (k0 + kProdSfStages < nk) {
@@ -895,7 +926,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       }
       tc::fence_before();
       __syncwarp();
-      tc::arrive_at(d_empty0 + 8 * buf);
+      tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
     }
   }
   __syncwarp();
