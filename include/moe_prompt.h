@@ -137,6 +137,12 @@ moe_status_t moe_product_run(moe_product_t handle, int32_t R, int32_t A, const u
  * `stream`; the return value is MOE_ERR_DEVICE_FAULT when a bit was set. */
 moe_status_t moe_product_get_error(moe_product_t handle, void* stream, uint32_t* device_flags);
 
+/* Test support: in the next run that launches something, the MMAs wait for an
+ * arrival that nothing makes, with a limit of some milliseconds instead of a
+ * second. Every role gives up, the launch completes with unspecified outputs,
+ * the handle reports MOE_DEVICE_TIMEOUT and its later runs are unaffected. */
+moe_status_t moe_product_arm_timeout(moe_product_t handle);
+
 #ifdef __cplusplus
 }
 #endif

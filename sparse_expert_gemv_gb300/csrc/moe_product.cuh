@@ -57,6 +57,7 @@ constexpr int kProdStages = 6;
 constexpr int kProdSfStages = 4;   // stages a batch of scales covers
 constexpr int kProdThreads = 640;
 constexpr int kProdMaxE = 1024;
+constexpr int kProdSettleSleeps = 50;   // of kWaitSuspendNs: a dead pair's time for its copies
 constexpr int kProdABytes = kProdRows * kProdK;
 constexpr int kProdBBytes = kProdCols / 2 * kProdK;
 constexpr int kProdSfaBytes = 512;    // a stage's weight scales of one CTA
@@ -91,6 +92,8 @@ struct ProductParams {
   int sf_vec;              // scale bytes a load may take: 16, 4 or 1
   uint32_t w_bytes;        // bytes a CTA's weight copy completes
   uint32_t a_format;       // the MMA's code for the weights' element type
+  uint32_t polls;          // of a bounded wait: kMbarPolls
+  uint32_t withheld;       // 1: stages lack an arrival, so that waits run out (tests)
 };
 
 struct ProductSmem {
@@ -361,19 +364,30 @@ __device__ __forceinline__ bool prod_poll(uint64_t* bar, uint32_t parity) {
   return done != 0;
 }
 // A whole warp's bounded wait on a phase of this CTA's mbarrier; a timeout
-// marks the CTA dead (every role winds down).
+// marks both CTAs of the pair dead (every role winds down).
 template <Arrivals A = Arrivals::kPair>
-__device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, uint32_t* err,
+__device__ __forceinline__ bool prod_wait(uint64_t* bar, uint32_t parity, const ProductParams& p,
                                           volatile int* dead) {
   if (__all_sync(kFull, prod_look<A>(bar, parity))) return true;
 #pragma unroll 1
-  for (uint32_t it = 0; it < kMbarPolls; ++it) {
+  for (uint32_t it = 0; it < p.polls; ++it) {
     if (__any_sync(kFull, *dead)) return false;
     if (__all_sync(kFull, prod_poll<A>(bar, parity))) return true;
   }
-  atomicOr(err, kDeviceTimeout);
+  atomicOr(p.err, kDeviceTimeout);
   *dead = 1;
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(
+                   tc::cluster_addr(const_cast<int*>(dead), (blockIdx.x & 1) ^ 1))
+               : "memory");
   return false;
+}
+// The wait for what must have ended before a CTA may leave: neither a dead pair
+// nor p.polls shortens it.
+__device__ __forceinline__ void prod_wait_end(uint64_t* bar, uint32_t parity, uint32_t* err) {
+#pragma unroll 1
+  for (uint32_t it = 0; it < kMbarPolls; ++it)
+    if (__all_sync(kFull, prod_poll<Arrivals::kPair>(bar, parity))) return;
+  atomicOr(err, kDeviceTimeout);
 }
 
 // Barrier over `nthreads` threads on named barrier `id`: whether `ok` holds
@@ -533,7 +547,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     for (int i = 0; i < kProdStages; ++i) {
       // the announcement of both CTAs' TMA bytes, and with gathered rows both
       // CTAs' word that their copies have landed
-      mbar_init(&full[i], p.rows ? 3 : 1);
+      mbar_init(&full[i], (p.rows ? 3 : 1) + p.withheld);
       mbar_init(&empty[i], 1);
       mbar_init(&copied[i], 128);
     }
@@ -595,7 +609,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       const int grp = SILU ? t.e * (p.N / 16) + t.m * 4 : 0;
       for (int kb = 0; kb < nk; ++kb, ++g) {
         const int s = rg.slot;
-        if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+        if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p, dead)) {
           ok = false;
           break;
         }
@@ -608,10 +622,6 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         rg.next();
       }
     }
-    // never leave with copies in flight (both CTAs' complete here)
-    if (rank == 0)
-      for (int d = max(0, g - kProdStages); d < g; ++d)
-        prod_wait(&full[d % kProdStages], (d / kProdStages) & 1, p.err, dead);
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (rank == 0) {
@@ -626,13 +636,13 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int n = t.cols();
         const uint32_t idesc = tc::mx_idesc(p.a_format, n);
         const int buf = lt & 1;
-        if (lt >= 2) ok = prod_wait(&d_empty[buf], ((lt >> 1) - 1) & 1, p.err, dead);
+        if (lt >= 2) ok = prod_wait(&d_empty[buf], ((lt >> 1) - 1) & 1, p, dead);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = tmem + buf * kProdCols;
         for (int k0 = 0; ok && k0 < nk; k0 += kProdSfStages) {
           const int ns = min(kProdSfStages, nk - k0);
-          ok = prod_wait(&sf_full[rs.slot], rs.phase, p.err, dead);
+          ok = prod_wait(&sf_full[rs.slot], rs.phase, p, dead);
           if (!ok) break;
           const uint32_t sfc = tmem + kProdSfCol + rs.slot * kProdSfStages * kProdSfCols;
           const uint32_t sfs = smem_addr(smem + L::sf + rs.slot * kProdSfBytes);
@@ -645,7 +655,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
           }
           for (int j = 0; j < ns; ++j) {
             const int s = rg.slot;
-            ok = prod_wait(&full[s], rg.phase, p.err, dead);
+            ok = prod_wait(&full[s], rg.phase, p, dead);
             if (!ok) break;
             const uint64_t ad = tc::sdesc_sw128(smem_addr(smem + L::a + s * kProdABytes));
             const uint64_t bd = tc::sdesc_sw128(smem_addr(smem + L::b + s * kProdBBytes));
@@ -671,9 +681,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (!ok) break;
         tc::commit2(&d_full[buf]);
       }
-      // every MMA done before tensor memory is released
       tc::commit2(drain);
-      mbar_wait(drain, 0, p.err);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------- contiguous rows
@@ -687,7 +695,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         const int half = t.half(), r0 = t.r0 + rank * half;
         for (int kb = 0; kb < nk; ++kb, ++g) {
           const int s = rg.slot;
-          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p, dead)) {
             ok = false;
             break;
           }
@@ -714,7 +722,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       bool ok = true;
       for (; ok && walk.valid(); walk.next())
         for (int kb = 0; kb < nk; ++kb) {
-          if (!prod_wait<Arrivals::kOwn>(&copied[rg.slot], rg.phase, p.err, dead)) {
+          if (!prod_wait<Arrivals::kOwn>(&copied[rg.slot], rg.phase, p, dead)) {
             ok = false;
             break;
           }
@@ -749,7 +757,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
         if (more) nxt.load(p, walk.tile(), rank, r);   // used a tile later
         for (int kb = 0; kb < nk; ++kb, ++g) {
           const int s = rg.slot, at = kb * kProdK + within;
-          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p.err, dead)) {
+          if (g >= kProdStages && !prod_wait(&empty[s], rg.phase ^ 1u, p, dead)) {
             ok = false;
             break;
           }
@@ -793,7 +801,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
       more = walk.valid();
       if (more) nxt.load(p, walk.tile(), r);
       for (int k0 = 0; k0 < nk; k0 += kProdSfStages, ++gb) {
-        if (gb >= 2 && !prod_wait(&sf_empty[rs.slot], rs.phase ^ 1u, p.err, dead)) {
+        if (gb >= 2 && !prod_wait(&sf_empty[rs.slot], rs.phase ^ 1u, p, dead)) {
           ok = false;
           break;
         }
@@ -831,7 +839,7 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
     for (; walk.valid(); walk.next(), ++lt) {
       const ProductTile t = walk.tile();
       const int buf = lt & 1;
-      bool ok = prod_wait(&d_full[buf], (lt >> 1) & 1, p.err, dead);
+      bool ok = prod_wait(&d_full[buf], (lt >> 1) & 1, p, dead);
       // a group's warps go on or leave together: no named barrier below waits
       // for a warp that gave up
       ok = named_all(bar, 128, ok);
@@ -932,6 +940,16 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
   __syncwarp();
   tc::fence_before();
   __syncthreads();
+  // Before a CTA leaves and tensor memory is released, every MMA is done (they
+  // read both CTAs' shared memory and arrive on both CTAs' barriers), and with
+  // them every copy into a stage that they read, which is all there are unless
+  // the pair is dead. Then copies of this CTA may still be in flight, and those
+  // of the second CTA complete on the first one's barriers: both stay for a time
+  // that is hundreds of times a copy's.
+  if (warp == 1) prod_wait_end(drain, 0, p.err);
+  if (warp == 0 && *dead)
+    for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
+  __syncwarp();
   cluster_sync();   // no CTA leaves while the other may still reach into it
   tc::fence_after();
   if (warp == 1) tc::tmem_dealloc2(*tmem_slot, kProdTmemCols);

@@ -23,6 +23,7 @@ struct moe_product {
   CUtensorMap tm_w;
   uint8_t* sfa;       // the weights' scales in tile order
   uint32_t* d_err;
+  std::atomic<bool> armed;   // the next run's waits run out (moe_product_arm_timeout)
 };
 
 namespace {
@@ -356,11 +357,20 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
   p.sf_vec = ks % 16 == 0 && aligned(a_scales, 16) ? 16 : ks % 4 == 0 && aligned(a_scales, 4) ? 4 : 1;
   p.w_bytes = is_fp4(c) ? moe::kProdABytes / 2 : moe::kProdABytes;
   p.a_format = is_fp4(c) ? 5 : 0;
+  const bool armed = m->armed.exchange(false, std::memory_order_relaxed);
+  p.polls = armed ? 50 : moe::kMbarPolls;   // a millisecond
+  p.withheld = armed;
   // one pair of CTAs a pair of SMs, and no more than there can be tiles
   const int64_t most = ((int64_t)std::min(c.E, R) + R / moe::kProdCols) * ((m->mt + 1) / 2);
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(std::max(1, m->num_sms / 2), most);
   return launch(silu ? moe::moe_product_tiles<true> : moe::moe_product_tiles<false>, grid,
                 moe::kProdThreads, kProductSmem, stream, 2, p);
+}
+
+moe_status_t moe_product_arm_timeout(moe_product_t m) {
+  if (!m) return MOE_ERR_INVALID_ARG;
+  m->armed.store(true, std::memory_order_relaxed);
+  return MOE_OK;
 }
 
 moe_status_t moe_product_get_error(moe_product_t m, void* stream, uint32_t* device_flags) {

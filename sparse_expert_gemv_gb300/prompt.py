@@ -130,6 +130,12 @@ class GroupedProduct:
         return _moe_torch.product_run(h, self.E, self.N, self.K, self.silu_mul, a, a_scales,
                                       offsets, rows, out, out_scales, _handle(stream))
 
+    def arm_timeout(self) -> None:
+        """Test support: the bounded waits of the next run that launches
+        something run out (it sets MOE_DEVICE_TIMEOUT, which get_error
+        reports)."""
+        check(lib.moe_product_arm_timeout(self._h), "moe_product_arm_timeout")
+
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits, after waiting for the
         stream."""

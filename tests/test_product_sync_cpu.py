@@ -34,3 +34,32 @@ def test_only_a_barrier_of_one_cta_is_waited_for_at_cta_scope():
     assert own == ["copied"]                      # its 128 arrivals are this CTA's copying warps
     assert re.search(r"template <Arrivals A = Arrivals::kPair>\s*__device__ __forceinline__ bool prod_wait",
                      text)
+
+
+def test_no_cta_leaves_with_copies_or_mmas_in_flight():
+    text = source()
+    end = text[text.rindex("tc::fence_before();"):]
+    order = [end.index(s) for s in ("__syncthreads();", "prod_wait_end(drain, 0, p.err);",
+                                    "if (warp == 0 && *dead)", "cluster_sync();", "tmem_dealloc2")]
+    assert order == sorted(order)                 # in both CTAs: no rank is asked before
+    assert "rank" not in end
+    # the last wait goes on when the pair is dead or its waits run out early
+    body = text[text.index("void prod_wait_end("):]
+    body = body[:body.index("\n}")]
+    assert "dead" not in body and "polls" not in body.replace("kMbarPolls", "")
+
+
+def test_a_timeout_marks_both_ctas():
+    text = source()
+    body = text[text.index("bool prod_wait(uint64_t* bar"):]
+    body = body[:body.index("\n}")]
+    assert "st.relaxed.cluster.shared::cluster" in body and "(blockIdx.x & 1) ^ 1" in body
+
+
+def test_arm_timeout_refuses_a_null_handle():
+    import __graft_entry__
+    b = __graft_entry__._build_module()
+    if b.stale(b.OUT):
+        b.build()
+    from sparse_expert_gemv_gb300._lib import lib
+    assert lib.moe_product_arm_timeout(None) == 1
