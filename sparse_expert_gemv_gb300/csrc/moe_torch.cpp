@@ -10,6 +10,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Stream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdarg>
@@ -74,7 +75,9 @@ const at::Tensor& matrix(PyObject* o, at::ScalarType dtype, const char* name) {
   return need(o, dtype, std::nullopt, name);
 }
 
-// The caller's output buffer, or a new one.
+// The caller's output buffer, or a new one: of the current stream's memory, so
+// the stream of the call has to be current (a block of another stream's may
+// still be read there, and would return there while this call writes it).
 at::Tensor output(PyObject* o, at::ScalarType dtype, at::IntArrayRef shape, const char* name,
                   const at::Tensor& like) {
   if (o != Py_None) return need(o, dtype, shape, name);
@@ -102,12 +105,16 @@ T* data(const at::Tensor& t) {
   return t.defined() ? static_cast<T*>(t.data_ptr()) : nullptr;
 }
 
-// None: the current stream of the tensor's device; else a cudaStream_t.
-void* stream_of(PyObject* o, const at::Tensor& t) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (!s && PyErr_Occurred()) throw Raised{};
-  return s;
+// The stream a call runs on: `o`, a torch.cuda.Stream of the tensor's device, or
+// that device's current stream for None.
+c10::cuda::CUDAStream stream_of(PyObject* o, const at::Tensor& t) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(t.device().index());
+  if (!THPStream_Check(o)) raise(PyExc_TypeError, "stream must be a torch.cuda.Stream");
+  const THPStream* s = reinterpret_cast<const THPStream*>(o);
+  if (s->device_type != (int64_t)c10::DeviceType::CUDA || s->device_index != t.device().index())
+    raise(PyExc_ValueError, "stream: expected one of %s", t.device().str().c_str());
+  return c10::cuda::CUDAStream::unpack3(s->stream_id, (c10::DeviceIndex)s->device_index,
+                                        (c10::DeviceType)s->device_type);
 }
 
 void check(moe_status_t st, const char* what) {
@@ -167,6 +174,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       raise(PyExc_ValueError, "add_rms_norm: ask for bf16 rows, mxfp8 rows or both");
     at::Tensor residual, sum, y, codes, scales;
     if (a[2] != Py_None) residual = need(a[2], at::kBFloat16, x.sizes(), "residual");
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[10], x));
     if (residual.defined() || a[6] != Py_None)
       sum = output(a[6], at::kBFloat16, x.sizes(), "sum", x);
     if (bf16) y = output(a[7], at::kBFloat16, x.sizes(), "y", x);
@@ -174,11 +182,10 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
       codes = output(a[8], at::kByte, x.sizes(), "codes", x);
       scales = output(a[9], at::kByte, {T, H / 32}, "scales", x);
     }
-    const c10::cuda::CUDAGuard device(x.device());
     check(moe_add_rms_norm(int32_of(T, "T"), int32_of(H, "H"), data<uint16_t>(x),
                            data<uint16_t>(residual), data<uint16_t>(weight), eps,
                            data<uint16_t>(sum), data<uint16_t>(y), data<uint8_t>(codes),
-                           data<uint8_t>(scales), stream_of(a[10], x)),
+                           data<uint8_t>(scales), on.current_stream().stream()),
           "moe_add_rms_norm");
     return wrap_all(sum, y, codes, scales);
   });
@@ -191,13 +198,13 @@ PyObject* group_by_expert(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t T = ids.size(0), k = ids.size(1);
     const int32_t E = int32_of(a[1], "E");
     if (E < 1) raise(PyExc_ValueError, "E must be positive");
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[5], ids));
     at::Tensor offsets = output(a[2], at::kInt, {(int64_t)E + 1}, "offsets", ids);
     at::Tensor rows = output(a[3], at::kInt, {T * k}, "rows", ids);
     at::Tensor slots = output(a[4], at::kInt, ids.sizes(), "slots", ids);
-    const c10::cuda::CUDAGuard device(ids.device());
     check(moe_group(int32_of(T, "T"), int32_of(k, "k"), E, data<int32_t>(ids),
                     data<int32_t>(offsets), data<int32_t>(rows), data<int32_t>(slots),
-                    stream_of(a[5], ids)),
+                    on.current_stream().stream()),
           "moe_group");
     return wrap_all(offsets, rows, slots);
   });
@@ -212,11 +219,11 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& w = need(a[2], at::kFloat, slots.sizes(), "w");
     at::Tensor residual;
     if (a[3] != Py_None) residual = need(a[3], at::kBFloat16, at::IntArrayRef{T, H}, "residual");
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[5], y));
     at::Tensor out = output(a[4], at::kBFloat16, {T, H}, "out", y);
-    const c10::cuda::CUDAGuard device(y.device());
     check(moe_combine(int32_of(T, "T"), int32_of(k, "k"), int32_of(H, "H"), int32_of(R, "R"),
                       data<uint16_t>(y), data<int32_t>(slots), data<float>(w),
-                      data<uint16_t>(residual), data<uint16_t>(out), stream_of(a[5], y)),
+                      data<uint16_t>(residual), data<uint16_t>(out), on.current_stream().stream()),
           "moe_combine");
     return wrap(out);
   });
@@ -241,6 +248,7 @@ PyObject* product_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
       R = tensor(a[8], "rows").numel();
       rows = need(a[8], at::kInt, at::IntArrayRef{R}, "rows");
     }
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[11], rows_of));
     at::Tensor out = output(a[9], silu ? at::kByte : at::kBFloat16, {R, silu ? N / 2 : N}, "out",
                             rows_of);
     at::Tensor scales;
@@ -248,11 +256,10 @@ PyObject* product_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
       scales = output(a[10], at::kByte, {R, N / 64}, "out_scales", rows_of);
     else if (a[10] != Py_None)
       raise(PyExc_ValueError, "out_scales: only a product with silu_mul has scales");
-    const c10::cuda::CUDAGuard device(rows_of.device());
     check(moe_product_run(handle, int32_of(R, "R"), int32_of(A, "A"), data<uint8_t>(rows_of),
                           data<uint8_t>(a_scales), data<int32_t>(offsets), data<int32_t>(rows),
                           silu ? nullptr : data<uint16_t>(out), silu ? data<uint8_t>(out) : nullptr,
-                          data<uint8_t>(scales), stream_of(a[11], rows_of)),
+                          data<uint8_t>(scales), on.current_stream().stream()),
           "moe_product_run");
     return silu ? wrap_all(out, scales) : wrap(out);
   });

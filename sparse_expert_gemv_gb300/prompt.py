@@ -15,7 +15,9 @@ MoEDecode.prompt is the part after the router on a layer's own weights. As in
 the decode layer, every call forwards device pointers and a stream to
 libmoe_decode.so; nothing is computed here. The calls a block makes go through
 the extension module _moe_torch (csrc/moe_torch.cpp), which checks the tensors,
-allocates the outputs that were not passed in, and takes the current stream.
+allocates the outputs that were not passed in, and takes the current stream or
+the torch.cuda.Stream given as `stream`. New outputs belong to the stream of
+the call, as if it were current.
 """
 from __future__ import annotations
 
@@ -39,10 +41,6 @@ class RmsNorm(NamedTuple):
     scales: torch.Tensor | None   # uint8 [T, H/32]: and UE8M0 scale codes
 
 
-def _handle(stream: torch.cuda.Stream | None) -> int | None:
-    return None if stream is None else stream.cuda_stream
-
-
 def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = True,
                  mxfp8: bool = False, sum=None, y=None, codes=None, scales=None,
                  stream=None) -> RmsNorm:
@@ -55,7 +53,7 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = Tr
     residual, which is then updated in place.
     """
     return RmsNorm._make(_moe_torch.add_rms_norm(
-        x, weight, residual, eps, bf16, mxfp8, sum, y, codes, scales, _handle(stream)))
+        x, weight, residual, eps, bf16, mxfp8, sum, y, codes, scales, stream))
 
 
 def group_by_expert(ids, E: int, *, offsets=None, rows=None, slots=None, stream=None):
@@ -64,14 +62,14 @@ def group_by_expert(ids, E: int, *, offsets=None, rows=None, slots=None, stream=
     rows[q] is the token of grouped row q (-1 past the last group) and
     slots[t, j] the grouped row of a slot (-1 for an id outside [0, E), which
     joins no group)."""
-    return _moe_torch.group_by_expert(ids, E, offsets, rows, slots, _handle(stream))
+    return _moe_torch.group_by_expert(ids, E, offsets, rows, slots, stream)
 
 
 def combine(y, slots, w, *, residual=None, out=None, stream=None):
     """out[t] = bf16(residual[t] + sum_j w[t, j] * y[slots[t, j]]) over expert
     rows y bf16 [R, H], slots int32 [T, k] (outside [0, R): nothing) and w
     float32 [T, k]; residual bf16 [T, H] is optional and may be `out`."""
-    return _moe_torch.combine(y, slots, w, residual, out, _handle(stream))
+    return _moe_torch.combine(y, slots, w, residual, out, stream)
 
 
 class GroupedProduct:
@@ -128,7 +126,7 @@ class GroupedProduct:
         `rows`, or A. Rows outside every group are left as they are."""
         h = self._h.value if self._h else 0
         return _moe_torch.product_run(h, self.E, self.N, self.K, self.silu_mul, a, a_scales,
-                                      offsets, rows, out, out_scales, _handle(stream))
+                                      offsets, rows, out, out_scales, stream)
 
     def arm_timeout(self) -> None:
         """Test support: the bounded waits of the next run that launches

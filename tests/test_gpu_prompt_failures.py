@@ -41,3 +41,78 @@ def test_an_armed_timeout_waits_for_a_run_that_launches(dev):  # noqa: F811
     assert p.get_error() == 0
     p(a, s, off)
     assert p.get_error() == MOE_DEVICE_TIMEOUT
+
+
+def calls(dev):  # noqa: F811
+    """Each operator as a call of its keyword arguments, with small inputs."""
+    from sparse_expert_gemv_gb300 import add_rms_norm, combine, group_by_expert
+    g = torch.Generator(device=dev).manual_seed(33)
+    x, res = (torch.randn(64, 512, device=dev, generator=g).bfloat16() for _ in range(2))
+    weight = torch.ones(512, dtype=torch.bfloat16, device=dev)
+    ids = torch.randint(0, 9, (64, 4), dtype=torch.int32, device=dev, generator=g)
+    w = torch.rand(64, 4, device=dev, generator=g)
+    y = torch.randn(256, 512, device=dev, generator=g).bfloat16()
+    slots = torch.randperm(256, device=dev, generator=g).int().view(64, 4)
+    c = Products(dev, "mxfp8", 256, 512, [100, 156], 34)
+    plain, gate_up, args = c.handle(False), c.handle(True), c.args()
+    return {"norm": lambda **kw: add_rms_norm(x, weight, res, mxfp8=True, **kw),
+            "group": lambda **kw: group_by_expert(ids, 9, **kw),
+            "combine": lambda **kw: combine(y, slots, w, residual=res, **kw),
+            "product": lambda **kw: plain(*args, **kw),
+            "gate/up": lambda **kw: gate_up(*args, **kw)}
+
+
+def listed(out):
+    return [out] if isinstance(out, torch.Tensor) else list(out)
+
+
+@pytest.mark.parametrize("op", ["norm", "group", "combine", "product", "gate/up"])
+def test_outputs_on_a_given_stream_are_of_its_memory(dev, op):  # noqa: F811
+    call = calls(dev)[op]
+    want = [t.clone() for t in listed(call())]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    # blocks of the outputs' sizes that the current stream has just let go of, with
+    # work on them still queued there
+    freed = [torch.full_like(t, 3) for t in want for _ in range(4)]
+    blocks = {f.data_ptr() for f in freed}
+    kept = [torch.empty_like(f) for f in freed]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    for k, f in zip(kept, freed):
+        k.copy_(f)
+    del freed, f
+    got = listed(call(stream=side))
+    assert not blocks & {t.data_ptr() for t in got}
+    side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    for k in kept:
+        assert k.eq(3).all()
+
+
+def test_prompt_on_a_given_stream(dev):  # noqa: F811
+    import numpy as np
+    import workloads as wl
+    from sparse_expert_gemv_gb300 import MoEDecode
+    E, k, H, I, T = 8, 2, 256, 128, 30
+    experts = wl.make_experts(wl.Workload(91, "stream", E, k, H, I, T, 0.05), 35, range(E))
+    stack = [torch.from_numpy(np.stack([experts[e][i] for e in range(E)])).to(dev) for i in range(4)]
+    layer = MoEDecode(*stack, k=k, max_T=4)
+    g = torch.Generator(device=dev).manual_seed(36)
+    codes = torch.randint(0, 120, (T, H), dtype=torch.uint8, device=dev, generator=g)
+    scales = torch.full((T, H // 32), 120, dtype=torch.uint8, device=dev)
+    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device=dev, generator=g)
+    w = torch.rand(T, k, device=dev, generator=g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = layer.prompt(codes, scales, ids, w, stream=side)
+    side.synchronize()
+    assert torch.equal(got, layer.prompt(codes, scales, ids, w))
+
+
+def test_a_stream_is_a_torch_stream(dev):  # noqa: F811
+    for call in calls(dev).values():
+        with pytest.raises(TypeError):
+            call(stream=torch.cuda.Stream().cuda_stream)
