@@ -1,6 +1,8 @@
 """Tensor arguments of the C ABI's calls: their checks, pointers and streams."""
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 
@@ -17,6 +19,14 @@ def _stream(stream: torch.cuda.Stream | None) -> int:
     if _raw_stream is not None:
         return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
+
+
+_current = contextlib.nullcontext()
+
+
+def _on(stream: torch.cuda.Stream | None):
+    """A context in which `stream` is the current stream; None changes nothing."""
+    return _current if stream is None else torch.cuda.stream(stream)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)

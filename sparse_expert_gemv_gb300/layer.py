@@ -11,7 +11,7 @@ import torch
 
 from ._lib import (MOE_FLAG_MXFP4, MOE_PATH_AUTO, MOE_PATH_TENSOR, MOE_PATH_WARP, MoEConfig, check,
                    lib)
-from ._tensors import _need, _ptr, _stream
+from ._tensors import _need, _on, _ptr, _stream
 from .prompt import GroupedProduct, combine, group_by_expert
 
 
@@ -98,9 +98,10 @@ class MoEDecode:
         (bounded; it sets MOE_DEVICE_TIMEOUT, which get_error reports)."""
         check(lib.moe_decode_arm_barrier_timeout(self._h), "moe_decode_arm_barrier_timeout")
 
-    def _dev(self, shape, dtype, out, name):
-        if out is None:
-            return torch.empty(shape, dtype=dtype, device=self._weights[0].device)
+    def _dev(self, shape, dtype, out, name, stream):
+        if out is None:             # of the memory of the stream that writes it
+            with _on(stream):
+                return torch.empty(shape, dtype=dtype, device=self._weights[0].device)
         _need(out, dtype, shape, name)
         return out
 
@@ -108,8 +109,8 @@ class MoEDecode:
     def route(self, logits, ids=None, w=None, stream=None):
         T = logits.shape[0]
         _need(logits, torch.float32, (T, self.E), "logits")
-        ids = self._dev((T, self.k), torch.int32, ids, "topk_ids")
-        w = self._dev((T, self.k), torch.float32, w, "topk_w")
+        ids = self._dev((T, self.k), torch.int32, ids, "topk_ids", stream)
+        w = self._dev((T, self.k), torch.float32, w, "topk_w", stream)
         check(lib.moe_route(self._h, T, _ptr(logits), _ptr(ids), _ptr(w), _stream(stream)),
               "moe_route")
         return ids, w
@@ -119,10 +120,11 @@ class MoEDecode:
         _need(ids, torch.int32, (T, self.k), "topk_ids")
         U = min(self.E, T * self.k)
         dev = ids.device
-        uniq = torch.full((U,), -1, dtype=torch.int32, device=dev)
-        off = torch.full((U + 1,), -1, dtype=torch.int32, device=dev)
-        pairs = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
-        n = torch.zeros((1,), dtype=torch.int32, device=dev)
+        with _on(stream):           # the fills come before the schedule there
+            uniq = torch.full((U,), -1, dtype=torch.int32, device=dev)
+            off = torch.full((U + 1,), -1, dtype=torch.int32, device=dev)
+            pairs = torch.full((T * self.k,), -1, dtype=torch.int32, device=dev)
+            n = torch.zeros((1,), dtype=torch.int32, device=dev)
         check(lib.moe_dedup_schedule(self._h, T, _ptr(ids), _ptr(uniq), _ptr(off), _ptr(pairs),
                                      _ptr(n), _stream(stream)), "moe_dedup_schedule")
         return uniq, off, pairs, n
@@ -131,7 +133,7 @@ class MoEDecode:
         T = x.shape[0]
         _need(x, torch.bfloat16, (T, self.H), "x")
         _need(ids, torch.int32, (T, self.k), "topk_ids")
-        h = self._dev((T, self.k, self.I), torch.bfloat16, h, "h")
+        h = self._dev((T, self.k, self.I), torch.bfloat16, h, "h", stream)
         check(lib.moe_gate_up(self._h, T, _ptr(x), _ptr(ids), _ptr(h), _stream(stream)),
               "moe_gate_up")
         return h
@@ -141,7 +143,7 @@ class MoEDecode:
         _need(h, torch.bfloat16, (T, self.k, self.I), "h")
         _need(ids, torch.int32, (T, self.k), "topk_ids")
         _need(w, torch.float32, (T, self.k), "topk_w")
-        y = self._dev((T, self.H), torch.bfloat16, y, "y")
+        y = self._dev((T, self.H), torch.bfloat16, y, "y", stream)
         check(lib.moe_down(self._h, T, _ptr(h), _ptr(ids), _ptr(w), _ptr(y), _stream(stream)),
               "moe_down")
         return y
@@ -151,8 +153,8 @@ class MoEDecode:
         _need(x, torch.bfloat16, (T, self.H), "x")
         _need(ids, torch.int32, (T, self.k), "topk_ids")
         _need(w, torch.float32, (T, self.k), "topk_w")
-        h = self._dev((T, self.k, self.I), torch.bfloat16, h, "h")
-        y = self._dev((T, self.H), torch.bfloat16, y, "y")
+        h = self._dev((T, self.k, self.I), torch.bfloat16, h, "h", stream)
+        y = self._dev((T, self.H), torch.bfloat16, y, "y", stream)
         check(lib.moe_decode_layer(self._h, T, _ptr(x), _ptr(ids), _ptr(w), _ptr(h), _ptr(y),
                                    _stream(stream)), "moe_decode_layer")
         return y

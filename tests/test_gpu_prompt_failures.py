@@ -59,14 +59,38 @@ def calls(dev):  # noqa: F811
             "group": lambda **kw: group_by_expert(ids, 9, **kw),
             "combine": lambda **kw: combine(y, slots, w, residual=res, **kw),
             "product": lambda **kw: plain(*args, **kw),
-            "gate/up": lambda **kw: gate_up(*args, **kw)}
+            "gate/up": lambda **kw: gate_up(*args, **kw)} | decode_calls(dev)
+
+
+def decode_calls(dev):  # noqa: F811
+    layer, T = small_layer(dev), 30
+    g = torch.Generator(device=dev).manual_seed(37)
+    logits = torch.randn(T, layer.E, device=dev, generator=g)
+    ids, w = layer.route(logits)
+    x = torch.randn(T, layer.H, device=dev, generator=g).bfloat16()
+    h = layer.gate_up(x, ids)
+    return {"route": lambda **kw: layer.route(logits, **kw),
+            "schedule": lambda **kw: layer.dedup_schedule(ids, **kw),
+            "decode gate/up": lambda **kw: layer.gate_up(x, ids, **kw),
+            "decode down": lambda **kw: layer.down(h, ids, w, **kw),
+            "decode layer": lambda **kw: layer.layer(x, ids, w, **kw)}
+
+
+def small_layer(dev, fmt="mxfp8"):  # noqa: F811
+    import numpy as np
+    import workloads as wl
+    from sparse_expert_gemv_gb300 import MoEDecode
+    experts = wl.make_experts(wl.Workload(91, "stream", 8, 2, 256, 128, 30, 0.05), 35, range(8), fmt=fmt)
+    stack = [torch.from_numpy(np.stack([experts[e][i] for e in range(8)])).to(dev) for i in range(4)]
+    return MoEDecode(*stack, k=2, max_T=30, fmt=fmt)
 
 
 def listed(out):
     return [out] if isinstance(out, torch.Tensor) else list(out)
 
 
-@pytest.mark.parametrize("op", ["norm", "group", "combine", "product", "gate/up"])
+@pytest.mark.parametrize("op", ["norm", "group", "combine", "product", "gate/up", "route", "schedule",
+                                "decode gate/up", "decode down", "decode layer"])
 def test_outputs_on_a_given_stream_are_of_its_memory(dev, op):  # noqa: F811
     call = calls(dev)[op]
     want = [t.clone() for t in listed(call())]
@@ -92,27 +116,25 @@ def test_outputs_on_a_given_stream_are_of_its_memory(dev, op):  # noqa: F811
         assert k.eq(3).all()
 
 
-def test_prompt_on_a_given_stream(dev):  # noqa: F811
-    import numpy as np
-    import workloads as wl
-    from sparse_expert_gemv_gb300 import MoEDecode
-    E, k, H, I, T = 8, 2, 256, 128, 30
-    experts = wl.make_experts(wl.Workload(91, "stream", E, k, H, I, T, 0.05), 35, range(E))
-    stack = [torch.from_numpy(np.stack([experts[e][i] for e in range(E)])).to(dev) for i in range(4)]
-    layer = MoEDecode(*stack, k=k, max_T=4)
+def prompt_args(dev, layer, T):  # noqa: F811
     g = torch.Generator(device=dev).manual_seed(36)
-    codes = torch.randint(0, 120, (T, H), dtype=torch.uint8, device=dev, generator=g)
-    scales = torch.full((T, H // 32), 120, dtype=torch.uint8, device=dev)
-    ids = torch.randint(0, E, (T, k), dtype=torch.int32, device=dev, generator=g)
-    w = torch.rand(T, k, device=dev, generator=g)
+    codes = torch.randint(0, 120, (T, layer.H), dtype=torch.uint8, device=dev, generator=g)
+    scales = torch.full((T, layer.H // 32), 120, dtype=torch.uint8, device=dev)
+    ids = torch.randint(0, layer.E, (T, layer.k), dtype=torch.int32, device=dev, generator=g)
+    return codes, scales, ids, torch.rand(T, layer.k, device=dev, generator=g)
+
+
+def test_prompt_on_a_given_stream(dev):  # noqa: F811
+    layer = small_layer(dev)
+    args = prompt_args(dev, layer, 30)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    got = layer.prompt(codes, scales, ids, w, stream=side)
+    got = layer.prompt(*args, stream=side)
     side.synchronize()
-    assert torch.equal(got, layer.prompt(codes, scales, ids, w))
+    assert torch.equal(got, layer.prompt(*args))
 
 
 def test_a_stream_is_a_torch_stream(dev):  # noqa: F811
-    for call in calls(dev).values():
-        with pytest.raises(TypeError):
+    for name, call in calls(dev).items():
+        with pytest.raises((TypeError, AttributeError)):
             call(stream=torch.cuda.Stream().cuda_stream)
