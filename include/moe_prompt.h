@@ -105,7 +105,8 @@ typedef struct moe_product* moe_product_t;
  *             copy in the order in which the tensor cores take them (padded to
  *             128 rows and 128 K elements), laid out by a kernel on `stream`,
  *             for which this call waits (so not while a graph is captured)
- * Allocates that copy and the error word.
+ * Allocates that copy and the error word, one CUDA event and one non-blocking
+ * stream (for reading the error word).
  */
 moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* w,
                                 const uint8_t* w_scales, moe_product_t* out, void* stream);
@@ -132,10 +133,13 @@ moe_status_t moe_product_run(moe_product_t handle, int32_t R, int32_t A, const u
                              const uint8_t* a_scales, const int32_t* offsets, const int32_t* rows,
                              uint16_t* y, uint8_t* codes, uint8_t* scales, void* stream);
 
-/* Read and clear the handle's device error word (MOE_DEVICE_TIMEOUT: a
- * bounded device wait gave up and outputs are undefined) after waiting for
- * `stream`; the return value is MOE_ERR_DEVICE_FAULT when a bit was set. */
+/* Read and clear, in one step, the handle's device error word
+ * (MOE_DEVICE_TIMEOUT: a bounded device wait gave up and outputs are undefined)
+ * after waiting for the handle's latest run that was not being captured into a
+ * graph, and moe_product_get_error for `stream` too (which covers graphs
+ * replayed there). The return value is MOE_ERR_DEVICE_FAULT when a bit was set. */
 moe_status_t moe_product_get_error(moe_product_t handle, void* stream, uint32_t* device_flags);
+moe_status_t moe_product_get_error_latest(moe_product_t handle, uint32_t* device_flags);
 
 /* Test support: in the next run that launches something, the MMAs wait for an
  * arrival that nothing makes, with a limit of some milliseconds instead of a

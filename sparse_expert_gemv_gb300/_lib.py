@@ -100,6 +100,7 @@ PROMPT_SIGNATURES = {
     "moe_product_destroy": (_st, [_p]),
     "moe_product_run": (_st, [_p, _i32, _i32, _p, _p, _p, _p, _p, _p, _p, _p]),
     "moe_product_get_error": (_st, [_p, _p, ctypes.POINTER(ctypes.c_uint32)]),
+    "moe_product_get_error_latest": (_st, [_p, ctypes.POINTER(ctypes.c_uint32)]),
     "moe_product_arm_timeout": (_st, [_p]),
 }
 

@@ -314,6 +314,9 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
   reinterpret_cast<uint32_t*>(out)[block * 128 + threadIdx.x] = v;
 }
 
+// err[1] = the error word err[0], which is cleared.
+__global__ void moe_product_take_error(uint32_t* err) { err[1] = atomicExch(err, 0u); }
+
 // ---------------------------------------------------------------------------
 // moe_product_tiles
 // ---------------------------------------------------------------------------

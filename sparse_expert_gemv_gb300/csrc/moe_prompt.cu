@@ -22,7 +22,14 @@ struct moe_product {
   int mt;             // weight tiles of an expert
   CUtensorMap tm_w;
   uint8_t* sfa;       // the weights' scales in tile order
-  uint32_t* d_err;
+  uint32_t* d_err;    // device error word, and where a read of it leaves its value
+  // as the decode layer's handle has them: completion of the latest run outside
+  // a capture, which the reads of the error word wait for, and their own
+  // non-blocking stream; reads take turns
+  cudaEvent_t done_ev;
+  std::atomic<bool> done_recorded;
+  cudaStream_t aux;
+  std::mutex read_mu;
   std::atomic<bool> armed;   // the next run's waits run out (moe_product_arm_timeout)
 };
 
@@ -180,7 +187,36 @@ bool encode_weights(moe_product* m, const uint8_t* w) {
 
 constexpr size_t kProductSmem = (size_t)moe::ProductSmem::total + 1024;
 
+// After a run has been enqueued on s: record its completion, unless s is being
+// captured into a graph (the event would stand for a graph node then).
+void mark_done(moe_product* m, cudaStream_t s) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return;
+  }
+  if (cs != cudaStreamCaptureStatusNone) return;
+  if (cudaEventRecord(m->done_ev, s) == cudaSuccess) m->done_recorded = true;
+}
+
+// Reads and clears the error word in one step, so that no bit set meanwhile is
+// lost, once the latest run outside a capture is over.
+moe_status_t read_error(moe_product* m, uint32_t* device_flags) {
+  if (m->done_recorded && cudaEventSynchronize(m->done_ev) != cudaSuccess) return MOE_ERR_CUDA;
+  const std::lock_guard<std::mutex> turn(m->read_mu);
+  moe::moe_product_take_error<<<1, 1, 0, m->aux>>>(m->d_err);
+  uint32_t v = 0;
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&v, m->d_err + 1, 4, cudaMemcpyDeviceToHost, m->aux) != cudaSuccess ||
+      cudaStreamSynchronize(m->aux) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  *device_flags = v;
+  return v ? MOE_ERR_DEVICE_FAULT : MOE_OK;
+}
+
 void free_product(moe_product* m) {
+  if (m->done_ev) cudaEventDestroy(m->done_ev);
+  if (m->aux) cudaStreamDestroy(m->aux);
   cudaFree(m->sfa);
   cudaFree(m->d_err);
   delete m;
@@ -286,8 +322,10 @@ moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* 
       blocks <= 0x7fffffff && cudaGetDevice(&dev) == cudaSuccess &&
       cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
       cudaMalloc(&m->sfa, (size_t)blocks * moe::kProdSfaBytes) == cudaSuccess &&
-      cudaMalloc(&m->d_err, 4) == cudaSuccess &&
-      cudaMemsetAsync(m->d_err, 0, 4, static_cast<cudaStream_t>(stream)) == cudaSuccess &&
+      cudaMalloc(&m->d_err, 8) == cudaSuccess &&
+      cudaMemsetAsync(m->d_err, 0, 8, static_cast<cudaStream_t>(stream)) == cudaSuccess &&
+      cudaEventCreateWithFlags(&m->done_ev, cudaEventDisableTiming) == cudaSuccess &&
+      cudaStreamCreateWithFlags(&m->aux, cudaStreamNonBlocking) == cudaSuccess &&
       encode_weights(m, w) &&
       cudaFuncSetAttribute(moe::moe_product_tiles<false>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -363,8 +401,11 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
   // one pair of CTAs a pair of SMs, and no more than there can be tiles
   const int64_t most = ((int64_t)std::min(c.E, R) + R / moe::kProdCols) * ((m->mt + 1) / 2);
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(std::max(1, m->num_sms / 2), most);
-  return launch(silu ? moe::moe_product_tiles<true> : moe::moe_product_tiles<false>, grid,
-                moe::kProdThreads, kProductSmem, stream, 2, p);
+  const moe_status_t st =
+      launch(silu ? moe::moe_product_tiles<true> : moe::moe_product_tiles<false>, grid,
+             moe::kProdThreads, kProductSmem, stream, 2, p);
+  if (st == MOE_OK) mark_done(m, static_cast<cudaStream_t>(stream));
+  return st;
 }
 
 moe_status_t moe_product_arm_timeout(moe_product_t m) {
@@ -373,16 +414,17 @@ moe_status_t moe_product_arm_timeout(moe_product_t m) {
   return MOE_OK;
 }
 
+moe_status_t moe_product_get_error_latest(moe_product_t m, uint32_t* device_flags) {
+  if (device_flags) *device_flags = 0;
+  if (!m || !device_flags) return MOE_ERR_INVALID_ARG;
+  return read_error(m, device_flags);
+}
+
 moe_status_t moe_product_get_error(moe_product_t m, void* stream, uint32_t* device_flags) {
   if (device_flags) *device_flags = 0;
   if (!m || !device_flags) return MOE_ERR_INVALID_ARG;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  uint32_t v = 0;
-  if (cudaMemcpyAsync(&v, m->d_err, 4, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaMemsetAsync(m->d_err, 0, 4, s) != cudaSuccess || cudaStreamSynchronize(s) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  *device_flags = v;
-  return v ? MOE_ERR_DEVICE_FAULT : MOE_OK;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+  return read_error(m, device_flags);
 }
 
 }  // extern "C"

@@ -205,5 +205,5 @@ class MoEDecode:
         if st not in (0, 5):
             check(st, "moe_decode_get_error")
         for p in self._products or ():
-            flags.value |= p.get_error(stream)
+            flags.value |= p._latest_error() if stream is None else p.get_error(stream)
         return int(flags.value)

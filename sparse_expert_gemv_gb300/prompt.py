@@ -136,9 +136,16 @@ class GroupedProduct:
 
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits, after waiting for the
-        stream."""
+        handle's latest call and for the stream (the current one if not given)."""
+        return self._error(lib.moe_product_get_error, _stream(stream))
+
+    def _latest_error(self) -> int:
+        """The same, after waiting for the handle's latest call alone."""
+        return self._error(lib.moe_product_get_error_latest)
+
+    def _error(self, read, *stream) -> int:
         flags = ctypes.c_uint32(0)
-        st = lib.moe_product_get_error(self._h, _stream(stream), ctypes.byref(flags))
+        st = read(self._h, *stream, ctypes.byref(flags))
         if st not in (0, 5):
             check(st, "moe_product_get_error")
         return int(flags.value)

@@ -138,3 +138,74 @@ def test_a_stream_is_a_torch_stream(dev):  # noqa: F811
     for name, call in calls(dev).items():
         with pytest.raises((TypeError, AttributeError)):
             call(stream=torch.cuda.Stream().cuda_stream)
+
+
+def test_get_error_waits_for_a_prompt_on_another_stream(dev):  # noqa: F811
+    from sparse_expert_gemv_gb300 import MOE_DEVICE_TIMEOUT
+    layer = small_layer(dev)
+    args = prompt_args(dev, layer, 30)
+    layer.prompt(*args)
+    assert layer.get_error() == 0
+    side, busy = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for product in layer._products:
+        product.arm_timeout()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+        layer.prompt(*args, stream=side)
+        over = side.record_event()
+        with torch.cuda.stream(busy):
+            torch.cuda._sleep(2_000_000_000)
+            end = busy.record_event()
+        assert layer.get_error() == MOE_DEVICE_TIMEOUT
+        # for that call's products, and for no other stream's work
+        assert not end.query()
+        over.synchronize()
+        assert layer.get_error() == 0
+        end.synchronize()
+
+
+def test_product_get_error_waits_for_its_latest_call_and_for_a_replay(dev):  # noqa: F811
+    from sparse_expert_gemv_gb300 import MOE_DEVICE_TIMEOUT
+    c = Products(dev, "mxfp8", 128, 512, [40, 50], 38)
+    args, p = c.args(), c.handle(False)
+    out = torch.empty(c.R, 128, dtype=torch.bfloat16, device=dev)
+    p(*args, out=out)
+    assert p.get_error() == 0
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    p.arm_timeout()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        p(*args, out=out)
+    assert p.get_error() == MOE_DEVICE_TIMEOUT        # from the default stream
+    g = torch.cuda.CUDAGraph()
+    p.arm_timeout()
+    with torch.cuda.graph(g):
+        p(*args, out=out)                              # every replay times out
+    assert p.get_error() == 0
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        g.replay()
+    assert p.get_error(side) == MOE_DEVICE_TIMEOUT
+
+
+def test_reads_of_the_error_word_lose_no_bit(dev):  # noqa: F811
+    # runs that time out and reads of the word from two threads: every timeout is
+    # seen by exactly one read, the one that first follows it
+    import threading
+    from sparse_expert_gemv_gb300 import MOE_DEVICE_TIMEOUT
+    c = Products(dev, "mxfp8", 128, 512, [40], 39)
+    args, p = c.args(), c.handle(False)
+    p(*args)
+    assert p.get_error() == 0
+    seen = []
+    for _ in range(20):
+        p.arm_timeout()
+        p(*args)
+        threads = [threading.Thread(target=lambda: seen.append(p._latest_error())) for _ in range(2)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    assert sorted(seen) == [0] * 20 + [MOE_DEVICE_TIMEOUT] * 20

@@ -56,10 +56,13 @@ def test_a_timeout_marks_both_ctas():
     assert "st.relaxed.cluster.shared::cluster" in body and "(blockIdx.x & 1) ^ 1" in body
 
 
-def test_arm_timeout_refuses_a_null_handle():
+def test_null_handles_are_refused():
+    import ctypes
     import __graft_entry__
     b = __graft_entry__._build_module()
     if b.stale(b.OUT):
         b.build()
     from sparse_expert_gemv_gb300._lib import lib
     assert lib.moe_product_arm_timeout(None) == 1
+    flags = ctypes.c_uint32(7)
+    assert lib.moe_product_get_error_latest(None, ctypes.byref(flags)) == 1 and flags.value == 0
