@@ -118,7 +118,8 @@ moe_status_t moe_product_destroy(moe_product_t handle);
  *   plain     y[q, n] = bf16(sum_K W[e, n, K] * a[q, K])
  *   SILU_MUL  h[q, i] = SiLU(sum W[e, i] a[q]) * (sum W[e, I + i] a[q]),
  *             codes[q], scales[q] = MXFP8(h[q])
- * with FP32 accumulation on the tensor cores' block-scaled 8-bit MMA.
+ * with FP32 accumulation on the tensor cores' block-scaled 8-bit MMA. The
+ * current device has to be the handle's.
  *   R         rows of the output; offsets are read as clamped to [0, R], rows
  *             outside every group are left as they are
  *   A         rows of a

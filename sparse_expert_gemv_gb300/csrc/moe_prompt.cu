@@ -18,6 +18,7 @@
 
 struct moe_product {
   moe_product_config_t cfg;
+  int device;         // where the handle was created
   int num_sms;
   int mt;             // weight tiles of an expert
   CUtensorMap tm_w;
@@ -204,12 +205,16 @@ void mark_done(moe_product* m, cudaStream_t s) {
 moe_status_t read_error(moe_product* m, uint32_t* device_flags) {
   if (m->done_recorded && cudaEventSynchronize(m->done_ev) != cudaSuccess) return MOE_ERR_CUDA;
   const std::lock_guard<std::mutex> turn(m->read_mu);
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(m->device) != cudaSuccess)
+    return MOE_ERR_CUDA;
   moe::moe_product_take_error<<<1, 1, 0, m->aux>>>(m->d_err);
   uint32_t v = 0;
-  if (cudaGetLastError() != cudaSuccess ||
-      cudaMemcpyAsync(&v, m->d_err + 1, 4, cudaMemcpyDeviceToHost, m->aux) != cudaSuccess ||
-      cudaStreamSynchronize(m->aux) != cudaSuccess)
-    return MOE_ERR_CUDA;
+  const bool ok =
+      cudaGetLastError() == cudaSuccess &&
+      cudaMemcpyAsync(&v, m->d_err + 1, 4, cudaMemcpyDeviceToHost, m->aux) == cudaSuccess &&
+      cudaStreamSynchronize(m->aux) == cudaSuccess;
+  if (cudaSetDevice(device) != cudaSuccess || !ok) return MOE_ERR_CUDA;
   *device_flags = v;
   return v ? MOE_ERR_DEVICE_FAULT : MOE_OK;
 }
@@ -317,10 +322,10 @@ moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* 
   const int nk = (c.K + moe::kProdK - 1) / moe::kProdK;
   const int mt2 = (m->mt + 1) / 2 * 2;   // a pair of CTAs takes two tiles
   const int64_t blocks = (int64_t)c.E * mt2 * nk;
-  int dev = 0;
   const bool ok =
-      blocks <= 0x7fffffff && cudaGetDevice(&dev) == cudaSuccess &&
-      cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess &&
+      blocks <= 0x7fffffff && cudaGetDevice(&m->device) == cudaSuccess &&
+      cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, m->device) ==
+          cudaSuccess &&
       cudaMalloc(&m->sfa, (size_t)blocks * moe::kProdSfaBytes) == cudaSuccess &&
       cudaMalloc(&m->d_err, 8) == cudaSuccess &&
       cudaMemsetAsync(m->d_err, 0, 8, static_cast<cudaStream_t>(stream)) == cudaSuccess &&
@@ -365,6 +370,9 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
   if (!aligned(a, 16) || !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(y, 16) ||
       !aligned(codes, 16))
     return MOE_ERR_MISALIGNED;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return MOE_ERR_CUDA;
+  if (device != m->device) return MOE_ERR_INVALID_ARG;
   moe::ProductParams p;
   p.tm_w = m->tm_w;
   if (!rows) {

@@ -52,9 +52,10 @@ const at::Tensor& tensor(PyObject* o, const char* name) {
   return THPVariable_Unpack(o);
 }
 
-// A contiguous CUDA tensor of the given type and, where `shape` is given, shape.
+// A contiguous CUDA tensor of the given type and, where they are given, shape
+// and device (that of `like`).
 const at::Tensor& need(PyObject* o, at::ScalarType dtype, std::optional<at::IntArrayRef> shape,
-                       const char* name) {
+                       const char* name, const at::Tensor* like = nullptr) {
   const at::Tensor& t = tensor(o, name);
   if (t.scalar_type() != dtype)
     raise(PyExc_TypeError, "%s: expected %s, got %s", name, dtype_name(dtype),
@@ -65,14 +66,20 @@ const at::Tensor& need(PyObject* o, at::ScalarType dtype, std::optional<at::IntA
   }
   if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);
   if (!t.is_cuda()) raise(PyExc_ValueError, "%s must be a CUDA tensor", name);
+  if (like && t.device() != like->device()) {
+    const std::string want = like->device().str(), got = t.device().str();
+    raise(PyExc_ValueError, "%s: expected a tensor on %s, got one on %s", name, want.c_str(),
+          got.c_str());
+  }
   return t;
 }
 
-const at::Tensor& matrix(PyObject* o, at::ScalarType dtype, const char* name) {
+const at::Tensor& matrix(PyObject* o, at::ScalarType dtype, const char* name,
+                         const at::Tensor* like = nullptr) {
   const at::Tensor& t = tensor(o, name);
   if (t.dim() != 2)
     raise(PyExc_ValueError, "%s: expected two dimensions, got %lld", name, (long long)t.dim());
-  return need(o, dtype, std::nullopt, name);
+  return need(o, dtype, std::nullopt, name, like);
 }
 
 // The caller's output buffer, or a new one: of the current stream's memory, so
@@ -80,7 +87,7 @@ const at::Tensor& matrix(PyObject* o, at::ScalarType dtype, const char* name) {
 // still be read there, and would return there while this call writes it).
 at::Tensor output(PyObject* o, at::ScalarType dtype, at::IntArrayRef shape, const char* name,
                   const at::Tensor& like) {
-  if (o != Py_None) return need(o, dtype, shape, name);
+  if (o != Py_None) return need(o, dtype, shape, name, &like);
   return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
 }
 
@@ -166,14 +173,14 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 11, [&] {
     const at::Tensor& x = matrix(a[0], at::kBFloat16, "x");
     const int64_t T = x.size(0), H = x.size(1);
-    const at::Tensor& weight = need(a[1], at::kBFloat16, at::IntArrayRef{H}, "weight");
+    const at::Tensor& weight = need(a[1], at::kBFloat16, at::IntArrayRef{H}, "weight", &x);
     const float eps = (float)PyFloat_AsDouble(a[3]);
     if (PyErr_Occurred()) throw Raised{};
     const bool bf16 = truth(a[4]), mxfp8 = truth(a[5]);
     if (!bf16 && !mxfp8)
       raise(PyExc_ValueError, "add_rms_norm: ask for bf16 rows, mxfp8 rows or both");
     at::Tensor residual, sum, y, codes, scales;
-    if (a[2] != Py_None) residual = need(a[2], at::kBFloat16, x.sizes(), "residual");
+    if (a[2] != Py_None) residual = need(a[2], at::kBFloat16, x.sizes(), "residual", &x);
     const c10::cuda::CUDAStreamGuard on(stream_of(a[10], x));
     if (residual.defined() || a[6] != Py_None)
       sum = output(a[6], at::kBFloat16, x.sizes(), "sum", x);
@@ -214,11 +221,12 @@ PyObject* group_by_expert(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 6, [&] {
     const at::Tensor& y = matrix(a[0], at::kBFloat16, "y");
-    const at::Tensor& slots = matrix(a[1], at::kInt, "slots");
+    const at::Tensor& slots = matrix(a[1], at::kInt, "slots", &y);
     const int64_t R = y.size(0), H = y.size(1), T = slots.size(0), k = slots.size(1);
-    const at::Tensor& w = need(a[2], at::kFloat, slots.sizes(), "w");
+    const at::Tensor& w = need(a[2], at::kFloat, slots.sizes(), "w", &y);
     at::Tensor residual;
-    if (a[3] != Py_None) residual = need(a[3], at::kBFloat16, at::IntArrayRef{T, H}, "residual");
+    if (a[3] != Py_None)
+      residual = need(a[3], at::kBFloat16, at::IntArrayRef{T, H}, "residual", &y);
     const c10::cuda::CUDAStreamGuard on(stream_of(a[5], y));
     at::Tensor out = output(a[4], at::kBFloat16, {T, H}, "out", y);
     check(moe_combine(int32_of(T, "T"), int32_of(k, "k"), int32_of(H, "H"), int32_of(R, "R"),
@@ -229,32 +237,38 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (handle, E, N, K, silu_mul, a, a_scales, offsets, rows, out, out_scales, stream)
+// (handle, device, E, N, K, silu_mul, a, a_scales, offsets, rows, out, out_scales, stream)
 //   -> out, or (out, out_scales) with silu_mul
 PyObject* product_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 12, [&]() -> PyObject* {
+  return guarded(n, 13, [&]() -> PyObject* {
     moe_product_t handle = static_cast<moe_product_t>(PyLong_AsVoidPtr(a[0]));
     if (!handle && PyErr_Occurred()) throw Raised{};
-    const int64_t E = int32_of(a[1], "E"), N = int32_of(a[2], "N"), K = int32_of(a[3], "K");
-    const bool silu = truth(a[4]);
-    const at::Tensor& rows_of = matrix(a[5], at::kByte, "a");
+    const int32_t device = int32_of(a[1], "device");
+    const int64_t E = int32_of(a[2], "E"), N = int32_of(a[3], "N"), K = int32_of(a[4], "K");
+    const bool silu = truth(a[5]);
+    const at::Tensor& rows_of = matrix(a[6], at::kByte, "a");
     const int64_t A = rows_of.size(0);
-    need(a[5], at::kByte, at::IntArrayRef{A, K}, "a");
-    const at::Tensor& a_scales = need(a[6], at::kByte, at::IntArrayRef{A, K / 32}, "a_scales");
-    const at::Tensor& offsets = need(a[7], at::kInt, at::IntArrayRef{E + 1}, "offsets");
+    need(a[6], at::kByte, at::IntArrayRef{A, K}, "a");
+    if (rows_of.device().index() != device)
+      raise(PyExc_ValueError, "a: expected a tensor on cuda:%d, where the weights are, got one on %s",
+            (int)device, rows_of.device().str().c_str());
+    const at::Tensor& a_scales =
+        need(a[7], at::kByte, at::IntArrayRef{A, K / 32}, "a_scales", &rows_of);
+    const at::Tensor& offsets =
+        need(a[8], at::kInt, at::IntArrayRef{E + 1}, "offsets", &rows_of);
     at::Tensor rows;
     int64_t R = A;
-    if (a[8] != Py_None) {
-      R = tensor(a[8], "rows").numel();
-      rows = need(a[8], at::kInt, at::IntArrayRef{R}, "rows");
+    if (a[9] != Py_None) {
+      R = tensor(a[9], "rows").numel();
+      rows = need(a[9], at::kInt, at::IntArrayRef{R}, "rows", &rows_of);
     }
-    const c10::cuda::CUDAStreamGuard on(stream_of(a[11], rows_of));
-    at::Tensor out = output(a[9], silu ? at::kByte : at::kBFloat16, {R, silu ? N / 2 : N}, "out",
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[12], rows_of));
+    at::Tensor out = output(a[10], silu ? at::kByte : at::kBFloat16, {R, silu ? N / 2 : N}, "out",
                             rows_of);
     at::Tensor scales;
     if (silu)
-      scales = output(a[10], at::kByte, {R, N / 64}, "out_scales", rows_of);
-    else if (a[10] != Py_None)
+      scales = output(a[11], at::kByte, {R, N / 64}, "out_scales", rows_of);
+    else if (a[11] != Py_None)
       raise(PyExc_ValueError, "out_scales: only a product with silu_mul has scales");
     check(moe_product_run(handle, int32_of(R, "R"), int32_of(A, "A"), data<uint8_t>(rows_of),
                           data<uint8_t>(a_scales), data<int32_t>(offsets), data<int32_t>(rows),

@@ -79,7 +79,8 @@ class GroupedProduct:
     uint8 [E, N, K/32]. With silu_mul the N = 2I rows of an expert are I gate
     rows and I up rows, and the product is finished to MXFP8(SiLU(g) * u).
     The weights are borrowed (kept alive by this object); the scales are
-    copied once into the order in which the tensor cores take them.
+    copied once into the order in which the tensor cores take them, on the
+    weights' device, where the rows of every call have to lie.
     """
 
     def __init__(self, w, w_scales, *, fmt: str = "mxfp8", silu_mul: bool = False, stream=None):
@@ -94,13 +95,18 @@ class GroupedProduct:
         K = RB * per
         _need(w, torch.uint8, (E, N, RB), "w")
         _need(w_scales, torch.uint8, (E, N, K // 32), "w_scales")
+        if w_scales.device != w.device:
+            raise ValueError(f"w_scales: expected a tensor on {w.device}, got one on {w_scales.device}")
+        if stream is not None and stream.device != w.device:
+            raise ValueError(f"stream: expected one of {w.device}, got one of {stream.device}")
         self.E, self.N, self.K, self.fmt, self.silu_mul = E, N, K, fmt, silu_mul
-        self._weights = (w, w_scales)
+        self._weights, self._device = (w, w_scales), w.device.index
         flags = (MOE_FLAG_MXFP4 if fmt == "mxfp4" else 0) | (MOE_PRODUCT_SILU_MUL if silu_mul else 0)
         h = ctypes.c_void_p()
-        check(lib.moe_product_create(ctypes.byref(MoEProductConfig(E, N, K, flags)), _ptr(w),
-                                     _ptr(w_scales), ctypes.byref(h), _stream(stream)),
-              "moe_product_create")
+        with torch.cuda.device(w.device):      # the handle belongs to the weights' device
+            check(lib.moe_product_create(ctypes.byref(MoEProductConfig(E, N, K, flags)), _ptr(w),
+                                         _ptr(w_scales), ctypes.byref(h), _stream(stream)),
+                  "moe_product_create")
         self._h = h
 
     def close(self) -> None:
@@ -125,8 +131,8 @@ class GroupedProduct:
         pair codes uint8 [R, I], scales uint8 [R, I/32]. R is the length of
         `rows`, or A. Rows outside every group are left as they are."""
         h = self._h.value if self._h else 0
-        return _moe_torch.product_run(h, self.E, self.N, self.K, self.silu_mul, a, a_scales,
-                                      offsets, rows, out, out_scales, stream)
+        return _moe_torch.product_run(h, self._device, self.E, self.N, self.K, self.silu_mul, a,
+                                      a_scales, offsets, rows, out, out_scales, stream)
 
     def arm_timeout(self) -> None:
         """Test support: the bounded waits of the next run that launches
@@ -137,7 +143,8 @@ class GroupedProduct:
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits, after waiting for the
         handle's latest call and for the stream (the current one if not given)."""
-        return self._error(lib.moe_product_get_error, _stream(stream))
+        with torch.cuda.device(self._device):
+            return self._error(lib.moe_product_get_error, _stream(stream))
 
     def _latest_error(self) -> int:
         """The same, after waiting for the handle's latest call alone."""

@@ -209,3 +209,14 @@ def test_reads_of_the_error_word_lose_no_bit(dev):  # noqa: F811
         for t in threads:
             t.join()
     assert sorted(seen) == [0] * 20 + [MOE_DEVICE_TIMEOUT] * 20
+
+
+def test_buffers_on_another_device_are_refused(dev):  # noqa: F811
+    from test_prompt_devices_cpu import fake
+    want = {name: listed(call()) for name, call in calls(dev).items()}
+    names = {"norm": ["sum", "y", "codes", "scales"], "group": ["offsets", "rows", "slots"],
+             "combine": ["out"], "product": ["out"], "gate/up": ["out", "out_scales"]}
+    for op, call in calls(dev).items():
+        for name, t in zip(names.get(op, []), want[op]):
+            with pytest.raises(ValueError, match=f"{name}: expected a tensor on cuda:0, got one on cuda:1"):
+                call(**{name: fake(t.shape, t.dtype, 1)})
