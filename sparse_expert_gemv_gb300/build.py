@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -42,13 +43,29 @@ def command(out: str = OUT, extra=()) -> list[str]:
             f"-Xlinker", f"-rpath,{cuda_lib}", "--threads", "0", *extra, *SRCS, "-o", out]
 
 
+def _torch_dir() -> str:
+    return importlib.util.find_spec("torch").submodule_search_locations[0]
+
+
+def torch_version() -> str:
+    """torch.__version__, without importing torch."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return re.search(r"^__version__ = ['\"](.+)['\"]", f.read(), re.M).group(1)
+
+
+def built_for(version: str) -> str:
+    """What the extension module says of the torch it was built with."""
+    return f"built with torch {version}"
+
+
 def binding_commands(obj: str, out: str) -> tuple[list[str], list[str]]:
     """Compile and link commands of the extension module (linked against the
     library beside it)."""
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     cxx = shutil.which("g++") or "c++"
     compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-c", BINDING_SRC, "-o", obj,
+                f'-DMOE_BUILT_FOR="{built_for(torch_version())}"',
                 f"-I{os.path.join(ROOT, 'include')}", f"-I{sysconfig.get_paths()['include']}",
                 f"-I{os.path.join(torch, 'include')}", f"-I{os.path.join(cuda, 'include')}"]
     link = [cxx, "-shared", obj, "-o", out, f"-L{os.path.join(torch, 'lib')}", "-ltorch_python",
@@ -86,9 +103,15 @@ def build(verbose: bool = False, timeline: bool = False) -> str:
 
 
 def stale(path: str) -> bool:
-    """True when `path` is missing or older than a CUDA source or header."""
-    if not os.path.exists(path):
+    """True when `path` is missing or older than a source or header; of the
+    extension module, which build() makes with the library, also when it was
+    built with another torch; and of the library when its module is."""
+    if not os.path.exists(path) or (path == OUT and stale(BINDING_OUT)):
         return True
+    if path == BINDING_OUT:
+        with open(path, "rb") as f:
+            if built_for(torch_version()).encode() + b"\0" not in f.read():
+                return True
     srcs = [os.path.join(HERE, "csrc", f) for f in os.listdir(os.path.join(HERE, "csrc"))]
     srcs += [os.path.join(ROOT, "include", f) for f in os.listdir(os.path.join(ROOT, "include"))]
     return os.path.getmtime(path) < max(os.path.getmtime(f) for f in srcs)

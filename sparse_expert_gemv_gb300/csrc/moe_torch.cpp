@@ -299,4 +299,8 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_moe_torch", nullptr, -1, kMethod
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__moe_torch(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__moe_torch(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "built_for", MOE_BUILT_FOR) < 0) Py_CLEAR(m);
+  return m;
+}

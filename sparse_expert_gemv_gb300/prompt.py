@@ -26,10 +26,17 @@ from typing import NamedTuple
 
 import torch
 
-from . import _moe_torch
 from ._lib import MOE_FLAG_MXFP4, MOE_PRODUCT_SILU_MUL, MoEError, MoEProductConfig, check, lib
 from ._tensors import _need, _ptr, _stream
 
+_BUILD = "build the extension module first (python -c 'import __graft_entry__ as g; g.build()')"
+try:
+    from . import _moe_torch
+except ImportError as e:
+    raise ImportError(f"_moe_torch.so is missing or does not load ({e}): {_BUILD}") from e
+if _moe_torch.built_for != f"built with torch {torch.__version__}":
+    raise ImportError(f"_moe_torch.so was {_moe_torch.built_for}, this is torch {torch.__version__}: "
+                      f"{_BUILD}")
 _moe_torch.set_error(MoEError)
 
 
