@@ -65,15 +65,17 @@ template <int V>
 moe_status_t norm_launch(const moe::NormParams& p, int T, void* stream) {
   const int nv = p.H / V;
   // One vector a thread while few rows are under way, two from 2048 rows or 512
-  // vectors on (smaller blocks, more rows an SM), up to four on 1024 threads
-  // (us with one and with two: 1 row of 2048 1.9 / 2.3, 1024 rows 3.3 / 3.5, 4096
-  // rows of 4096 20.1 / 16.7, 16384 of 2048 39.7 / 37.2, MXFP8 rows out).
+  // vectors on (smaller blocks, more rows an SM), of single values up to 16 on
+  // 1024 threads (us with one and with two: 1 row of 2048 1.9 / 2.3, 1024 rows 3.3
+  // / 3.5, 4096 rows of 4096 20.1 / 16.7, 16384 of 2048 39.7 / 37.2, MXFP8 rows out).
   const bool two = nv > 512 || (nv > 128 && T >= 2048);
   const int threads = nv > 1024 ? 1024 : ((two ? (nv + 1) / 2 : nv) + 31) / 32 * 32;
   const int per = (nv + threads - 1) / threads;
   if (per <= 1) return launch(moe::moe_add_rms_norm_rows<V, 1>, T, threads, 0, stream, 1, p);
-  if (per <= 2) return launch(moe::moe_add_rms_norm_rows<V, 2>, T, threads, 0, stream, 1, p);
-  if (V > 1 || per <= 4) return launch(moe::moe_add_rms_norm_rows<V, 4>, T, threads, 0, stream, 1, p);
+  static_assert(moe::kNormMaxH <= 2 * 1024 * 8, "at most two vectors of eight a thread");
+  if (V > 1 || per <= 2)
+    return launch(moe::moe_add_rms_norm_rows<V, 2>, T, threads, 0, stream, 1, p);
+  if (per <= 4) return launch(moe::moe_add_rms_norm_rows<1, 4>, T, threads, 0, stream, 1, p);
   return launch(moe::moe_add_rms_norm_rows<1, 16>, T, threads, 0, stream, 1, p);
 }
 
