@@ -889,7 +889,11 @@ __global__ void __launch_bounds__(kProdThreads, 1) moe_product_tiles(
             // SiLU with e = exp(-|gate|) <= 1: nothing overflows, and the divisor
             // stays where the short division is good to two units. The short
             // exp is off by 2 + 1.2 |gate| units, far below the 2^-4 that E4M3
-            // keeps; expf costs 1.5% at 2048 tokens, exact division 7%.
+            // keeps. Over eight inputs of 4096 tokens the codes' error against 64
+            // bits is 1.16e-4 so, 1.15e-4 with expf and 1.19e-4 with exact division
+            // as well (the FP32 sum's order decides); at 2048 tokens of 4-bit
+            // weights 8.4e-5, 7.9e-5 and 8.2e-5. Those take 98.3, 100.6, 107.5 us
+            // and 53.8, 55.1, 61.6.
             const float e = __expf(-fabsf(gate));
             h[x] = __fdividef(gate < 0.f ? gate * e : gate, 1.0f + e) * up;
           }

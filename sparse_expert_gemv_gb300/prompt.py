@@ -11,7 +11,9 @@ arithmetic):
     y = down(hc, hs, offsets)                                 # GroupedProduct
     out = combine(y, slots, w, residual=n.sum)
 
-MoEDecode.prompt is the part after the router on a layer's own weights. As in
+MoEDecode.prompt is the part after the router on a layer's own weights. Like
+the rest of the package these are forward operators: inputs that require grad
+are taken as they are, and the results carry no graph. As in
 the decode layer, every call forwards device pointers and a stream to
 libmoe_decode.so; nothing is computed here. The calls a block makes go through
 the extension module _moe_torch (csrc/moe_torch.cpp), which checks the tensors,
@@ -54,8 +56,9 @@ def add_rms_norm(x, weight, residual=None, *, eps: float = 1e-6, bf16: bool = Tr
     """The residual stream s = bf16(x + residual) and s * rsqrt(mean(s^2) + eps) * weight,
     in bf16 (`bf16`), as MXFP8 codes and scales (`mxfp8`), or both.
 
-    x and residual are bf16 [T, H], weight is bf16 [H]. Without a residual, s
-    is x and RmsNorm.sum is None (unless a buffer for it is passed). The
+    x and residual are bf16 [T, H], weight is bf16 [H]. No result requires grad,
+    even where an input (a weight that is a Parameter) does. Without a residual,
+    s is x and RmsNorm.sum is None (unless a buffer for it is passed). The
     buffers sum, y, codes and scales may be passed in; sum may be x or
     residual, which is then updated in place.
     """
@@ -75,7 +78,8 @@ def group_by_expert(ids, E: int, *, offsets=None, rows=None, slots=None, stream=
 def combine(y, slots, w, *, residual=None, out=None, stream=None):
     """out[t] = bf16(residual[t] + sum_j w[t, j] * y[slots[t, j]]) over expert
     rows y bf16 [R, H], slots int32 [T, k] (outside [0, R): nothing) and w
-    float32 [T, k]; residual bf16 [T, H] is optional and may be `out`."""
+    float32 [T, k]; residual bf16 [T, H] is optional and may be `out`. The result
+    carries no graph."""
     return _moe_torch.combine(y, slots, w, residual, out, stream)
 
 
