@@ -26,12 +26,15 @@
 // Two FP32 accumulators in tensor memory let the epilogue of a tile overlap
 // the next tile's MMAs.
 //
-// What bounds it, measured (us a call, E=128 k=8 H=2048 I=768 unless noted): few
-// rows an expert, HBM (gate/up of 8 tokens 31, 5.4 TB/s; of 256 tokens 68, 6.1
-// TB/s); hundreds of rows an expert, the board's power limit, which takes the
-// clock from 2070 MHz to 1820 (gate/up of 2048 tokens, MXFP4, 52 to 55), 1520
-// (4096 tokens 97 to 108) and 1275 (down of 32768 rows, E=32 H=7168 I=2048, 318
-// to 367, 3.0 PFLOP/s): shorter figures from runs too short to reach the limit.
+// What bounds it, measured (us a call, E=128 k=8 H=2048 I=768 unless noted; the
+// shorter figures are of runs too short to reach the board's power limit). Every
+// call takes 5 until its first MMA: offsets, tiles, the first copies. Few rows an
+// expert: HBM (gate/up of 8 tokens 30 to 33, 5.3 TB/s; of 256 tokens 68, 6.1).
+// Hundreds of rows: 420 to 480 cycles a stage, of which its MMAs are 256 to 384,
+// waits for rows and weights 120 to 140 and for scales 30 to 55, at a clock that the
+// power limit takes from 2070 MHz to 1770 (gate/up of 2048 tokens, MXFP4, 54 to 59),
+// 1560 (4096 tokens, 98 to 116) and 1300 (down of 32768 rows, E=32 H=7168 I=2048,
+// 312 to 385, 2.5 to 3.1 PFLOP/s). Rows gathered or contiguous make no difference.
 #pragma once
 
 #include <cuda.h>

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kGroupThreads) moe_group_slots(const GroupPara
 // with read-once loads, 7.3 TB/s). It lets no dependent launch start early: the
 // next one's CTAs would take this one's places (49.9 us then). With few rows a
 // token the writes and the residual are most of the traffic: 16384 tokens of one
-// row of 2592 50 to 57 us, 5 TB/s (83 with registers for eight rows and an uneven
+// row of 2592 50 to 59 us, 5 TB/s (83 with registers for eight rows and an uneven
 // second CTA); two or four tokens a thread are no faster (50, 53).
 // ---------------------------------------------------------------------------
 struct CombineParams {
