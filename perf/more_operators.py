@@ -170,7 +170,7 @@ def prepare(case, seed):
         s["residual"] = (2 * loud * randn(T, H)).to(torch.bfloat16)
         s["post"] = (0.5 + 0.1 * randn(H)).to(torch.bfloat16) if case["post"] else None
         s["pre"] = (1 + 0.1 * randn(H)).to(torch.bfloat16) if case["out"] != "sum" else None
-        shape = {"none": None, "channel": (H,), "row": (T,), "full": (T, H)}[case["gate"]]
+        shape = {"none": None, "channel": (H,), "row": (T, 1), "full": (T, H)}[case["gate"]]
         s["gate"] = None if shape is None else (0.5 + randn(*shape)).to(torch.bfloat16)
         s["scale"] = 0.875
     else:
@@ -262,7 +262,7 @@ def _norm_plain(s):
             gate = 1 / (1 + torch.exp(-gate))
         elif case["gate_fn"] == "tanh":
             gate = torch.tanh(gate)
-        p = p * (gate.unsqueeze(1) if case["gate"] == "row" else gate)
+        p = p * gate
     total = (s["residual"].float() + s["scale"] * p).to(torch.bfloat16)
     out = [total]
     if case["out"] != "sum":
@@ -365,7 +365,7 @@ def _norm_exact(s):
         gate = s["gate"].double()
         gate = {"none": lambda v: v, "sigmoid": torch.sigmoid, "tanh": torch.tanh}[
             case["gate_fn"]](gate)
-        p = p * (gate.view(-1, 1) if case["gate"] == "row" else gate)
+        p = p * gate
     t = s["residual"].double() + s["scale"] * p
     out = [t]
     if case["out"] != "sum":
