@@ -15,6 +15,8 @@ pages (cited per function):
   moe      routing, the dedup schedule, the gate/up and down projections
   prompt   the prompt operators (MXFP8 quantisation, residual norm, grouping,
            ragged expert products, weighted combination)
+  block    the block operators (expert choice with scores, bias and groups, norms
+           around a block's end, dense products with epilogues)
 
 Pins (tests/test_oracle_*.py) tie each function to something other than
 itself: torch's float8 and bfloat16 conversions, exhaustive bit-pattern
@@ -27,10 +29,10 @@ from .mxfp4 import dequantize as dequantize_mxfp4
 from .bf16 import bf16_rne
 from .moe import (silu, route, dedup_schedule, gate_up, down, layer,
                   requantize_mxfp8, layer_classic)
-from . import prompt
+from . import block, prompt
 
 __all__ = [
-    "prompt",
+    "block", "prompt",
     "E4M3", "UE8M0", "e4m3_decode", "ue8m0_decode", "dequantize", "bf16_rne",
     "E2M1", "e2m1_decode", "dequantize_mxfp4",
     "silu", "route", "dedup_schedule", "gate_up", "down", "layer",

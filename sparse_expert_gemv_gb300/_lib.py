@@ -1,5 +1,5 @@
-"""ctypes view of libmoe_decode.so (the C ABI declared in include/moe_decode.h
-and include/moe_prompt.h).
+"""ctypes view of libmoe_decode.so (the C ABI declared in include/moe_decode.h,
+include/moe_prompt.h and include/moe_block.h).
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels. Importing this module fails loudly when the library has not been
@@ -45,6 +45,17 @@ class MoEProductConfig(ctypes.Structure):
     """moe_product_config_t."""
     _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class MoERouteConfig(ctypes.Structure):
+    """moe_route_config_t."""
+    _fields_ = [("E", ctypes.c_int32), ("k", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class MoEDenseConfig(ctypes.Structure):
+    """moe_dense_config_t."""
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
 class MoEError(RuntimeError):
@@ -105,13 +116,25 @@ PROMPT_SIGNATURES = {
 }
 
 
+# the same for include/moe_block.h
+BLOCK_SIGNATURES = {
+    "moe_route_experts": (_st, [ctypes.POINTER(MoERouteConfig), _i32, _p, _p, _p, _p, _p]),
+    "moe_norm_add_norm": (_st, [_i32, _i32, _p, _p, _p, _p, _p, ctypes.c_float, ctypes.c_float,
+                                ctypes.c_float, ctypes.c_uint32, _p, _p, _p, _p, _p]),
+    "moe_dense_create": (_st, [ctypes.POINTER(MoEDenseConfig), _p, _p, ctypes.POINTER(_p)]),
+    "moe_dense_destroy": (_st, [_p]),
+    "moe_dense_run": (_st, [_p, _i32, _p, _p, _p, _i32, _p]),
+    "moe_dense_get_error": (_st, [_p, _p, ctypes.POINTER(ctypes.c_uint32)]),
+}
+
+
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(
             f"{path} is missing: build the CUDA library first "
             "(python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(path)
-    for name, (res, args) in {**SIGNATURES, **PROMPT_SIGNATURES}.items():
+    for name, (res, args) in {**SIGNATURES, **PROMPT_SIGNATURES, **BLOCK_SIGNATURES}.items():
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args

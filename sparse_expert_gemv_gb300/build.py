@@ -1,7 +1,7 @@
 """Build libmoe_decode.so in-tree with nvcc for sm_103a (no cmake; the decode
-layer and the prompt operators are one translation unit each, compiled side by
-side), and with g++ the extension module _moe_torch.so, which passes torch
-tensors to the prompt operators.
+layer, the prompt operators and the block operators are one translation unit
+each, compiled side by side), and with g++ the extension module _moe_torch.so,
+which passes torch tensors to the prompt and block operators.
 
     python -m sparse_expert_gemv_gb300.build
 """
@@ -17,7 +17,7 @@ import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_decode.cu", "moe_prompt.cu")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_decode.cu", "moe_prompt.cu", "moe_block.cu")]
 OUT = os.path.join(HERE, "libmoe_decode.so")
 # the same library with the one-launch kernel's per-CTA timeline compiled in
 # (-DMOE_TIMELINE: globaltimer stamps per CTA and phase, written to a

@@ -300,7 +300,7 @@ __host__ __device__ __forceinline__ bool product_row(bool silu, int N, int m, in
   return i < I;
 }
 
-__global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, uint8_t* out, int N,
+static __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, uint8_t* out, int N,
                                                               int K, int mt, int silu) {
   const int ks = K / 32, nk = (K + kProdK - 1) / kProdK;
   const size_t block = blockIdx.x;            // ((e * mt) + m) * nk + kb
@@ -316,9 +316,6 @@ __global__ void __launch_bounds__(128) moe_product_lay_scales(const uint8_t* s, 
   }
   reinterpret_cast<uint32_t*>(out)[block * 128 + threadIdx.x] = v;
 }
-
-// err[1] = the error word err[0], which is cleared.
-__global__ void moe_product_take_error(uint32_t* err) { err[1] = atomicExch(err, 0u); }
 
 // ---------------------------------------------------------------------------
 // moe_product_tiles

@@ -3,61 +3,32 @@
 #include "moe_prompt.h"
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstddef>
 #include <cstdint>
-#include <mutex>
 #include <new>
 
+#include "moe_host.cuh"
 #include "moe_product.cuh"
 #include "moe_prompt_rows.cuh"
 
-struct moe_product {
+struct moe_product : moe::Handle {
   moe_product_config_t cfg;
-  int device;         // where the handle was created
   int num_sms;
   int mt;             // weight tiles of an expert
   CUtensorMap tm_w;
   uint8_t* sfa;       // the weights' scales in tile order
-  uint32_t* d_err;    // device error word, and where a read of it leaves its value
-  // as the decode layer's handle has them: completion of the latest run outside
-  // a capture, which the reads of the error word wait for, and their own
-  // non-blocking stream; reads take turns
-  cudaEvent_t done_ev;
-  std::atomic<bool> done_recorded;
-  cudaStream_t aux;
-  std::mutex read_mu;
   std::atomic<bool> armed;   // the next run's waits run out (moe_product_arm_timeout)
 };
 
 namespace {
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-template <typename... KArgs, typename... Args>
-moe_status_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
-                    void* stream, unsigned cluster, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) (void)cudaGetLastError();
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
-}
+using moe::aligned;
+using moe::encode;
+using moe::launch;
 
 // ---- norm --------------------------------------------------------------------
 
@@ -136,30 +107,6 @@ int group_cluster_limit() {
 
 // ---- product -----------------------------------------------------------------
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
-bool encode(CUtensorMap* tm, CUtensorMapDataType type, int rank, const void* base,
-            const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
-  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  return fn && fn(tm, type, rank, const_cast<void*>(base), dims, strides, box, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool is_fp4(const moe_product_config_t& c) { return (c.flags & MOE_FLAG_MXFP4) != 0; }
 bool is_silu(const moe_product_config_t& c) { return (c.flags & MOE_PRODUCT_SILU_MUL) != 0; }
 
@@ -190,42 +137,9 @@ bool encode_weights(moe_product* m, const uint8_t* w) {
 
 constexpr size_t kProductSmem = (size_t)moe::ProductSmem::total + 1024;
 
-// After a run has been enqueued on s: record its completion, unless s is being
-// captured into a graph (the event would stand for a graph node then).
-void mark_done(moe_product* m, cudaStream_t s) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return;
-  }
-  if (cs != cudaStreamCaptureStatusNone) return;
-  if (cudaEventRecord(m->done_ev, s) == cudaSuccess) m->done_recorded = true;
-}
-
-// Reads and clears the error word in one step, so that no bit set meanwhile is
-// lost, once the latest run outside a capture is over.
-moe_status_t read_error(moe_product* m, uint32_t* device_flags) {
-  if (m->done_recorded && cudaEventSynchronize(m->done_ev) != cudaSuccess) return MOE_ERR_CUDA;
-  const std::lock_guard<std::mutex> turn(m->read_mu);
-  int device = 0;
-  if (cudaGetDevice(&device) != cudaSuccess || cudaSetDevice(m->device) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  moe::moe_product_take_error<<<1, 1, 0, m->aux>>>(m->d_err);
-  uint32_t v = 0;
-  const bool ok =
-      cudaGetLastError() == cudaSuccess &&
-      cudaMemcpyAsync(&v, m->d_err + 1, 4, cudaMemcpyDeviceToHost, m->aux) == cudaSuccess &&
-      cudaStreamSynchronize(m->aux) == cudaSuccess;
-  if (cudaSetDevice(device) != cudaSuccess || !ok) return MOE_ERR_CUDA;
-  *device_flags = v;
-  return v ? MOE_ERR_DEVICE_FAULT : MOE_OK;
-}
-
 void free_product(moe_product* m) {
-  if (m->done_ev) cudaEventDestroy(m->done_ev);
-  if (m->aux) cudaStreamDestroy(m->aux);
+  m->release();
   cudaFree(m->sfa);
-  cudaFree(m->d_err);
   delete m;
 }
 
@@ -330,10 +244,7 @@ moe_status_t moe_product_create(const moe_product_config_t* cfg, const uint8_t* 
       cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, m->device) ==
           cudaSuccess &&
       cudaMalloc(&m->sfa, (size_t)blocks * moe::kProdSfaBytes) == cudaSuccess &&
-      cudaMalloc(&m->d_err, 8) == cudaSuccess &&
-      cudaMemsetAsync(m->d_err, 0, 8, static_cast<cudaStream_t>(stream)) == cudaSuccess &&
-      cudaEventCreateWithFlags(&m->done_ev, cudaEventDisableTiming) == cudaSuccess &&
-      cudaStreamCreateWithFlags(&m->aux, cudaStreamNonBlocking) == cudaSuccess &&
+      m->acquire(static_cast<cudaStream_t>(stream)) &&
       encode_weights(m, w) &&
       cudaFuncSetAttribute(moe::moe_product_tiles<false>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -415,7 +326,7 @@ moe_status_t moe_product_run(moe_product_t m, int32_t R, int32_t A, const uint8_
   const moe_status_t st =
       launch(silu ? moe::moe_product_tiles<true> : moe::moe_product_tiles<false>, grid,
              moe::kProdThreads, kProductSmem, stream, 2, p);
-  if (st == MOE_OK) mark_done(m, static_cast<cudaStream_t>(stream));
+  if (st == MOE_OK) m->mark_done(static_cast<cudaStream_t>(stream));
   return st;
 }
 
@@ -428,14 +339,14 @@ moe_status_t moe_product_arm_timeout(moe_product_t m) {
 moe_status_t moe_product_get_error_latest(moe_product_t m, uint32_t* device_flags) {
   if (device_flags) *device_flags = 0;
   if (!m || !device_flags) return MOE_ERR_INVALID_ARG;
-  return read_error(m, device_flags);
+  return m->read_error(device_flags);
 }
 
 moe_status_t moe_product_get_error(moe_product_t m, void* stream, uint32_t* device_flags) {
   if (device_flags) *device_flags = 0;
   if (!m || !device_flags) return MOE_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return MOE_ERR_CUDA;
-  return read_error(m, device_flags);
+  return m->read_error(device_flags);
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
-// Argument marshalling of the prompt operators between torch tensors and the
-// C ABI of include/moe_prompt.h, as a CPython extension: the checks of the
+// Argument marshalling of the prompt and block operators between torch tensors
+// and the C ABI of include/moe_prompt.h and include/moe_block.h, as a CPython extension: the checks of the
 // tensors, the allocation of outputs, the current stream, one call. Nothing is
 // computed here. It exists for latency: the smallest calls run 2 to 3 us on the
 // GPU, and the same steps in Python with ctypes took 16.5 us a norm with four
@@ -18,6 +18,7 @@
 #include <optional>
 #include <string>
 
+#include "moe_block.h"
 #include "moe_prompt.h"
 
 namespace {
@@ -279,6 +280,107 @@ PyObject* product_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// (logits, bias, k, groups, top_groups, scale, flags, ids, w, stream) -> (ids, w)
+PyObject* route_experts(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 10, [&] {
+    const at::ScalarType type = tensor(a[0], "logits").scalar_type();
+    const at::Tensor& logits = matrix(a[0], type == at::kBFloat16 ? type : at::kFloat, "logits");
+    const int64_t T = logits.size(0), E = logits.size(1);
+    at::Tensor bias;
+    if (a[1] != Py_None) bias = need(a[1], at::kFloat, at::IntArrayRef{E}, "bias", &logits);
+    const float scale = (float)PyFloat_AsDouble(a[5]);
+    if (PyErr_Occurred()) throw Raised{};
+    moe_route_config_t cfg{int32_of(E, "E"), int32_of(a[2], "k"), int32_of(a[3], "groups"),
+                           int32_of(a[4], "top_groups"), scale, (uint32_t)int32_of(a[6], "flags")};
+    if (type == at::kBFloat16) cfg.flags |= MOE_ROUTE_BF16;
+    if (cfg.k < 1) raise(PyExc_ValueError, "k must be positive");
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[9], logits));
+    at::Tensor ids = output(a[7], at::kInt, {T, cfg.k}, "ids", logits);
+    at::Tensor w = output(a[8], at::kFloat, {T, cfg.k}, "w", logits);
+    check(moe_route_experts(&cfg, int32_of(T, "T"), data<void>(logits), data<float>(bias),
+                            data<int32_t>(ids), data<float>(w), on.current_stream().stream()),
+          "moe_route_experts");
+    return wrap_all(ids, w);
+  });
+}
+
+// (x, residual, post, pre, gate, scale, residual_scale, eps, flags, bf16, mxfp8, sum, y, codes,
+//  scales, stream) -> (sum, y, codes, scales)
+PyObject* norm_add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&] {
+    const at::Tensor& x = matrix(a[0], at::kBFloat16, "x");
+    const int64_t T = x.size(0), H = x.size(1);
+    const at::Tensor& residual = need(a[1], at::kBFloat16, x.sizes(), "residual", &x);
+    at::Tensor post, pre, gate, sum, y, codes, scales;
+    if (a[2] != Py_None) post = need(a[2], at::kBFloat16, at::IntArrayRef{H}, "post_weight", &x);
+    if (a[3] != Py_None) pre = need(a[3], at::kBFloat16, at::IntArrayRef{H}, "pre_weight", &x);
+    float f[3];
+    for (int i = 0; i < 3; ++i) {
+      f[i] = (float)PyFloat_AsDouble(a[5 + i]);
+      if (PyErr_Occurred()) throw Raised{};
+    }
+    uint32_t flags = (uint32_t)int32_of(a[8], "flags");
+    if (a[4] != Py_None) {   // by its shape: a value per channel, per row or per element
+      gate = tensor(a[4], "gate");
+      if (gate.sizes() == at::IntArrayRef{T, H})
+        flags |= MOE_NORM_GATE_FULL;
+      else if (gate.sizes() == at::IntArrayRef{T, 1})
+        flags |= MOE_NORM_GATE_ROW;
+      else if (gate.sizes() != at::IntArrayRef{H}) {
+        const std::string got = c10::str(gate.sizes());
+        raise(PyExc_ValueError, "gate: expected a value per channel [H], row [T, 1] or element [T, H], got %s",
+              got.c_str());
+      }
+      need(a[4], at::kBFloat16, std::nullopt, "gate", &x);
+    }
+    const bool bf16 = truth(a[9]), mxfp8 = truth(a[10]);
+    if (pre.defined() && !bf16 && !mxfp8)
+      raise(PyExc_ValueError, "norm_add_norm: ask for bf16 rows, mxfp8 rows or both");
+    if (!pre.defined() && mxfp8)
+      raise(PyExc_ValueError, "norm_add_norm: mxfp8 rows need a pre_weight");
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[15], x));
+    sum = output(a[11], at::kBFloat16, x.sizes(), "sum", x);
+    if (bf16 && pre.defined()) y = output(a[12], at::kBFloat16, x.sizes(), "y", x);
+    if (mxfp8) {
+      codes = output(a[13], at::kByte, x.sizes(), "codes", x);
+      scales = output(a[14], at::kByte, {T, H / 32}, "scales", x);
+    }
+    check(moe_norm_add_norm(int32_of(T, "T"), int32_of(H, "H"), data<uint16_t>(x),
+                            data<uint16_t>(residual), data<uint16_t>(post), data<uint16_t>(pre),
+                            data<uint16_t>(gate), f[0], f[1], f[2], flags, data<uint16_t>(sum),
+                            data<uint16_t>(y), data<uint8_t>(codes), data<uint8_t>(scales),
+                            on.current_stream().stream()),
+          "moe_norm_add_norm");
+    return wrap_all(sum, y, codes, scales);
+  });
+}
+
+// (handle, device, K, M, x, residual, out, float32, stream) -> out
+PyObject* dense_run(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 9, [&] {
+    moe_dense_t handle = static_cast<moe_dense_t>(PyLong_AsVoidPtr(a[0]));
+    if (!handle && PyErr_Occurred()) throw Raised{};
+    const int32_t device = int32_of(a[1], "device");
+    const int64_t K = int32_of(a[2], "K"), M = int32_of(a[3], "M");
+    const at::Tensor& x = matrix(a[4], at::kBFloat16, "x");
+    const int64_t R = x.size(0);
+    need(a[4], at::kBFloat16, at::IntArrayRef{R, K}, "x");
+    if (x.device().index() != device)
+      raise(PyExc_ValueError, "x: expected a tensor on cuda:%d, where the weight is, got one on %s",
+            (int)device, x.device().str().c_str());
+    at::Tensor residual;
+    if (a[5] != Py_None)
+      residual = need(a[5], at::kBFloat16, at::IntArrayRef{R, M}, "residual", &x);
+    const bool float32 = truth(a[7]);
+    const c10::cuda::CUDAStreamGuard on(stream_of(a[8], x));
+    at::Tensor out = output(a[6], float32 ? at::kFloat : at::kBFloat16, {R, M}, "out", x);
+    check(moe_dense_run(handle, int32_of(R, "R"), data<uint16_t>(x), data<uint16_t>(residual),
+                        data<void>(out), float32, on.current_stream().stream()),
+          "moe_dense_run");
+    return wrap(out);
+  });
+}
+
 // (MoEError): the exception of a refused call, made from (status, what)
 PyObject* set_error(PyObject*, PyObject* error) {
   Py_INCREF(error);
@@ -291,6 +393,9 @@ PyMethodDef kMethods[] = {
     {"group_by_expert", (PyCFunction)(void (*)(void))group_by_expert, METH_FASTCALL, nullptr},
     {"combine", (PyCFunction)(void (*)(void))combine, METH_FASTCALL, nullptr},
     {"product_run", (PyCFunction)(void (*)(void))product_run, METH_FASTCALL, nullptr},
+    {"route_experts", (PyCFunction)(void (*)(void))route_experts, METH_FASTCALL, nullptr},
+    {"norm_add_norm", (PyCFunction)(void (*)(void))norm_add_norm, METH_FASTCALL, nullptr},
+    {"dense_run", (PyCFunction)(void (*)(void))dense_run, METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
