@@ -58,6 +58,11 @@ class MoEDenseConfig(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32), ("activation", ctypes.c_int32)]
 
 
+class MoEDensePlan(ctypes.Structure):
+    """moe_dense_plan_t: how moe_dense_plan cuts a run."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("split", "nt", "parts", "stages", "smem", "ctas")]
+
+
 class MoEError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
@@ -125,6 +130,9 @@ BLOCK_SIGNATURES = {
     "moe_dense_destroy": (_st, [_p]),
     "moe_dense_run": (_st, [_p, _i32, _p, _p, _p, _i32, _p]),
     "moe_dense_get_error": (_st, [_p, _p, ctypes.POINTER(ctypes.c_uint32)]),
+    "moe_dense_plan": (_st, [ctypes.POINTER(MoEDenseConfig), _i32, _i32,
+                             ctypes.POINTER(MoEDensePlan)]),
+    "moe_dense_arm_timeout": (_st, [_p]),
 }
 
 

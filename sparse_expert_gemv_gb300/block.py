@@ -151,6 +151,12 @@ class DenseProduct:
         return _moe_torch.dense_run(h, self._device, self.K, self.M, x, residual, out, float32,
                                     stream)
 
+    def arm_timeout(self) -> None:
+        """Test support: the bounded waits of the next run that launches
+        something run out (it sets MOE_DEVICE_TIMEOUT, which get_error
+        reports)."""
+        check(lib.moe_dense_arm_timeout(self._h), "moe_dense_arm_timeout")
+
     def get_error(self, stream=None) -> int:
         """Read and clear the handle's device error bits, after waiting for the
         handle's latest call and for the stream (the current one if not given)."""

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -17,8 +18,10 @@
 
 struct moe_dense : moe::Handle {
   moe_dense_config_t cfg;
-  const uint16_t* weight;
+  int num_sms;
+  CUtensorMap tm_w;
   const uint16_t* bias;
+  std::atomic<bool> armed;   // the next run's waits run out (moe_dense_arm_timeout)
 };
 
 namespace {
@@ -49,6 +52,103 @@ moe_status_t norm_pair_launch(const moe::NormPairParams& p, int T, void* stream)
     return launch(moe::moe_norm_add_norm_rows<V, 2>, T, threads, 0, stream, 1, p);
   if (per <= 4) return launch(moe::moe_norm_add_norm_rows<1, 4>, T, threads, 0, stream, 1, p);
   return launch(moe::moe_norm_add_norm_rows<1, 16>, T, threads, 0, stream, 1, p);
+}
+
+// ---- dense products ------------------------------------------------------------
+
+bool is_silu(const moe_dense_config_t& c) { return c.activation == MOE_ACT_SILU_MUL; }
+
+// bf16 [rows, K] in boxes of `box` rows by one stage of K
+bool encode_rows(CUtensorMap* tm, const void* base, int rows, int K, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
+  const cuuint32_t b[2] = {moe::kDenseK, (cuuint32_t)box};
+  return moe::encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, b);
+}
+
+// How a call is cut.
+struct DensePlan {
+  bool split;
+  int nt;       // rows of x a tile
+  int S;        // parts of K (split)
+  int stages;   // of the ring (split)
+  double cycles;
+};
+
+// Shared memory of a CTA of moe_dense_split. Two fit on an SM, so that clusters
+// find room wherever an SM is left, and no third: the tensor memory of two is
+// never more than there is, so none waits for it while it holds up its cluster.
+constexpr int kSplitSmemMax = 113 * 1024, kSplitSmemMin = 78 * 1024;
+
+int split_stages(bool silu, int nt, int S) {
+  const int room = kSplitSmemMax - 1024 - moe::kSplitBars - moe::split_sum_bytes(silu, nt, S);
+  return std::min(16, room / moe::split_stage_bytes(silu, nt));
+}
+
+// The cheapest cut by a model of its cycles: a stage takes its MMAs or, where
+// that is longer, its bytes' way into an SM; whole rounds over the SMs.
+DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
+  const bool silu = is_silu(c);
+  const int M = silu ? c.N / 2 : c.N, two = silu ? 2 : 1;
+  const int nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
+  DensePlan best{false, 0, 1, 0, 0.0};
+  auto take = [&](const DensePlan& p) {
+    if (!best.nt || p.cycles < best.cycles) best = p;
+  };
+  const int pairs = std::max(1, num_sms / 2);
+  for (int nt = moe::kDenseCols / two; nt >= 32; nt -= 32) {
+    const double tiles = std::ceil(M / 256.0) * std::ceil((double)R / nt);
+    const double stage = std::max(2.0 * two * nt, (128 * two + nt / 2) * 128 / 72.0);
+    take({false, nt, 1, 0, std::ceil(tiles / pairs) * nk * stage + 4000 + 12.0 * nt});
+  }
+  for (int nt = moe::kSplitMaxCols; nt >= 16; nt -= 16)
+    for (int S = 1; S <= 8 && S <= nk; S *= 2) {
+      const int stages = split_stages(silu, nt, S);
+      if (stages < 2) continue;
+      const double ctas = std::ceil(M / 128.0) * std::ceil((double)R / nt) * S;
+      const double stage = std::max(1.0 * two * nt, (128 * two + nt) * 128 / 60.0);
+      take({true, nt, S, stages,
+            std::ceil(ctas / num_sms) * std::ceil((double)nk / S) * stage + 3000 + 12.0 * nt / S +
+                (S > 1 ? 1200 : 0)});
+    }
+  return best;
+}
+
+size_t split_smem(bool silu, const DensePlan& p) {
+  const int need = 1024 + moe::kSplitBars + p.stages * moe::split_stage_bytes(silu, p.nt) +
+                   moe::split_sum_bytes(silu, p.nt, p.S);
+  return std::max(need, kSplitSmemMin);
+}
+
+constexpr size_t kDenseSmem[2] = {moe::DenseSmem<false>::total + 1024,
+                                  moe::DenseSmem<true>::total + 1024};
+
+template <bool SILU>
+bool set_dense_attributes() {
+  return cudaFuncSetAttribute(moe::moe_dense_tiles<SILU>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)kDenseSmem[SILU]) == cudaSuccess &&
+         cudaFuncSetAttribute(moe::moe_dense_split<SILU>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kSplitSmemMax) == cudaSuccess;
+}
+
+moe_status_t check_dense(const moe_dense_config_t& c) {
+  if (c.N < 1 || c.K < 1 || c.activation < MOE_ACT_NONE || c.activation > MOE_ACT_SILU_MUL)
+    return MOE_ERR_INVALID_ARG;
+  return c.K % 8 || (is_silu(c) && c.N % 2) ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+}
+
+// Tiles along M and R and the CTAs of a launch; false when there are too many.
+bool dense_grid(const moe_dense_config_t& c, const DensePlan& p, int R, int num_sms, int& mt, int& tt,
+                int& ctas) {
+  const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = p.split ? 128 : 256;
+  const int64_t m = (M + rows - 1) / rows, t = ((int64_t)R + p.nt - 1) / p.nt;
+  if (m * t * p.S > 0x3fffffff) return false;
+  mt = (int)m;
+  tt = (int)t;
+  ctas = (int)(p.split ? m * t * p.S : 2 * std::min<int64_t>(std::max(1, num_sms / 2), m * t));
+  return true;
 }
 
 void free_dense(moe_dense* m) {
@@ -149,17 +249,20 @@ moe_status_t moe_dense_create(const moe_dense_config_t* cfg, const uint16_t* wei
   if (out) *out = nullptr;
   if (!cfg || !out || !weight) return MOE_ERR_INVALID_ARG;
   const moe_dense_config_t c = *cfg;
-  if (c.N < 1 || c.K < 1 || c.activation < MOE_ACT_NONE || c.activation > MOE_ACT_SILU_MUL)
-    return MOE_ERR_INVALID_ARG;
-  if (c.K % 8 || (c.activation == MOE_ACT_SILU_MUL && c.N % 2)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  const moe_status_t st = check_dense(c);
+  if (st != MOE_OK) return st;
   if (!aligned(weight, 16) || !aligned(bias, 2)) return MOE_ERR_MISALIGNED;
   moe_dense* m = new (std::nothrow) moe_dense();
   if (!m) return MOE_ERR_CUDA;
   m->cfg = c;
-  m->weight = weight;
   m->bias = bias;
-  const bool ok = cudaGetDevice(&m->device) == cudaSuccess && m->acquire(nullptr) &&
-                  cudaStreamSynchronize(nullptr) == cudaSuccess;
+  const bool ok =
+      cudaGetDevice(&m->device) == cudaSuccess &&
+      cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, m->device) ==
+          cudaSuccess &&
+      encode_rows(&m->tm_w, weight, c.N, c.K, moe::kDenseRows) &&
+      (is_silu(c) ? set_dense_attributes<true>() : set_dense_attributes<false>()) &&
+      m->acquire(nullptr) && cudaStreamSynchronize(nullptr) == cudaSuccess;
   if (!ok) {
     (void)cudaGetLastError();
     free_dense(m);
@@ -185,22 +288,61 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   if (cudaGetDevice(&device) != cudaSuccess) return MOE_ERR_CUDA;
   if (device != m->device) return MOE_ERR_INVALID_ARG;
   const moe_dense_config_t& c = m->cfg;
+  const bool silu = is_silu(c);
+  const DensePlan plan = plan_dense(c, R, m->num_sms);
   moe::DenseParams p;
-  p.x = x;
-  p.w = m->weight;
+  p.M = silu ? c.N / 2 : c.N;
+  p.nt = plan.nt;
+  p.nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
+  int ctas;
+  if (!dense_grid(c, plan, R, m->num_sms, p.mt, p.tt, ctas)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  p.tm_w = m->tm_w;
+  if (!encode_rows(&p.tm_x, x, R, c.K, plan.split ? plan.nt : plan.nt / 2)) return MOE_ERR_CUDA;
   p.bias = m->bias;
   p.residual = residual;
   p.out = out;
+  p.err = m->d_err;
   p.R = R;
-  p.N = c.N;
-  p.K = c.K;
-  p.M = c.activation == MOE_ACT_SILU_MUL ? c.N / 2 : c.N;
   p.act = c.activation;
   p.out_float = out_float != 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  moe::moe_dense_simple<<<dim3((p.M + 63) / 64, (R + 63) / 64), 256, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
-  m->mark_done(s);
+  p.vec = p.M % 8 == 0 && aligned(out, 16) && aligned(residual, 16);
+  p.stages = plan.stages;
+  const bool armed = m->armed.exchange(false, std::memory_order_relaxed);
+  p.polls = armed ? 50 : moe::kMbarPolls;   // a millisecond
+  p.withheld = armed;
+  moe_status_t st;
+  if (plan.split)
+    st = launch(silu ? moe::moe_dense_split<true> : moe::moe_dense_split<false>, ctas,
+                moe::kSplitThreads, split_smem(silu, plan), stream, plan.S, p, plan.S);
+  else
+    st = launch(silu ? moe::moe_dense_tiles<true> : moe::moe_dense_tiles<false>, ctas,
+                moe::kDenseThreads, kDenseSmem[silu], stream, 2, p);
+  if (st == MOE_OK) m->mark_done(static_cast<cudaStream_t>(stream));
+  return st;
+}
+
+moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t num_sms,
+                            moe_dense_plan_t* out) {
+  if (!cfg || !out || R < 1 || num_sms < 1) return MOE_ERR_INVALID_ARG;
+  const moe_status_t st = check_dense(*cfg);
+  if (st != MOE_OK) return st;
+  const bool silu = is_silu(*cfg);
+  const DensePlan p = plan_dense(*cfg, R, num_sms);
+  int mt, tt, ctas;
+  if (!dense_grid(*cfg, p, R, num_sms, mt, tt, ctas)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  out->split = p.split;
+  out->nt = p.nt;
+  out->parts = p.S;
+  out->stages = p.split ? p.stages
+                        : silu ? moe::DenseSmem<true>::stages : moe::DenseSmem<false>::stages;
+  out->smem = (int)(p.split ? split_smem(silu, p) : kDenseSmem[silu]);
+  out->ctas = ctas;
+  return MOE_OK;
+}
+
+moe_status_t moe_dense_arm_timeout(moe_dense_t m) {
+  if (!m) return MOE_ERR_INVALID_ARG;
+  m->armed.store(true, std::memory_order_relaxed);
   return MOE_OK;
 }
 

@@ -1,92 +1,683 @@
 // Dense matrix products of bf16 rows with bias, activation and residual in the
-// epilogue.
+// epilogue, on the tensor cores (tcgen05.mma kind::f16, FP32 accumulators in
+// tensor memory, operands staged by TMA).
+//
+// Operands are swapped, as in the grouped product: weight rows are the MMA's M
+// dimension and the caller's rows its N dimension, so that a handful of rows
+// still fills a tile and a call's rows can be cut to any multiple of 16.
+//
+//   moe_dense_tiles  many rows: a persistent pair of CTAs (cta_group::2) a pair
+//                    of SMs over tiles of 256 weight rows by up to 256 rows
+//   moe_dense_split  few rows: a cluster of CTAs (cta_group::1) a tile of 128
+//                    weight rows, each over a part of K; the parts meet in
+//                    distributed shared memory and are added in a fixed order
 #pragma once
 
-#include <cuda_runtime.h>
+#include <cuda.h>
 
 #include <cstdint>
 
 #include "moe_block.h"
 #include "moe_device.cuh"
+#include "moe_product.cuh"
+#include "moe_tcgen05.cuh"
 
 namespace moe {
 
-// SiLU with e = exp(-|v|) <= 1: nothing overflows.
-__device__ __forceinline__ float dense_silu(float v) {
-  const float e = expf(-fabsf(v));
-  return (v < 0.f ? v * e : v) / (1.f + e);
-}
-
-__device__ __forceinline__ float dense_act(int act, float v) {
-  switch (act) {
-    case MOE_ACT_RELU: return v > 0.f ? v : v != v ? v : 0.f;
-    case MOE_ACT_SILU: return dense_silu(v);
-    case MOE_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-    case MOE_ACT_GELU_TANH:
-      return 0.5f * v * (1.f + tanhf(0.79788456080286536f * (v + 0.044715f * v * v * v)));
-    default: return v;
-  }
-}
+constexpr int kDenseRows = 128;   // weight rows a CTA
+constexpr int kDenseK = 64;       // K elements a stage: one 128-byte swizzle row
+constexpr int kDenseABytes = kDenseRows * kDenseK * 2;
+constexpr int kDenseCols = 256;   // rows of x a tile of moe_dense_tiles, at most
 
 struct DenseParams {
-  const uint16_t* x;         // [R, K]
-  const uint16_t* w;         // [N, K]
-  const uint16_t* bias;      // or null
-  const uint16_t* residual;  // or null
+  CUtensorMap tm_w;          // boxes of 128 rows
+  CUtensorMap tm_x;          // boxes of nt / 2 rows (tiles), nt rows (split)
+  const uint16_t* bias;      // [N] or null
+  const uint16_t* residual;  // [R, M] or null
   void* out;                 // [R, M]
-  int R, N, K, M, act, out_float;
+  uint32_t* err;
+  int R, M, nk;              // nk: stages K takes
+  int act, out_float;
+  int vec;                   // rows of out and residual take 16-byte accesses
+  int nt;                    // rows of x a tile
+  int mt, tt;                // tiles along M and R
+  int stages;                // of the ring (split)
+  uint32_t polls;            // of a bounded wait: kMbarPolls
+  uint32_t withheld;         // 1: stages lack an arrival, so that waits run out (tests)
 };
 
-// The plain form: tiles of 64 x 64 outputs, FP32 FMAs from shared memory.
-__global__ void __launch_bounds__(256) moe_dense_simple(const DenseParams p) {
-  __shared__ float xs[16][65], ws[2][16][65];
-  const int silu_mul = p.act == MOE_ACT_SILU_MUL;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int m0 = blockIdx.x * 64, r0 = blockIdx.y * 64;
-  float acc[2][4][4] = {};
-  pdl_wait();
-  for (int k0 = 0; k0 < p.K; k0 += 16) {
-    for (int i = threadIdx.x; i < 64 * 16; i += 256) {
-      const int k = i & 15, r = i >> 4;
-      const bool in = k0 + k < p.K;
-      auto get = [&](const uint16_t* a, int row, int rows) {
-        return in && row < rows ? __uint_as_float((uint32_t)a[(size_t)row * p.K + k0 + k] << 16) : 0.f;
-      };
-      xs[k][r] = get(p.x, r0 + r, p.R);
-      ws[0][k][r] = get(p.w, m0 + r, p.M);
-      if (silu_mul) ws[1][k][r] = m0 + r < p.M ? get(p.w, p.M + m0 + r, p.N) : 0.f;
-    }
-    __syncthreads();
-    for (int k = 0; k < 16; ++k)
-      for (int h = 0; h <= silu_mul; ++h)
+// ---------------------------------------------------------------------------
+// activations
+// ---------------------------------------------------------------------------
+
+// SiLU with e = exp(-|v|) <= 1: nothing overflows, and the divisor stays where
+// the short division is good to two units. The short exp is off by 2 + 1.2 |v|
+// units of 2^-23.
+__device__ __forceinline__ float dense_silu(float v) {
+  const float e = __expf(-fabsf(v));
+  return __fdividef(v < 0.f ? v * e : v, 1.f + e);
+}
+// v (1 + tanh z) / 2 = v sigmoid(2 z), the same way
+__device__ __forceinline__ float dense_gelu_tanh(float v) {
+  const float z2 = 1.5957691216057308f * v * fmaf(0.044715f * v, v, 1.f);
+  const float e = __expf(-fabsf(z2));
+  return __fdividef(z2 < 0.f ? v * e : v, 1.f + e);
+}
+__device__ __forceinline__ float dense_gelu(float v) {
+  return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+}
+// (NaN stays NaN)
+__device__ __forceinline__ float dense_relu(float v) { return v < 0.f ? 0.f : v; }
+
+// One switch for all of a thread's values.
+template <int N>
+__device__ __forceinline__ void dense_act(int act, float (&v)[N]) {
+  if (act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i) v[i] = dense_relu(v[i]);
+  } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            acc[h][i][j] = fmaf(xs[k][ty + 16 * i], ws[h][k][tx + 16 * j], acc[h][i][j]);
-    __syncthreads();
+    for (int i = 0; i < N; ++i) v[i] = dense_silu(v[i]);
+  } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = dense_gelu(v[i]);
+  } else if (act == MOE_ACT_GELU_TANH) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = dense_gelu_tanh(v[i]);
   }
-  auto bf16 = [](uint16_t v) { return __uint_as_float((uint32_t)v << 16); };
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = r0 + ty + 16 * i, m = m0 + tx + 16 * j;
-      if (r >= p.R || m >= p.M) continue;
-      float v = acc[0][i][j] + (p.bias ? bf16(p.bias[m]) : 0.f);
-      if (silu_mul) {
-        const float up = acc[1][i][j] + (p.bias ? bf16(p.bias[p.M + m]) : 0.f);
-        v = dense_silu(v) * up;
-      } else {
-        v = dense_act(p.act, v);
-      }
-      const size_t at = (size_t)r * p.M + m;
-      if (p.residual) v += bf16(p.residual[at]);
-      if (p.out_float)
-        static_cast<float*>(p.out)[at] = v;
-      else
-        static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rn(v);
+}
+
+__device__ __forceinline__ float bf16_at(const uint16_t* p) {
+  return __uint_as_float((uint32_t)*p << 16);
+}
+
+namespace tc {
+
+// D (+)= A * B^T, both in shared memory, over both CTAs of a pair or in one.
+template <bool PAIR>
+__device__ __forceinline__ void mma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t" MOE_ELECT
+        ".reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t" MOE_ELECT
+        ".reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f16: FP32 D, bf16 A and B, both K-major.
+__device__ __forceinline__ uint32_t f16_idesc(int m, int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void commit1(uint64_t* bar) {
+  asm volatile(
+      "{\n\t" MOE_ELECT
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma1_load_2d(void* dst, const void* tmap, int x, int y,
+                                             uint64_t* bar) {
+  asm volatile(
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The inverse of stm4_trans.
+__device__ __forceinline__ void ldm4_trans(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+
+}  // namespace tc
+
+// The two halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// A whole warp's bounded wait on a phase of this CTA's mbarrier; a timeout
+// marks the CTA dead, and with PAIR the other one of its pair (every role winds
+// down).
+template <bool PAIR>
+__device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const DenseParams& p,
+                                           volatile int* dead) {
+  constexpr Arrivals A = PAIR ? Arrivals::kPair : Arrivals::kOwn;
+  if (__all_sync(kFull, prod_look<A>(bar, parity))) return true;
+#pragma unroll 1
+  for (uint32_t it = 0; it < p.polls; ++it) {
+    if (__any_sync(kFull, *dead)) return false;
+    if (__all_sync(kFull, prod_poll<A>(bar, parity))) return true;
+  }
+  atomicOr(p.err, kDeviceTimeout);
+  *dead = 1;
+  if constexpr (PAIR)
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;" ::"r"(
+                     tc::cluster_addr(const_cast<int*>(dead), (blockIdx.x & 1) ^ 1))
+                 : "memory");
+  return false;
+}
+
+// ---------------------------------------------------------------------------
+// moe_dense_tiles. Roles:
+//   warp 0      weights and rows by TMA
+//   warp 1      (first CTA) the MMAs of both CTAs
+//   warps 4-11  epilogue, one per lane quarter of tensor memory, two groups of
+//               four that take chunks of 32 rows in turn
+// Two accumulators in tensor memory let the epilogue of a tile overlap the next
+// tile's MMAs. With SILU a tile is 256 gate rows, the 256 up rows of the same
+// neurons and up to 128 rows of x, and an accumulator holds both.
+// ---------------------------------------------------------------------------
+constexpr int kDenseThreads = 384;
+constexpr int kDenseChunk = 32 * 256;   // epilogue staging: 32 rows of 128 bf16
+
+template <bool SILU>
+struct DenseSmem {
+  static constexpr int cols = SILU ? kDenseCols / 2 : kDenseCols;   // rows of x a tile, at most
+  static constexpr int stages = SILU ? 5 : 6;
+  static constexpr int stage = (SILU ? 2 : 1) * kDenseABytes + cols / 2 * kDenseK * 2;
+  static constexpr int chunks = SILU ? 1 : 2;              // a group's, in turn
+  static constexpr int out = stages * stage;               // [2 groups][chunks]
+  static constexpr int bars = out + 2 * chunks * kDenseChunk;
+  static constexpr int total = bars + (2 * stages + 5) * 8 + 16;
+};
+static_assert(DenseSmem<false>::total + 1024 <= 232448 && DenseSmem<true>::total + 1024 <= 232448,
+              "shared memory of a CTA");
+
+// Tile i of a call: bands of kDenseBand token tiles, within a band all token
+// tiles of a weight tile in turn, so that pairs side by side share both
+// operands in L2.
+constexpr int kDenseBand = 8;
+__device__ __forceinline__ void dense_tile(const DenseParams& p, int i, int& m, int& t) {
+  const int band = i / (kDenseBand * p.mt), j = i - band * kDenseBand * p.mt;
+  const int g = min(kDenseBand, p.tt - band * kDenseBand);
+  m = j / g;
+  t = band * kDenseBand + j - m * g;
+}
+
+template <bool SILU>
+__global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
+    const __grid_constant__ DenseParams p) {
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  using L = DenseSmem<SILU>;
+  constexpr int kA = (SILU ? 2 : 1) * kDenseABytes;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
+  uint64_t* empty = full + L::stages;
+  uint64_t* d_full = empty + L::stages;
+  uint64_t* d_empty = d_full + 2;                                 // used in the first CTA
+  uint64_t* drain = d_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x & 1;   // clusters are pairs of neighbours
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  const int tiles = p.mt * p.tt;
+
+  if (warp == 0 && lane == 0) {
+    tc::prefetch_tmap(&p.tm_w);
+    tc::prefetch_tmap(&p.tm_x);
+    for (int i = 0; i < L::stages; ++i) {
+      mbar_init(&full[i], 1 + p.withheld);   // the announcement of both CTAs' bytes
+      mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 16);   // both CTAs' epilogue warps
+    }
+    mbar_init(drain, 1);
+    *dead = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tc::tmem_alloc2(tmem_slot, 512);
+  tc::fence_before();
+  __syncthreads();
+  cluster_sync();   // the other CTA's barriers are ready too
+  tc::fence_after();
+  pdl_trigger();   // the next kernel's prologue may run beside this one
+  // all of tensor memory is this CTA's, so its columns start at 0
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- copies
+    RingPos rg(L::stages);
+    const uint32_t full0 = tc::cluster_addr(full, 0);
+    const int half = p.nt / 2;
+    const uint32_t bytes = 2 * (kA + half * kDenseK * 2);
+    auto weights = [&](int s, int m, int kb) {
+      uint8_t* dst = smem + s * L::stage;
+      const int n = (2 * m + rank) * kDenseRows;
+      if (rank == 0) tc::expect(&full[s], bytes);
+      tc::tma2_load_2d(dst, &p.tm_w, kb * kDenseK, n, full0 + 8 * s);
+      if (SILU)
+        tc::tma2_load_2d(dst + kDenseABytes, &p.tm_w, kb * kDenseK, p.M + n, full0 + 8 * s);
+    };
+    // the first stages' weights, which no earlier kernel writes, come before the
+    // wait for the kernels before this one
+    int ahead = 0, m, t;
+    if (first < tiles) {
+      dense_tile(p, first, m, t);
+      for (; ahead < min(p.nk, L::stages); ++ahead) weights(ahead, m, ahead);
+    }
+    pdl_wait();
+    int g = 0;
+    bool ok = true;
+    for (int i = first; ok && i < tiles; i += step) {
+      dense_tile(p, i, m, t);
+      const int r0 = t * p.nt + rank * half;
+      for (int kb = 0; kb < p.nk; ++kb, ++g) {
+        const int s = rg.slot;
+        if (g >= L::stages && !dense_wait<true>(&empty[s], rg.phase ^ 1u, p, dead)) {
+          ok = false;
+          break;
+        }
+        if (g >= ahead) weights(s, m, kb);
+        tc::tma2_load_2d(smem + s * L::stage + kA, &p.tm_x, kb * kDenseK, r0, full0 + 8 * s);
+        rg.next();
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (rank == 0) {
+      RingPos rg(L::stages);
+      const uint32_t idesc = tc::f16_idesc(2 * kDenseRows, p.nt);
+      int lt = 0;
+      bool ok = true;
+      for (int i = first; ok && i < tiles; i += step, ++lt) {
+        const int buf = lt & 1;
+        if (lt >= 2) ok = dense_wait<true>(&d_empty[buf], ((lt >> 1) - 1) & 1, p, dead);
+        if (!ok) break;
+        tc::fence_after();
+        const uint32_t d = buf * 256;
+        for (int kb = 0; kb < p.nk; ++kb) {
+          const int s = rg.slot;
+          ok = dense_wait<true>(&full[s], rg.phase, p, dead);
+          if (!ok) break;
+          const uint32_t base = smem_addr(smem + s * L::stage);
+          const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kA);
+          const uint64_t ud = tc::sdesc_sw128(base + kDenseABytes);
+#pragma unroll
+          for (int q = 0; q < kDenseK / 16; ++q) {   // 32 bytes further in the swizzled rows
+            tc::mma_f16<true>(d, ad + 2 * q, bd + 2 * q, idesc, kb + q > 0 ? 1u : 0u);
+            if (SILU) tc::mma_f16<true>(d + 128, ud + 2 * q, bd + 2 * q, idesc, kb + q > 0 ? 1u : 0u);
+          }
+          tc::commit2(&empty[s]);
+          rg.next();
+        }
+        if (ok) tc::commit2(&d_full[buf]);
+      }
+      tc::commit2(drain);
+    }
+  } else if (warp >= 4) {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3, et = threadIdx.x & 127;
+    const int grp = (warp >> 2) - 1;
+    const int bar = 1 + grp;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
+    // this thread's 16 bytes of rows pr + 8 k of a chunk, and its place in the
+    // matrices that turn 32 columns of tensor memory into rows: 16-byte piece
+    // 4q + m of row r holds weight rows 8m.. and sits at piece ^ (r & 7)
+    const int pc = et & 15, pr = et >> 4;
+    const int mr = lane & 7;
+    const uint32_t mat = mr * 256 + (((4 * q + (lane >> 3)) ^ mr) << 4);
+    int lt = 0, chunk = 0;
+    pdl_wait();
+    for (int i = first; i < tiles; i += step, ++lt) {
+      int m, t;
+      dense_tile(p, i, m, t);
+      const int n0 = (2 * m + rank) * kDenseRows, r0 = t * p.nt;
+      const int n = min(p.nt, p.R - r0), pn = n0 + 8 * pc;
+      const int buf = lt & 1;
+      // bias of this thread's weight rows 8 k + lane / 4 of the warp's 32
+      float bias[SILU ? 8 : 4] = {};
+      if (p.bias) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = n0 + 32 * q + 8 * k + (lane >> 2);
+          if (row < p.M) {
+            bias[k] = bf16_at(p.bias + row);
+            if constexpr (SILU) bias[4 + k] = bf16_at(p.bias + p.M + row);
+          }
+        }
+      }
+      uint4 res[4];
+      auto load_residual = [&](int c0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = c0 + pr + 8 * k;
+          res[k] = make_uint4(0, 0, 0, 0);
+          if (row >= n || pn >= p.M) continue;
+          const uint16_t* src = p.residual + (size_t)(r0 + row) * p.M + pn;
+          if (p.vec) {
+            res[k] = __ldcs(reinterpret_cast<const uint4*>(src));
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = (pn + 2 * j < p.M ? src[2 * j] : 0u) |
+                     (pn + 2 * j + 1 < p.M ? (uint32_t)src[2 * j + 1] << 16 : 0u);
+            res[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      };
+      if (p.residual) load_residual(32 * grp);
+      bool ok = dense_wait<true>(&d_full[buf], (lt >> 1) & 1, p, dead);
+      // a group's warps go on or leave together: no named barrier below waits
+      // for a warp that gave up
+      ok = named_all(bar, 128, ok);
+      if (!ok) break;
+      tc::fence_after();
+      for (int c0 = 32 * grp; c0 < n; c0 += 64, ++chunk) {
+        uint8_t* stage = smem + L::out + (grp * L::chunks + chunk % L::chunks) * kDenseChunk;
+        // register 4 b + 2 i + j of the two halves: weight row 8 i + lane / 4 (16
+        // further in the second), row 8 b + 2 (lane % 4) + j of x
+        uint32_t raw[2][16];
+        float v[32];
+        tc::ld_16x32(lanes + buf * 256 + c0, raw[0]);
+        tc::ld_16x32(lanes + (16u << 16) + buf * 256 + c0, raw[1]);
+        tc::wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          v[x] = __uint_as_float(raw[x >> 4][x & 15]) + bias[2 * (x >> 4) + ((x >> 1) & 1)];
+        if constexpr (SILU) {
+          tc::ld_16x32(lanes + buf * 256 + 128 + c0, raw[0]);
+          tc::ld_16x32(lanes + (16u << 16) + buf * 256 + 128 + c0, raw[1]);
+          tc::wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            v[x] = dense_silu(v[x]) * (__uint_as_float(raw[x >> 4][x & 15]) +
+                                       bias[4 + 2 * (x >> 4) + ((x >> 1) & 1)]);
+        } else {
+          dense_act(p.act, v);
+        }
+        const uint32_t mats = smem_addr(stage) + mat;
+        if (p.residual) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(stage + (pr + 8 * k) * 256 + ((pc ^ (pr & 7)) << 4)) = res[k];
+          if (c0 + 64 < n) load_residual(c0 + 64);
+          named_sync(bar, 128);
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            uint32_t w[4];
+            tc::ldm4_trans(mats + b * 8 * 256, w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int x = 16 * (k >> 1) + 4 * b + 2 * (k & 1);
+              v[x] += bf16_lo(w[k]);
+              v[x + 1] += bf16_hi(w[k]);
+            }
+          }
+        }
+        if (p.out_float) {
+          float* out = static_cast<float*>(p.out);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const int row = c0 + 8 * ((x >> 2) & 3) + 2 * (lane & 3) + (x & 1);
+            const int col = n0 + 32 * q + 16 * (x >> 4) + 8 * ((x >> 1) & 1) + (lane >> 2);
+            if (row < n && col < p.M) out[(size_t)(r0 + row) * p.M + col] = v[x];
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            auto pack = [&](int k) {
+              const int x = 16 * (k >> 1) + 4 * b + 2 * (k & 1);
+              return RowVec<8>::pack(v[x], v[x + 1]);
+            };
+            tc::stm4_trans(mats + b * 8 * 256, pack(0), pack(1), pack(2), pack(3));
+          }
+          named_sync(bar, 128);
+          uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = c0 + pr + 8 * k;
+            if (row >= n || pn >= p.M) continue;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + (pr + 8 * k) * 256 +
+                                                            ((pc ^ (pr & 7)) << 4));
+            uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
+            if (p.vec) {
+              *reinterpret_cast<uint4*>(dst) = w;
+            } else {
+              const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (pn + j < p.M) dst[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
+            }
+          }
+        }
+        if (L::chunks == 1) named_sync(bar, 128);   // the chunk's place is free again
+      }
+      tc::fence_before();
+      __syncwarp();
+      tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  __syncthreads();
+  // as in moe_product_tiles: before a CTA leaves and tensor memory is released,
+  // every MMA is done, and with them every copy into a stage that they read,
+  // which is all there are unless the pair is dead. Then copies may still be in
+  // flight, and both CTAs stay for a time that is hundreds of times a copy's.
+  if (warp == 1) prod_wait_end(drain, 0, p.err);
+  if (warp == 0 && *dead)
+    for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
+  __syncwarp();
+  cluster_sync();   // no CTA leaves while the other may still reach into it
+  tc::fence_after();
+  if (warp == 1) tc::tmem_dealloc2(*tmem_slot, 512);
+}
+
+// ---------------------------------------------------------------------------
+// moe_dense_split. One tile of 128 weight rows (with SILU 128 gate and their 128
+// up rows) by nt rows of x a cluster; CTA j of its S takes the j-th part of K.
+// Warps 0-3 are the epilogue, one per lane quarter of tensor memory, warp 4
+// copies, warp 5 issues the MMAs. Each part's sums go to the CTA that finishes
+// the row of x they belong to (row r: CTA r mod S), which adds them in the order
+// of the parts.
+// ---------------------------------------------------------------------------
+constexpr int kSplitThreads = 192;
+constexpr int kSplitMaxCols = 128;
+constexpr int kSplitBars = 1024;   // bytes kept for barriers in front of the ring
+
+__host__ __device__ constexpr int split_stage_bytes(bool silu, int nt) {
+  return (silu ? 2 : 1) * kDenseABytes + nt * kDenseK * 2;
+}
+// what the parts of a tile's sums take in the CTAs that add them
+__host__ __device__ constexpr int split_sum_bytes(bool silu, int nt, int S) {
+  return S > 1 ? (silu ? 2 : 1) * ((nt + S - 1) / S) * S * kDenseRows * 4 : 0;
+}
+
+template <bool SILU>
+__global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
+    const __grid_constant__ DenseParams p, const int S) {
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  constexpr int kA = (SILU ? 2 : 1) * kDenseABytes;
+  constexpr int kMaxStages = 16;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* d_full = empty + kMaxStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
+  volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint8_t* ring = smem + kSplitBars;
+  const int stage = split_stage_bytes(SILU, p.nt);
+  float* sums = reinterpret_cast<float*>(ring + p.stages * stage);   // [S][slots][128] (x 2)
+
+  const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % S, tile = blockIdx.x / S;
+  const int m = tile % p.mt, t = tile / p.mt;
+  const int n0 = m * kDenseRows, r0 = t * p.nt;
+  const int n = min(p.nt, p.R - r0);
+  const int k0 = (int)((int64_t)p.nk * rank / S), k1 = (int)((int64_t)p.nk * (rank + 1) / S);
+  const uint32_t cols = p.nt * (SILU ? 2 : 1);
+  const uint32_t tcols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+
+  if (warp == 4 && lane == 0) {
+    tc::prefetch_tmap(&p.tm_w);
+    tc::prefetch_tmap(&p.tm_x);
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(&full[i], 1 + p.withheld);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(d_full, 1);
+    *dead = 0;
+    mbar_init_fence();
+  }
+  if (warp == 5) tc::tmem_alloc(tmem_slot, tcols);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  if (S > 1) cluster_arrive();   // this CTA runs: others may write to it
+
+  if (warp == 4) {
+    RingPos rg(p.stages);
+    const uint32_t bytes = kA + p.nt * kDenseK * 2;
+    auto weights = [&](int s, int kb) {
+      tc::expect(&full[s], bytes);
+      tc::tma1_load_2d(ring + s * stage, &p.tm_w, kb * kDenseK, n0, &full[s]);
+      if (SILU)
+        tc::tma1_load_2d(ring + s * stage + kDenseABytes, &p.tm_w, kb * kDenseK, p.M + n0, &full[s]);
+    };
+    // weights, which no earlier kernel writes, before the wait for earlier kernels
+    const int ahead = min(k1 - k0, p.stages);
+    for (int g = 0; g < ahead; ++g) weights(g, k0 + g);
+    pdl_wait();
+    for (int g = 0; g < k1 - k0; ++g) {
+      const int s = rg.slot;
+      if (g >= p.stages && !dense_wait<false>(&empty[s], rg.phase ^ 1u, p, dead)) {
+        ok = false;
+        break;
+      }
+      if (g >= ahead) weights(s, k0 + g);
+      tc::tma1_load_2d(ring + s * stage + kA, &p.tm_x, (k0 + g) * kDenseK, r0, &full[s]);
+      rg.next();
+    }
+  } else if (warp == 5) {
+    RingPos rg(p.stages);
+    const uint32_t idesc = tc::f16_idesc(kDenseRows, p.nt);
+    for (int kb = k0; kb < k1; ++kb) {
+      const int s = rg.slot;
+      ok = dense_wait<false>(&full[s], rg.phase, p, dead);
+      if (!ok) break;
+      const uint32_t base = smem_addr(ring + s * stage);
+      const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kA);
+      const uint64_t ud = tc::sdesc_sw128(base + kDenseABytes);
+#pragma unroll
+      for (int q = 0; q < kDenseK / 16; ++q) {
+        const uint32_t add = kb > k0 || q > 0 ? 1u : 0u;
+        tc::mma_f16<false>(tmem, ad + 2 * q, bd + 2 * q, idesc, add);
+        if (SILU) tc::mma_f16<false>(tmem + p.nt, ud + 2 * q, bd + 2 * q, idesc, add);
+      }
+      tc::commit1(&empty[s]);
+      rg.next();
+    }
+    tc::commit1(d_full);   // in any case: nothing leaves before the MMAs are done
+    prod_wait_end(d_full, 0, p.err);
+  }
+  __syncwarp();
+  const int row = n0 + threadIdx.x;   // an epilogue thread's weight row
+  const int slots = (p.nt + S - 1) / S;
+  // The result for row r of the tile from its sums.
+  auto finish = [&](int r, float v, float up) {
+    if (row >= p.M || r >= n) return;
+    if (p.bias) v += bf16_at(p.bias + row);
+    if constexpr (SILU) {
+      if (p.bias) up += bf16_at(p.bias + p.M + row);
+      v = dense_silu(v) * up;
+    } else {
+      float a[1] = {v};
+      dense_act(p.act, a);
+      v = a[0];
+    }
+    const size_t at = (size_t)(r0 + r) * p.M + row;
+    if (p.residual) v += bf16_at(p.residual + at);
+    if (p.out_float)
+      static_cast<float*>(p.out)[at] = v;
+    else
+      static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rn(v);
+  };
+  if (warp < 4) {
+    ok = dense_wait<false>(d_full, 0, p, dead);
+    ok = named_all(1, 128, ok && !*dead);
+    tc::fence_after();
+    pdl_wait();
+    if (S > 1) cluster_wait();
+    if (ok) {
+      for (int c0 = 0; c0 < n; c0 += 16) {
+        uint32_t v[16], u[16];
+        tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
+        if (SILU) tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + p.nt + c0, u);
+        tc::wait_ld();
+        if (S == 1) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            finish(c0 + j, __uint_as_float(v[j]), SILU ? __uint_as_float(u[j]) : 0.f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int r = c0 + j;
+            if (r >= n) break;
+            const int slot = r / S;
+            const uint32_t to = tc::cluster_addr(
+                sums + ((rank * slots + slot) * (SILU ? 2 : 1)) * kDenseRows + threadIdx.x, r - slot * S);
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v[j]) : "memory");
+            if (SILU)
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + kDenseRows * 4), "r"(u[j])
+                           : "memory");
+          }
+        }
+      }
+      tc::fence_before();
+    }
+  } else if (S > 1) {
+    cluster_wait();
+  }
+  __syncwarp();
+  if (S > 1) {
+    cluster_sync();   // the parts have landed, and no CTA reaches into another after it
+    if (warp < 4 && ok) {
+      for (int r = rank, slot = 0; r < n; r += S, ++slot) {
+        float v = 0.f, up = 0.f;
+        for (int j = 0; j < S; ++j) {
+          const float* from = sums + ((j * slots + slot) * (SILU ? 2 : 1)) * kDenseRows + threadIdx.x;
+          v += from[0];
+          if (SILU) up += from[kDenseRows];
+        }
+        finish(r, v, up);
+      }
+    }
+  }
+  __syncthreads();
+  // copies of a dead CTA may still be in flight
+  if (warp == 4 && *dead)
+    for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 5) tc::tmem_dealloc(tmem, tcols);
 }
 
 }  // namespace moe

@@ -82,7 +82,53 @@ def test_dense_create_refusals(lib, kw, status):
     assert h.value is None
 
 
+def plan(lib, R, K, N, act=0, sms=152):
+    from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan
+    p = MoEDensePlan()
+    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(N, K, act)), R, sms, ctypes.byref(p)) == 0
+    return p
+
+
+def test_dense_plans_keep_the_kernels_limits(lib):
+    r = np.random.default_rng(5)
+    seen = set()
+    for _ in range(3000):
+        R, K, N = (int(np.exp(r.uniform(0, np.log(hi)))) for hi in (20000, 1000, 10000))
+        K, act, sms = 8 * K, int(r.choice([0, 5])), int(r.choice([1, 2, 76, 148, 152]))
+        N += N % 2
+        p, two = plan(lib, R, K, N, act, sms), 2 if act == 5 else 1
+        M, nk = N // two, -(-K // 64)
+        seen.add((p.split, p.parts))
+        assert p.stages >= 2
+        if p.split:
+            assert p.nt % 16 == 0 and 16 <= p.nt <= 128 and p.stages <= 16
+            assert p.parts in (1, 2, 4, 8) and p.parts <= nk
+            # barriers, ring, sums; two CTAs an SM and no third
+            stage = two * 16384 + p.nt * 128
+            sums = two * -(-p.nt // p.parts) * p.parts * 512 if p.parts > 1 else 0
+            assert 2048 + p.stages * stage + sums <= p.smem <= 113 * 1024
+            assert 3 * (p.smem + 1024) > 228 * 1024 and 2 * p.nt * two <= 512
+            assert p.ctas == -(-M // 128) * -(-R // p.nt) * p.parts
+        else:
+            assert p.nt % 32 == 0 and 32 <= p.nt <= 256 // two and p.smem <= 232448
+            assert p.ctas == 2 * min(max(1, sms // 2), -(-M // 256) * -(-R // p.nt))
+    assert seen >= {(0, 1), (1, 1), (1, 2), (1, 4), (1, 8)}
+
+
+def test_dense_plan_refusals(lib):
+    from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan
+    p, ok = MoEDensePlan(), MoEDenseConfig(64, 64, 0)
+    assert lib.moe_dense_plan(None, 1, 152, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 0, 152, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 0, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 152, None) == 1
+    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(64, 60, 0)), 1, 152, ctypes.byref(p)) == 2
+    huge = MoEDenseConfig(2 ** 31 - 2, 8, 0)
+    assert lib.moe_dense_plan(ctypes.byref(huge), 2 ** 31 - 1, 152, ctypes.byref(p)) == 2
+
+
 def test_dense_null_handles(lib):
+    assert lib.moe_dense_arm_timeout(None) == 1
     assert lib.moe_dense_create(None, P, P, None) == 1
     assert lib.moe_dense_run(None, 1, P, 0, P, 0, 0) == 1
     flags = ctypes.c_uint32(7)

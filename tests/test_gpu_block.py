@@ -338,7 +338,8 @@ DENSE = [
     (1, 8, 1), (1, 2048, 128), (2, 64, 2), (3, 72, 60), (7, 256, 130), (8, 2048, 128), (16, 1024, 384),
     (17, 200, 128), (31, 4096, 96), (33, 64, 514), (64, 520, 256), (65, 128, 1000), (100, 264, 258),
     (127, 64, 64), (129, 328, 640), (256, 512, 512), (300, 1032, 776), (513, 96, 130), (1000, 80, 1030),
-    (1, 7168, 256), (5, 7168, 34), (12, 8, 4100)]
+    (1, 7168, 256), (5, 7168, 34), (12, 8, 4100), (2000, 192, 2600), (3001, 136, 1544), (700, 448, 5000),
+    (4100, 64, 514)]
 
 
 @pytest.mark.parametrize("R,K,N", DENSE)
@@ -381,6 +382,29 @@ def test_dense_outputs_off_the_vector_alignment(dev, N, float32):  # noqa: F811
         p(bf16(c.x, dev), rv, out=ov, float32=float32)
         assert torch.equal(ov, want)
         assert out[:skew_out].eq(7).all() and out[skew_out + 37 * N:].eq(7).all()
+
+
+@pytest.mark.parametrize("act", [None, "silu_mul"])
+@pytest.mark.parametrize("R,K,N", [(2, 64, 128), (5, 2048, 384), (40, 1024, 4096), (600, 512, 2048),
+                                   (3000, 256, 2048)])
+def test_dense_winds_down_when_its_waits_give_up(dev, R, K, N, act):  # noqa: F811
+    # failure detection without a fault: the MMAs' bounded wait runs out (for an
+    # arrival that nothing makes), and then every other role's; the launch ends, the
+    # handle reports it once, and the next runs are right
+    from sparse_expert_gemv_gb300 import MOE_DEVICE_TIMEOUT
+    c = Dense(R, K, N, True, act, True, seed=33)
+    p = c.handle(dev)
+    want = c.run(dev, p)
+    assert p.get_error() == 0
+    for _ in range(3):
+        p.arm_timeout()
+        p(bf16(c.x[:0], dev))                     # launches nothing
+        assert p.get_error() == 0
+        c.run(dev, p)
+        assert p.get_error() == MOE_DEVICE_TIMEOUT
+        assert p.get_error() == 0
+        assert torch.equal(c.run(dev, p), want)
+        assert p.get_error() == 0
 
 
 def test_dense_of_exact_sums(dev):  # noqa: F811
