@@ -32,26 +32,55 @@ using moe::launch;
 // ---- routing -----------------------------------------------------------------
 
 template <int R>
-moe_status_t route_launch(const moe::RouteParams& p, void* stream) {
-  const size_t smem = p.groups > 1 ? (size_t)moe::kRouteWarps * p.E * sizeof(double) : 0;
-  return launch(moe::moe_route_experts_rows<R>, (p.T + moe::kRouteWarps - 1) / moe::kRouteWarps,
-                moe::kRouteWarps * 32, smem, stream, 1, p);
+moe_status_t route_launch(moe::RouteParams p, void* stream) {
+  const int size = p.bf16 ? 2 : 4;
+  p.vec = p.E % R == 0 && aligned(p.logits, std::min(16, R * size));
+  p.lane_shift = -1;
+  if (p.per % R == 0)
+    for (int s = 0; s <= 5; ++s)
+      if (p.per / R == 1 << s) p.lane_shift = s;
+  p.bias_vec = p.E % R == 0 && aligned(p.bias, 16);
+  p.smem = std::max(p.E * (int)sizeof(double), 128 * (R + 1));   // route_slow's, sorted keys
+  const size_t smem = (size_t)moe::kRouteWarps * p.smem;
+  const unsigned grid = (p.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
+  return p.bf16 && !p.bias ? launch(moe::moe_route_experts_rows<R, true>, grid,
+                                    moe::kRouteWarps * 32, smem, stream, 1, p)
+                           : launch(moe::moe_route_experts_rows<R, false>, grid,
+                                    moe::kRouteWarps * 32, smem, stream, 1, p);
 }
 
 // ---- norms -------------------------------------------------------------------
 
-template <int V>
-moe_status_t norm_pair_launch(const moe::NormPairParams& p, int T, void* stream) {
-  const int nv = p.H / V;
-  const bool two = nv > 512 || (nv > 128 && T >= 2048);
-  const int threads = nv > 1024 ? 1024 : ((two ? (nv + 1) / 2 : nv) + 31) / 32 * 32;
-  const int per = (nv + threads - 1) / threads;
-  if (per <= 1) return launch(moe::moe_norm_add_norm_rows<V, 1>, T, threads, 0, stream, 1, p);
-  static_assert(moe::kNormMaxH <= 2 * 1024 * 8, "at most two vectors of eight a thread");
-  if (V > 1 || per <= 2)
-    return launch(moe::moe_norm_add_norm_rows<V, 2>, T, threads, 0, stream, 1, p);
-  if (per <= 4) return launch(moe::moe_norm_add_norm_rows<1, 4>, T, threads, 0, stream, 1, p);
-  return launch(moe::moe_norm_add_norm_rows<1, 16>, T, threads, 0, stream, 1, p);
+// NV vectors a thread; rows of at most 32 threads several a CTA.
+template <int V, int NV>
+moe_status_t norm_pair_rows(const moe::NormPairParams& p, void* stream) {
+  const int threads = ((p.H / V + NV - 1) / NV + 31) / 32 * 32;
+  const int rows = threads == 32 ? 8 : 1;
+  const unsigned grid = (p.T + rows - 1) / rows;
+  const dim3 block(threads, rows);
+  return p.gate && !p.gate_row
+             ? launch(moe::moe_norm_add_norm_rows<V, NV, true>, grid, block, 0, stream, 1, p)
+             : launch(moe::moe_norm_add_norm_rows<V, NV, false>, grid, block, 0, stream, 1, p);
+}
+
+moe_status_t norm_pair_launch(const moe::NormPairParams& p, bool vec, void* stream) {
+  if (!vec) {
+    if (p.H <= 1024) return norm_pair_rows<1, 1>(p, stream);
+    if (p.H <= 4096) return norm_pair_rows<1, 4>(p, stream);
+    return norm_pair_rows<1, 16>(p, stream);
+  }
+  const int nv = p.H / 8;
+  // Few values: as many threads as a row takes, for the latency (us of 300 rows of
+  // 1024 with one, two and four vectors a thread 2.1, 2.4, 3.4). Many: more values a
+  // thread spread the two reductions' instructions further (16384 rows of 2048
+  // 50 / 47 / 48, 8191 of 7168 90 / 87 / 71, with eight 72; 2000 of 16384 with two 57,
+  // with eight 46).
+  if ((int64_t)p.T * nv < 65536)
+    return nv <= 1024 ? norm_pair_rows<8, 1>(p, stream) : norm_pair_rows<8, 2>(p, stream);
+  if (nv <= 32) return norm_pair_rows<8, 1>(p, stream);
+  if (nv <= 256) return norm_pair_rows<8, 2>(p, stream);
+  if (nv <= 1024) return norm_pair_rows<8, 4>(p, stream);
+  return norm_pair_rows<8, 8>(p, stream);
 }
 
 // ---- dense products ------------------------------------------------------------
@@ -193,9 +222,11 @@ moe_status_t moe_route_experts(const moe_route_config_t* cfg, int32_t T, const v
   p.sigmoid = (c.flags & MOE_ROUTE_SIGMOID) != 0;
   p.top2 = (c.flags & MOE_ROUTE_GROUP_TOP2) != 0;
   p.renormalize = (c.flags & MOE_ROUTE_RENORMALIZE) != 0;
+  if (c.E <= 32) return route_launch<1>(p, stream);
   if (c.E <= 64) return route_launch<2>(p, stream);
   if (c.E <= 128) return route_launch<4>(p, stream);
   if (c.E <= 256) return route_launch<8>(p, stream);
+  if (c.E <= 512) return route_launch<16>(p, stream);
   return route_launch<32>(p, stream);
 }
 
@@ -228,7 +259,9 @@ moe_status_t moe_norm_add_norm(int32_t T, int32_t H, const uint16_t* x, const ui
   p.y = y;
   p.codes = codes;
   p.scales = scales;
+  p.T = T;
   p.H = H;
+  p.inv_h = 1.f / (float)H;
   p.scale = scale;
   p.residual_scale = residual_scale;
   p.eps = eps;
@@ -241,7 +274,7 @@ moe_status_t moe_norm_add_norm(int32_t T, int32_t H, const uint16_t* x, const ui
   for (const uint16_t* a : {x, residual, post_weight, pre_weight, const_cast<const uint16_t*>(sum),
                             const_cast<const uint16_t*>(y)})
     vec = vec && aligned(a, 16);
-  return vec ? norm_pair_launch<8>(p, T, stream) : norm_pair_launch<1>(p, T, stream);
+  return norm_pair_launch(p, vec, stream);
 }
 
 moe_status_t moe_dense_create(const moe_dense_config_t* cfg, const uint16_t* weight,

@@ -18,11 +18,11 @@ namespace moe {
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 template <typename... KArgs, typename... Args>
-moe_status_t launch(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem,
-                    void* stream, unsigned cluster, const Args&... args) {
+moe_status_t launch(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, void* stream,
+                    unsigned cluster, const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];

@@ -65,11 +65,15 @@ struct RowVec<8> {
     f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
   }
   __device__ __forceinline__ static uint32_t pack(float a, float b) {
-    return (uint32_t)f32_to_bf16_rn(a) | ((uint32_t)f32_to_bf16_rn(b) << 16);
+    uint32_t r;   // both at once: a quarter of the instructions of two roundings
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+  }
+  __device__ __forceinline__ static Raw packed(const float (&f)[8]) {
+    return make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
   }
   __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[8]) {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    *reinterpret_cast<uint4*>(p) = packed(f);
   }
   __device__ __forceinline__ static void store_codes(uint8_t* p, const float (&f)[8]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16),
@@ -88,8 +92,9 @@ struct RowVec<1> {
   __device__ __forceinline__ static void values(uint16_t v, float (&f)[1]) {
     f[0] = __uint_as_float((uint32_t)v << 16);
   }
+  __device__ __forceinline__ static Raw packed(const float (&f)[1]) { return f32_to_bf16_rn(f[0]); }
   __device__ __forceinline__ static void store(uint16_t* p, const float (&f)[1]) {
-    *p = f32_to_bf16_rn(f[0]);
+    *p = packed(f);
   }
   __device__ __forceinline__ static void store_codes(uint8_t* p, const float (&f)[1]) {
     *p = (uint8_t)e4m3x2(f[0], f[0]);
