@@ -19,7 +19,8 @@
 struct moe_dense : moe::Handle {
   moe_dense_config_t cfg;
   int num_sms;
-  CUtensorMap tm_w;
+  CUtensorMap tm_w;       // boxes of 128 rows
+  CUtensorMap tm_w_half;  // of 64
   const uint16_t* bias;
   std::atomic<bool> armed;   // the next run's waits run out (moe_dense_arm_timeout)
 };
@@ -101,52 +102,80 @@ struct DensePlan {
   int nt;       // rows of x a tile
   int S;        // parts of K (split)
   int stages;   // of the ring (split)
-  double cycles;
+  double us;    // by the model below
 };
 
-// Shared memory of a CTA of moe_dense_split. Two fit on an SM, so that clusters
-// find room wherever an SM is left, and no third: the tensor memory of two is
-// never more than there is, so none waits for it while it holds up its cluster.
-constexpr int kSplitSmemMax = 113 * 1024, kSplitSmemMin = 78 * 1024;
+// Shared memory of a CTA of moe_dense_split: half an SM's or all of it. A third CTA
+// never fits on an SM, so that the tensor memory of those that do is never more
+// than there is: none waits for it while it holds up its cluster.
+constexpr int kSplitHalf = 113 * 1024, kSplitFull = 226 * 1024, kSplitSmemMin = 78 * 1024;
 
-int split_stages(bool silu, int nt, int S) {
-  const int room = kSplitSmemMax - 1024 - moe::kSplitBars - moe::split_sum_bytes(silu, nt, S);
-  return std::min(16, room / moe::split_stage_bytes(silu, nt));
+int split_stages(int nt, int S, int room) {
+  room -= 1024 + moe::kSplitBars + moe::split_sum_bytes(nt, S);
+  return std::min(moe::kSplitStages, room / moe::split_stage_bytes(nt));
 }
 
-// The cheapest cut by a model of its cycles: a stage takes its MMAs or, where
-// that is longer, its bytes' way into an SM; whole rounds over the SMs.
+size_t split_smem(const DensePlan& p) {
+  const int need = 1024 + moe::kSplitBars + p.stages * moe::split_stage_bytes(p.nt) +
+                   moe::split_sum_bytes(p.nt, p.S);
+  return std::max(need, kSplitSmemMin);
+}
+
+// The cheapest cut by a model of its time, in us. Its constants were fitted to 560
+// timings (24 shapes from 1 to 4096 rows, every cut of each, inputs beyond L2); its
+// choices are on average 1.4 % slower than the best of them, 9 % at worst.
+//   split   a start, then the stages of a CTA at what an SM, shared by the CTAs on
+//           it, or all of L2 delivers, or its ring's latency allows where it turns;
+//           the parts' exchange; clusters that find no room wait for a round more
+//   tiles   rounds of tiles over the pairs, whose stages take their MMAs or their
+//           bytes' way into an SM
 DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
   const bool silu = is_silu(c);
   const int M = silu ? c.N / 2 : c.N, two = silu ? 2 : 1;
   const int nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
+  constexpr double kStart = 0.16, kL2 = 14.7e6;   // us, bytes a us
   DensePlan best{false, 0, 1, 0, 0.0};
   auto take = [&](const DensePlan& p) {
-    if (!best.nt || p.cycles < best.cycles) best = p;
+    if (!best.nt || p.us < best.us) best = p;
   };
   const int pairs = std::max(1, num_sms / 2);
   for (int nt = moe::kDenseCols / two; nt >= 32; nt -= 32) {
+    if (nt - 32 >= R) continue;
     const double tiles = std::ceil(M / 256.0) * std::ceil((double)R / nt);
-    const double stage = std::max(2.0 * two * nt, (128 * two + nt / 2) * 128 / 72.0);
-    take({false, nt, 1, 0, std::ceil(tiles / pairs) * nk * stage + 4000 + 12.0 * nt});
+    const double bytes = (128 * two + nt / 2) * 128.0;   // a stage's, of one CTA
+    const double stage = std::max({0.0012 * two * nt, bytes / 108.8e3,
+                                   std::min<double>(tiles, pairs) * 2 * bytes / kL2});
+    take({false, nt, 1, 0, kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
+                               0.0082 * std::min(nt, R)});
   }
-  for (int nt = moe::kSplitMaxCols; nt >= 16; nt -= 16)
-    for (int S = 1; S <= 8 && S <= nk; S *= 2) {
-      const int stages = split_stages(silu, nt, S);
-      if (stages < 2) continue;
-      const double ctas = std::ceil(M / 128.0) * std::ceil((double)R / nt) * S;
-      const double stage = std::max(1.0 * two * nt, (128 * two + nt) * 128 / 60.0);
-      take({true, nt, S, stages,
-            std::ceil(ctas / num_sms) * std::ceil((double)nk / S) * stage + 3000 + 12.0 * nt / S +
-                (S > 1 ? 1200 : 0)});
-    }
+  const double hbm = 2.0 * c.K * ((double)c.N + R) / 6.8e6;
+  for (int nt = moe::kSplitMaxCols; nt >= 16; nt -= 16) {
+    if (nt - 16 >= R) continue;
+    const int n = std::min(nt, R), bytes = moe::split_stage_bytes(nt);
+    for (int S = 1; S <= 8 && S <= nk; S *= 2)
+      for (const int room : {kSplitFull, kSplitHalf}) {
+        const int stages = split_stages(nt, S, room);
+        if (stages < 2) continue;
+        const bool half = room == kSplitHalf;
+        const double ctas = std::ceil(M / (silu ? 64.0 : 128.0)) * std::ceil((double)R / nt) * S;
+        // CTAs that run at once: clusters of 4 and 8 leave SMs of a GPC over
+        const double most = num_sms * (half ? (S == 8 ? 288 : S == 4 ? 296 : 304)
+                                            : (S == 8 ? 120 : S == 4 ? 144 : 152)) / 152.0;
+        const double run = std::min(ctas, most), shared = half ? std::min(2.0, std::ceil(run / num_sms)) : 1;
+        const double g = std::ceil((double)nk / S);
+        const double rate = std::min(153e3 / shared, g > stages ? stages * bytes / 1.68 : 153e3);
+        const double stream = std::max(g * bytes / rate, run * g * bytes / kL2);
+        const double per = 1.71 + stream + n * (0.01 / S + (S > 1 ? 0.0129 : 0)) + 0.118 * (S - 1);
+        take({true, nt, S, stages, kStart + std::max(std::ceil(ctas / most) * per, hbm + 1.71)});
+      }
+  }
   return best;
 }
 
-size_t split_smem(bool silu, const DensePlan& p) {
-  const int need = 1024 + moe::kSplitBars + p.stages * moe::split_stage_bytes(silu, p.nt) +
-                   moe::split_sum_bytes(silu, p.nt, p.S);
-  return std::max(need, kSplitSmemMin);
+int log2_of(int v) {
+  int l = 0;
+  while (1 << (l + 1) <= v) ++l;
+  return l;
 }
 
 constexpr size_t kDenseSmem[2] = {moe::DenseSmem<false>::total + 1024,
@@ -159,7 +188,7 @@ bool set_dense_attributes() {
                               (int)kDenseSmem[SILU]) == cudaSuccess &&
          cudaFuncSetAttribute(moe::moe_dense_split<SILU>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kSplitSmemMax) == cudaSuccess;
+                              kSplitFull) == cudaSuccess;
 }
 
 moe_status_t check_dense(const moe_dense_config_t& c) {
@@ -171,7 +200,7 @@ moe_status_t check_dense(const moe_dense_config_t& c) {
 // Tiles along M and R and the CTAs of a launch; false when there are too many.
 bool dense_grid(const moe_dense_config_t& c, const DensePlan& p, int R, int num_sms, int& mt, int& tt,
                 int& ctas) {
-  const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = p.split ? 128 : 256;
+  const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = p.split ? (is_silu(c) ? 64 : 128) : 256;
   const int64_t m = (M + rows - 1) / rows, t = ((int64_t)R + p.nt - 1) / p.nt;
   if (m * t * p.S > 0x3fffffff) return false;
   mt = (int)m;
@@ -294,6 +323,7 @@ moe_status_t moe_dense_create(const moe_dense_config_t* cfg, const uint16_t* wei
       cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, m->device) ==
           cudaSuccess &&
       encode_rows(&m->tm_w, weight, c.N, c.K, moe::kDenseRows) &&
+      encode_rows(&m->tm_w_half, weight, c.N, c.K, moe::kDenseRows / 2) &&
       (is_silu(c) ? set_dense_attributes<true>() : set_dense_attributes<false>()) &&
       m->acquire(nullptr) && cudaStreamSynchronize(nullptr) == cudaSuccess;
   if (!ok) {
@@ -329,7 +359,7 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   p.nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
   int ctas;
   if (!dense_grid(c, plan, R, m->num_sms, p.mt, p.tt, ctas)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  p.tm_w = m->tm_w;
+  p.tm_w = plan.split && silu ? m->tm_w_half : m->tm_w;
   if (!encode_rows(&p.tm_x, x, R, c.K, plan.split ? plan.nt : plan.nt / 2)) return MOE_ERR_CUDA;
   p.bias = m->bias;
   p.residual = residual;
@@ -346,7 +376,7 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   moe_status_t st;
   if (plan.split)
     st = launch(silu ? moe::moe_dense_split<true> : moe::moe_dense_split<false>, ctas,
-                moe::kSplitThreads, split_smem(silu, plan), stream, plan.S, p, plan.S);
+                moe::kSplitThreads, split_smem(plan), stream, plan.S, p, log2_of(plan.S));
   else
     st = launch(silu ? moe::moe_dense_tiles<true> : moe::moe_dense_tiles<false>, ctas,
                 moe::kDenseThreads, kDenseSmem[silu], stream, 2, p);
@@ -368,7 +398,7 @@ moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t nu
   out->parts = p.S;
   out->stages = p.split ? p.stages
                         : silu ? moe::DenseSmem<true>::stages : moe::DenseSmem<false>::stages;
-  out->smem = (int)(p.split ? split_smem(silu, p) : kDenseSmem[silu]);
+  out->smem = (int)(p.split ? split_smem(p) : kDenseSmem[silu]);
   out->ctas = ctas;
   return MOE_OK;
 }

@@ -488,52 +488,107 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
 }
 
 // ---------------------------------------------------------------------------
-// moe_dense_split. One tile of 128 weight rows (with SILU 128 gate and their 128
-// up rows) by nt rows of x a cluster; CTA j of its S takes the j-th part of K.
-// Warps 0-3 are the epilogue, one per lane quarter of tensor memory, warp 4
-// copies, warp 5 issues the MMAs. Each part's sums go to the CTA that finishes
-// the row of x they belong to (row r: CTA r mod S), which adds them in the order
-// of the parts.
+// moe_dense_split. One tile of 128 weight rows (with SILU 64 gate rows and their
+// 64 up rows) by nt rows of x a cluster; CTA j of its S takes the j-th part of K.
+// Warps 0-7 are the epilogue, two per lane quarter of tensor memory, warp 8
+// copies, warp 9 issues the MMAs. Each part's sums go to the CTA that finishes the
+// row of x they belong to (row r: CTA r mod S), which adds them in the order of the
+// parts. (They go as stores to its shared memory: bulk copies from the CTA's own,
+// 0.35 us more for 1 to 16 rows, gained nothing up to 1000.)
 // ---------------------------------------------------------------------------
-constexpr int kSplitThreads = 192;
+constexpr int kSplitEpilogue = 256;   // threads
+constexpr int kSplitThreads = kSplitEpilogue + 64;
 constexpr int kSplitMaxCols = 128;
 constexpr int kSplitBars = 1024;   // bytes kept for barriers in front of the ring
+constexpr int kSplitStages = 16;   // of the ring, at most
 
-__host__ __device__ constexpr int split_stage_bytes(bool silu, int nt) {
-  return (silu ? 2 : 1) * kDenseABytes + nt * kDenseK * 2;
+__host__ __device__ constexpr int split_stage_bytes(int nt) { return kDenseABytes + nt * kDenseK * 2; }
+// What the parts of a tile's sums take in the CTAs that add them (a single part
+// takes the ring's place, which is free then).
+__host__ __device__ constexpr int split_sum_bytes(int nt, int S) {
+  return S > 1 ? (nt + S - 1) / S * S * kDenseRows * 4 : 0;
 }
-// what the parts of a tile's sums take in the CTAs that add them
-__host__ __device__ constexpr int split_sum_bytes(bool silu, int nt, int S) {
-  return S > 1 ? (silu ? 2 : 1) * ((nt + S - 1) / S) * S * kDenseRows * 4 : 0;
+
+// The results of outputs m.. m + 7 for row r of x from their sums v, with SILU the
+// gates', and up; rows of out and residual in 16-byte accesses with p.vec.
+template <bool SILU>
+__device__ __forceinline__ void split_finish(const DenseParams& p, size_t r, int m, float (&v)[8],
+                                             const float (&up)[8], const float (&bias)[8],
+                                             const float (&up_bias)[8]) {
+  const size_t at = r * p.M + m;
+  float res[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) res[i] = 0.f;
+  if (p.residual) {
+    if (p.vec) {
+      RowVec<8>::load(p.residual + at, res);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < p.M) res[i] = bf16_at(p.residual + at + i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += bias[i];
+  if constexpr (SILU) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = dense_silu(v[i]) * (up[i] + up_bias[i]);
+  } else {
+    dense_act(p.act, v);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] += res[i];
+  if (p.out_float) {
+    float* out = static_cast<float*>(p.out) + at;
+    if (p.vec) {
+      *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(out + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < p.M) out[i] = v[i];
+    }
+  } else {
+    uint16_t* out = static_cast<uint16_t*>(p.out) + at;
+    if (p.vec) {
+      RowVec<8>::store(out, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (m + i < p.M) out[i] = f32_to_bf16_rn(v[i]);
+    }
+  }
 }
 
 template <bool SILU>
 __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
-    const __grid_constant__ DenseParams p, const int S) {
+    const __grid_constant__ DenseParams p, const int log_parts) {
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  constexpr int kA = (SILU ? 2 : 1) * kDenseABytes;
-  constexpr int kMaxStages = 16;
+  constexpr int kTile = SILU ? kDenseRows / 2 : kDenseRows;   // outputs a tile
+  const int S = 1 << log_parts;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem);
-  uint64_t* empty = full + kMaxStages;
-  uint64_t* d_full = empty + kMaxStages;
+  uint64_t* empty = full + kSplitStages;
+  uint64_t* d_full = empty + kSplitStages;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(d_full + 1);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint8_t* ring = smem + kSplitBars;
-  const int stage = split_stage_bytes(SILU, p.nt);
-  float* sums = reinterpret_cast<float*>(ring + p.stages * stage);   // [S][slots][128] (x 2)
+  const int stage = split_stage_bytes(p.nt);
+  // rows of x that a CTA finishes, and the parts of their sums [S][slots][128]
+  const int slots = (p.nt + S - 1) >> log_parts;
+  float* sums = reinterpret_cast<float*>(ring + (S > 1 ? p.stages * stage : 0));
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % S, tile = blockIdx.x / S;
+  const int rank = blockIdx.x & (S - 1), tile = blockIdx.x >> log_parts;
   const int m = tile % p.mt, t = tile / p.mt;
-  const int n0 = m * kDenseRows, r0 = t * p.nt;
+  const int n0 = m * kTile, r0 = t * p.nt;
   const int n = min(p.nt, p.R - r0);
-  const int k0 = (int)((int64_t)p.nk * rank / S), k1 = (int)((int64_t)p.nk * (rank + 1) / S);
-  const uint32_t cols = p.nt * (SILU ? 2 : 1);
-  const uint32_t tcols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+  const int k0 = (int)((int64_t)p.nk * rank >> log_parts);
+  const int k1 = (int)((int64_t)p.nk * (rank + 1) >> log_parts);
+  const uint32_t tcols = p.nt <= 32 ? 32 : p.nt <= 64 ? 64 : 128;
 
-  if (warp == 4 && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
     tc::prefetch_tmap(&p.tm_x);
     for (int i = 0; i < p.stages; ++i) {
@@ -544,7 +599,7 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     *dead = 0;
     mbar_init_fence();
   }
-  if (warp == 5) tc::tmem_alloc(tmem_slot, tcols);
+  if (warp == 9) tc::tmem_alloc(tmem_slot, tcols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -553,14 +608,15 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
   bool ok = true;
   if (S > 1) cluster_arrive();   // this CTA runs: others may write to it
 
-  if (warp == 4) {
+  if (warp == 8) {
     RingPos rg(p.stages);
-    const uint32_t bytes = kA + p.nt * kDenseK * 2;
+    const uint32_t bytes = stage;
     auto weights = [&](int s, int kb) {
       tc::expect(&full[s], bytes);
       tc::tma1_load_2d(ring + s * stage, &p.tm_w, kb * kDenseK, n0, &full[s]);
       if (SILU)
-        tc::tma1_load_2d(ring + s * stage + kDenseABytes, &p.tm_w, kb * kDenseK, p.M + n0, &full[s]);
+        tc::tma1_load_2d(ring + s * stage + kDenseABytes / 2, &p.tm_w, kb * kDenseK, p.M + n0,
+                         &full[s]);
     };
     // weights, which no earlier kernel writes, before the wait for earlier kernels
     const int ahead = min(k1 - k0, p.stages);
@@ -573,10 +629,10 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
         break;
       }
       if (g >= ahead) weights(s, k0 + g);
-      tc::tma1_load_2d(ring + s * stage + kA, &p.tm_x, (k0 + g) * kDenseK, r0, &full[s]);
+      tc::tma1_load_2d(ring + s * stage + kDenseABytes, &p.tm_x, (k0 + g) * kDenseK, r0, &full[s]);
       rg.next();
     }
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     RingPos rg(p.stages);
     const uint32_t idesc = tc::f16_idesc(kDenseRows, p.nt);
     for (int kb = k0; kb < k1; ++kb) {
@@ -584,14 +640,10 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
       ok = dense_wait<false>(&full[s], rg.phase, p, dead);
       if (!ok) break;
       const uint32_t base = smem_addr(ring + s * stage);
-      const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kA);
-      const uint64_t ud = tc::sdesc_sw128(base + kDenseABytes);
+      const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kDenseABytes);
 #pragma unroll
-      for (int q = 0; q < kDenseK / 16; ++q) {
-        const uint32_t add = kb > k0 || q > 0 ? 1u : 0u;
-        tc::mma_f16<false>(tmem, ad + 2 * q, bd + 2 * q, idesc, add);
-        if (SILU) tc::mma_f16<false>(tmem + p.nt, ud + 2 * q, bd + 2 * q, idesc, add);
-      }
+      for (int q = 0; q < kDenseK / 16; ++q)
+        tc::mma_f16<false>(tmem, ad + 2 * q, bd + 2 * q, idesc, kb > k0 || q > 0 ? 1u : 0u);
       tc::commit1(&empty[s]);
       rg.next();
     }
@@ -599,55 +651,46 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     prod_wait_end(d_full, 0, p.err);
   }
   __syncwarp();
-  const int row = n0 + threadIdx.x;   // an epilogue thread's weight row
-  const int slots = (p.nt + S - 1) / S;
-  // The result for row r of the tile from its sums.
-  auto finish = [&](int r, float v, float up) {
-    if (row >= p.M || r >= n) return;
-    if (p.bias) v += bf16_at(p.bias + row);
-    if constexpr (SILU) {
-      if (p.bias) up += bf16_at(p.bias + p.M + row);
-      v = dense_silu(v) * up;
-    } else {
-      float a[1] = {v};
-      dense_act(p.act, a);
-      v = a[0];
+  // The sums go through shared memory, from a thread a weight row to a thread eight
+  // outputs of one row of x (a thread a weight row to the end, with its 2-byte
+  // accesses, took 84 ns a row of x).
+  constexpr int kGroups = kTile / 8;
+  const int grp = threadIdx.x & (kGroups - 1), out_m = n0 + 8 * grp;
+  float bias[8], up_bias[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) bias[i] = up_bias[i] = 0.f;
+  if (warp < 8) {
+    if (p.bias) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (out_m + i < p.M) {
+          bias[i] = bf16_at(p.bias + out_m + i);
+          if (SILU) up_bias[i] = bf16_at(p.bias + p.M + out_m + i);
+        }
     }
-    const size_t at = (size_t)(r0 + r) * p.M + row;
-    if (p.residual) v += bf16_at(p.residual + at);
-    if (p.out_float)
-      static_cast<float*>(p.out)[at] = v;
-    else
-      static_cast<uint16_t*>(p.out)[at] = f32_to_bf16_rn(v);
-  };
-  if (warp < 4) {
     ok = dense_wait<false>(d_full, 0, p, dead);
-    ok = named_all(1, 128, ok && !*dead);
+    ok = named_all(1, kSplitEpilogue, ok && !*dead);
     tc::fence_after();
-    pdl_wait();
-    if (S > 1) cluster_wait();
+    if (S > 1) cluster_wait();   // every CTA runs
     if (ok) {
-      for (int c0 = 0; c0 < n; c0 += 16) {
-        uint32_t v[16], u[16];
-        tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + c0, v);
-        if (SILU) tc::ld16(tmem + ((uint32_t)(32 * warp) << 16) + p.nt + c0, u);
+#pragma unroll 1
+      for (int c0 = 16 * (warp >> 2); c0 < n; c0 += 32) {
+        uint32_t raw[16];
+        tc::ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0, raw);
         tc::wait_ld();
+        float* to = sums + rank * slots * kDenseRows + (threadIdx.x & 127);
         if (S == 1) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            finish(c0 + j, __uint_as_float(v[j]), SILU ? __uint_as_float(u[j]) : 0.f);
+          for (int j = 0; j < 16; ++j) to[(c0 + j) * kDenseRows] = __uint_as_float(raw[j]);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int r = c0 + j;
             if (r >= n) break;
-            const int slot = r / S;
-            const uint32_t to = tc::cluster_addr(
-                sums + ((rank * slots + slot) * (SILU ? 2 : 1)) * kDenseRows + threadIdx.x, r - slot * S);
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to), "r"(v[j]) : "memory");
-            if (SILU)
-              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + kDenseRows * 4), "r"(u[j])
-                           : "memory");
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(tc::cluster_addr(
+                             to + (r >> log_parts) * kDenseRows, r & (S - 1))),
+                         "r"(raw[j])
+                         : "memory");
           }
         }
       }
@@ -657,27 +700,41 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     cluster_wait();
   }
   __syncwarp();
-  if (S > 1) {
+  if (S > 1)
     cluster_sync();   // the parts have landed, and no CTA reaches into another after it
-    if (warp < 4 && ok) {
-      for (int r = rank, slot = 0; r < n; r += S, ++slot) {
-        float v = 0.f, up = 0.f;
-        for (int j = 0; j < S; ++j) {
-          const float* from = sums + ((j * slots + slot) * (SILU ? 2 : 1)) * kDenseRows + threadIdx.x;
-          v += from[0];
-          if (SILU) up += from[kDenseRows];
+  else
+    __syncthreads();
+  if (warp < 8) pdl_wait();
+  if (warp < 8 && ok && out_m < p.M) {
+#pragma unroll 2
+    for (int slot = threadIdx.x / kGroups; (slot << log_parts) + rank < n;
+         slot += kSplitEpilogue / kGroups) {
+      float v[8], up[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = up[i] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < S; ++j) {
+        const float4* from =
+            reinterpret_cast<const float4*>(sums + (j * slots + slot) * kDenseRows + 8 * grp);
+        const float4 a = from[0], b = from[1];
+        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+        if constexpr (SILU) {
+          const float4 c = from[kTile / 4], d = from[kTile / 4 + 1];
+          up[0] += c.x, up[1] += c.y, up[2] += c.z, up[3] += c.w;
+          up[4] += d.x, up[5] += d.y, up[6] += d.z, up[7] += d.w;
         }
-        finish(r, v, up);
       }
+      split_finish<SILU>(p, (size_t)(r0 + (slot << log_parts) + rank), out_m, v, up, bias, up_bias);
     }
   }
   __syncthreads();
   // copies of a dead CTA may still be in flight
-  if (warp == 4 && *dead)
+  if (warp == 8 && *dead)
     for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
   __syncthreads();
   tc::fence_after();
-  if (warp == 5) tc::tmem_dealloc(tmem, tcols);
+  if (warp == 9) tc::tmem_dealloc(tmem, tcols);
 }
 
 }  // namespace moe

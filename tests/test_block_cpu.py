@@ -103,12 +103,12 @@ def test_dense_plans_keep_the_kernels_limits(lib):
         if p.split:
             assert p.nt % 16 == 0 and 16 <= p.nt <= 128 and p.stages <= 16
             assert p.parts in (1, 2, 4, 8) and p.parts <= nk
-            # barriers, ring, sums; two CTAs an SM and no third
-            stage = two * 16384 + p.nt * 128
-            sums = two * -(-p.nt // p.parts) * p.parts * 512 if p.parts > 1 else 0
-            assert 2048 + p.stages * stage + sums <= p.smem <= 113 * 1024
-            assert 3 * (p.smem + 1024) > 228 * 1024 and 2 * p.nt * two <= 512
-            assert p.ctas == -(-M // 128) * -(-R // p.nt) * p.parts
+            # barriers, ring, sums; at most two CTAs an SM, whose tensor memory it has
+            stage, sums = 16384 + p.nt * 128, p.nt * 512
+            assert sums <= p.stages * stage
+            assert 2048 + p.stages * stage + (sums if p.parts > 1 else 0) <= p.smem <= 226 * 1024
+            assert 3 * (p.smem + 1024) > 228 * 1024 and 2 * p.nt <= 512
+            assert p.ctas == -(-M // (64 if act else 128)) * -(-R // p.nt) * p.parts
         else:
             assert p.nt % 32 == 0 and 32 <= p.nt <= 256 // two and p.smem <= 232448
             assert p.ctas == 2 * min(max(1, sms // 2), -(-M // 256) * -(-R // p.nt))
