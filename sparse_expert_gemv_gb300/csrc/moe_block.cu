@@ -101,7 +101,7 @@ struct DensePlan {
   bool split;
   int nt;       // rows of x a tile
   int S;        // parts of K (split)
-  int stages;   // of the ring (split)
+  int stages;   // of the ring
   double us;    // by the model below
 };
 
@@ -119,6 +119,10 @@ size_t split_smem(const DensePlan& p) {
   const int need = 1024 + moe::kSplitBars + p.stages * moe::split_stage_bytes(p.nt) +
                    moe::split_sum_bytes(p.nt, p.S);
   return std::max(need, kSplitSmemMin);
+}
+
+int tiles_stages(bool silu, int nt) {
+  return silu ? moe::DenseSmem<true>::stages(nt) : moe::DenseSmem<false>::stages(nt);
 }
 
 // The cheapest cut by a model of its time, in us. Its constants were fitted to 560
@@ -145,7 +149,7 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
     const double bytes = (128 * two + nt / 2) * 128.0;   // a stage's, of one CTA
     const double stage = std::max({0.0012 * two * nt, bytes / 108.8e3,
                                    std::min<double>(tiles, pairs) * 2 * bytes / kL2});
-    take({false, nt, 1, 0, kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
+    take({false, nt, 1, tiles_stages(silu, nt), kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
                                0.0082 * std::min(nt, R)});
   }
   const double hbm = 2.0 * c.K * ((double)c.N + R) / 6.8e6;
@@ -178,14 +182,14 @@ int log2_of(int v) {
   return l;
 }
 
-constexpr size_t kDenseSmem[2] = {moe::DenseSmem<false>::total + 1024,
-                                  moe::DenseSmem<true>::total + 1024};
+constexpr size_t kDenseSmem = moe::kDenseSmemMax + 1024;
+static_assert(kDenseSmem <= 232448, "shared memory of a CTA");
 
 template <bool SILU>
 bool set_dense_attributes() {
   return cudaFuncSetAttribute(moe::moe_dense_tiles<SILU>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)kDenseSmem[SILU]) == cudaSuccess &&
+                              (int)kDenseSmem) == cudaSuccess &&
          cudaFuncSetAttribute(moe::moe_dense_split<SILU>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               kSplitFull) == cudaSuccess;
@@ -379,7 +383,7 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
                 moe::kSplitThreads, split_smem(plan), stream, plan.S, p, log2_of(plan.S));
   else
     st = launch(silu ? moe::moe_dense_tiles<true> : moe::moe_dense_tiles<false>, ctas,
-                moe::kDenseThreads, kDenseSmem[silu], stream, 2, p);
+                moe::kDenseThreads, kDenseSmem, stream, 2, p);
   if (st == MOE_OK) m->mark_done(static_cast<cudaStream_t>(stream));
   return st;
 }
@@ -396,9 +400,8 @@ moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t nu
   out->split = p.split;
   out->nt = p.nt;
   out->parts = p.S;
-  out->stages = p.split ? p.stages
-                        : silu ? moe::DenseSmem<true>::stages : moe::DenseSmem<false>::stages;
-  out->smem = (int)(p.split ? split_smem(p) : kDenseSmem[silu]);
+  out->stages = p.stages;
+  out->smem = (int)(p.split ? split_smem(p) : kDenseSmem);
   out->ctas = ctas;
   return MOE_OK;
 }

@@ -41,7 +41,7 @@ struct DenseParams {
   int vec;                   // rows of out and residual take 16-byte accesses
   int nt;                    // rows of x a tile
   int mt, tt;                // tiles along M and R
-  int stages;                // of the ring (split)
+  int stages;                // of the ring
   uint32_t polls;            // of a bounded wait: kMbarPolls
   uint32_t withheld;         // 1: stages lack an arrival, so that waits run out (tests)
 };
@@ -188,18 +188,30 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const
 constexpr int kDenseThreads = 384;
 constexpr int kDenseChunk = 32 * 256;   // epilogue staging: 32 rows of 128 bf16
 
+constexpr int kDenseStages = 12;        // of the ring, at most
+constexpr int kDenseSmemMax = 232448 - 1024;
+
+// The ring takes what the epilogue's chunks leave: a slot's way from the MMA's
+// release through a copy back to the MMA takes more than a microsecond, and narrow
+// tiles' stages are small (router logits of 8191 x 7168 x 256 in tiles of 128 rows:
+// 30.4 us with six stages, FIGURE with eight).
 template <bool SILU>
 struct DenseSmem {
   static constexpr int cols = SILU ? kDenseCols / 2 : kDenseCols;   // rows of x a tile, at most
-  static constexpr int stages = SILU ? 5 : 6;
-  static constexpr int stage = (SILU ? 2 : 1) * kDenseABytes + cols / 2 * kDenseK * 2;
-  static constexpr int chunks = SILU ? 1 : 2;              // a group's, in turn
-  static constexpr int out = stages * stage;               // [2 groups][chunks]
+  static constexpr int chunks = SILU ? 1 : 2;                      // a group's, in turn
+  static constexpr int out = 0;                                    // [2 groups][chunks]
   static constexpr int bars = out + 2 * chunks * kDenseChunk;
-  static constexpr int total = bars + (2 * stages + 5) * 8 + 16;
+  static constexpr int ring = bars + 1024;
+  __host__ __device__ static constexpr int stage(int nt) {
+    return (SILU ? 2 : 1) * kDenseABytes + nt / 2 * kDenseK * 2;
+  }
+  __host__ __device__ static constexpr int stages(int nt) {
+    return (kDenseSmemMax - ring) / stage(nt) < kDenseStages ? (kDenseSmemMax - ring) / stage(nt)
+                                                             : kDenseStages;
+  }
 };
-static_assert(DenseSmem<false>::total + 1024 <= 232448 && DenseSmem<true>::total + 1024 <= 232448,
-              "shared memory of a CTA");
+static_assert((2 * kDenseStages + 5) * 8 + 16 <= 1024, "barriers");
+static_assert(DenseSmem<false>::stages(256) >= 6 && DenseSmem<true>::stages(128) >= 5, "ring");
 
 // Tile i of a call: bands of kDenseBand token tiles, within a band all token
 // tiles of a weight tile in turn, so that pairs side by side share both
@@ -221,8 +233,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   using L = DenseSmem<SILU>;
   constexpr int kA = (SILU ? 2 : 1) * kDenseABytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
-  uint64_t* empty = full + L::stages;
-  uint64_t* d_full = empty + L::stages;
+  uint64_t* empty = full + kDenseStages;
+  uint64_t* d_full = empty + kDenseStages;
   uint64_t* d_empty = d_full + 2;                                 // used in the first CTA
   uint64_t* drain = d_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -232,11 +244,13 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   const int rank = blockIdx.x & 1;   // clusters are pairs of neighbours
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
   const int tiles = p.mt * p.tt;
+  const int stages = p.stages, stage_bytes = L::stage(p.nt);
+  uint8_t* ring = smem + L::ring;
 
   if (warp == 0 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
     tc::prefetch_tmap(&p.tm_x);
-    for (int i = 0; i < L::stages; ++i) {
+    for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1 + p.withheld);   // the announcement of both CTAs' bytes
       mbar_init(&empty[i], 1);
     }
@@ -258,12 +272,12 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies
-    RingPos rg(L::stages);
+    RingPos rg(stages);
     const uint32_t full0 = tc::cluster_addr(full, 0);
     const int half = p.nt / 2;
     const uint32_t bytes = 2 * (kA + half * kDenseK * 2);
     auto weights = [&](int s, int m, int kb) {
-      uint8_t* dst = smem + s * L::stage;
+      uint8_t* dst = ring + s * stage_bytes;
       const int n = (2 * m + rank) * kDenseRows;
       if (rank == 0) tc::expect(&full[s], bytes);
       tc::tma2_load_2d(dst, &p.tm_w, kb * kDenseK, n, full0 + 8 * s);
@@ -275,7 +289,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     int ahead = 0, m, t;
     if (first < tiles) {
       dense_tile(p, first, m, t);
-      for (; ahead < min(p.nk, L::stages); ++ahead) weights(ahead, m, ahead);
+      for (; ahead < min(p.nk, stages); ++ahead) weights(ahead, m, ahead);
     }
     pdl_wait();
     int g = 0;
@@ -285,19 +299,25 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
       const int r0 = t * p.nt + rank * half;
       for (int kb = 0; kb < p.nk; ++kb, ++g) {
         const int s = rg.slot;
-        if (g >= L::stages && !dense_wait<true>(&empty[s], rg.phase ^ 1u, p, dead)) {
+        if (g >= stages && !dense_wait<true>(&empty[s], rg.phase ^ 1u, p, dead)) {
           ok = false;
           break;
         }
         if (g >= ahead) weights(s, m, kb);
-        tc::tma2_load_2d(smem + s * L::stage + kA, &p.tm_x, kb * kDenseK, r0, full0 + 8 * s);
+        tc::tma2_load_2d(ring + s * stage_bytes + kA, &p.tm_x, kb * kDenseK, r0, full0 + 8 * s);
         rg.next();
       }
+    }
+    // every arrival that the first CTA's MMAs make here, before this one may leave
+    if (g < stages) rg.slot = 0, rg.phase = 1u;
+    for (int j = 0; ok && j < min(g, stages); ++j) {
+      ok = dense_wait<true>(&empty[rg.slot], rg.phase ^ 1u, p, dead);
+      rg.next();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (rank == 0) {
-      RingPos rg(L::stages);
+      RingPos rg(stages);
       const uint32_t idesc = tc::f16_idesc(2 * kDenseRows, p.nt);
       int lt = 0;
       bool ok = true;
@@ -311,7 +331,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           const int s = rg.slot;
           ok = dense_wait<true>(&full[s], rg.phase, p, dead);
           if (!ok) break;
-          const uint32_t base = smem_addr(smem + s * L::stage);
+          const uint32_t base = smem_addr(ring + s * stage_bytes);
           const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kA);
           const uint64_t ud = tc::sdesc_sw128(base + kDenseABytes);
 #pragma unroll
