@@ -19,8 +19,8 @@
 struct moe_dense : moe::Handle {
   moe_dense_config_t cfg;
   int num_sms;
-  CUtensorMap tm_w;       // boxes of 128 rows
-  CUtensorMap tm_w_half;  // of 64
+  CUtensorMap tm_tiles, tm_split;   // the weight as the two kernels take it
+  int groups;                       // tm_tiles has groups of 16 rows
   const uint16_t* bias;
   std::atomic<bool> armed;   // the next run's waits run out (moe_dense_arm_timeout)
 };
@@ -96,6 +96,26 @@ bool encode_rows(CUtensorMap* tm, const void* base, int rows, int K, int box) {
   return moe::encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, b);
 }
 
+// The gate and up rows of neurons 16 g.. as [g][gate, up][16][K], four groups a box.
+bool encode_groups(CUtensorMap* tm, const void* w, int I, int K) {
+  const cuuint64_t row = (cuuint64_t)K * 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)K, 16, 2, (cuuint64_t)I / 16};
+  const cuuint64_t strides[3] = {row, I * row, 16 * row};
+  const cuuint32_t box[4] = {moe::kDenseK, 16, 2, 4};
+  return moe::encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, w, dims, strides, box);
+}
+
+bool encode_weight(moe_dense* m, const uint16_t* w) {
+  const moe_dense_config_t& c = m->cfg;
+  if (!is_silu(c))
+    return encode_rows(&m->tm_tiles, w, c.N, c.K, moe::kDenseRows) &&
+           encode_rows(&m->tm_split, w, c.N, c.K, moe::kDenseRows);
+  m->groups = c.N / 2 % 16 == 0;
+  return (m->groups ? encode_groups(&m->tm_tiles, w, c.N / 2, c.K)
+                    : encode_rows(&m->tm_tiles, w, c.N, c.K, 16)) &&
+         encode_rows(&m->tm_split, w, c.N, c.K, moe::kDenseRows / 2);
+}
+
 // How a call is cut.
 struct DensePlan {
   bool split;
@@ -121,10 +141,6 @@ size_t split_smem(const DensePlan& p) {
   return std::max(need, kSplitSmemMin);
 }
 
-int tiles_stages(bool silu, int nt) {
-  return silu ? moe::DenseSmem<true>::stages(nt) : moe::DenseSmem<false>::stages(nt);
-}
-
 // The cheapest cut by a model of its time, in us. Its constants were fitted to 560
 // timings (24 shapes from 1 to 4096 rows, every cut of each, inputs beyond L2); its
 // choices are on average 1.4 % slower than the best of them, 9 % at worst.
@@ -135,7 +151,7 @@ int tiles_stages(bool silu, int nt) {
 //           bytes' way into an SM
 DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
   const bool silu = is_silu(c);
-  const int M = silu ? c.N / 2 : c.N, two = silu ? 2 : 1;
+  const int M = silu ? c.N / 2 : c.N;
   const int nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
   constexpr double kStart = 0.16, kL2 = 14.7e6;   // us, bytes a us
   DensePlan best{false, 0, 1, 0, 0.0};
@@ -143,13 +159,13 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
     if (!best.nt || p.us < best.us) best = p;
   };
   const int pairs = std::max(1, num_sms / 2);
-  for (int nt = moe::kDenseCols / two; nt >= 32; nt -= 32) {
+  for (int nt = moe::kDenseCols; nt >= 32; nt -= 32) {
     if (nt - 32 >= R) continue;
-    const double tiles = std::ceil(M / 256.0) * std::ceil((double)R / nt);
-    const double bytes = (128 * two + nt / 2) * 128.0;   // a stage's, of one CTA
-    const double stage = std::max({0.0012 * two * nt, bytes / 108.8e3,
+    const double tiles = std::ceil(M / (silu ? 128.0 : 256.0)) * std::ceil((double)R / nt);
+    const double bytes = moe::DenseSmem::stage(nt);   // a stage's, of one CTA
+    const double stage = std::max({0.0012 * nt, bytes / 108.8e3,
                                    std::min<double>(tiles, pairs) * 2 * bytes / kL2});
-    take({false, nt, 1, tiles_stages(silu, nt), kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
+    take({false, nt, 1, moe::DenseSmem::stages(nt), kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
                                0.0082 * std::min(nt, R)});
   }
   const double hbm = 2.0 * c.K * ((double)c.N + R) / 6.8e6;
@@ -204,7 +220,7 @@ moe_status_t check_dense(const moe_dense_config_t& c) {
 // Tiles along M and R and the CTAs of a launch; false when there are too many.
 bool dense_grid(const moe_dense_config_t& c, const DensePlan& p, int R, int num_sms, int& mt, int& tt,
                 int& ctas) {
-  const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = p.split ? (is_silu(c) ? 64 : 128) : 256;
+  const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = (p.split ? 128 : 256) / (is_silu(c) ? 2 : 1);
   const int64_t m = (M + rows - 1) / rows, t = ((int64_t)R + p.nt - 1) / p.nt;
   if (m * t * p.S > 0x3fffffff) return false;
   mt = (int)m;
@@ -326,8 +342,7 @@ moe_status_t moe_dense_create(const moe_dense_config_t* cfg, const uint16_t* wei
       cudaGetDevice(&m->device) == cudaSuccess &&
       cudaDeviceGetAttribute(&m->num_sms, cudaDevAttrMultiProcessorCount, m->device) ==
           cudaSuccess &&
-      encode_rows(&m->tm_w, weight, c.N, c.K, moe::kDenseRows) &&
-      encode_rows(&m->tm_w_half, weight, c.N, c.K, moe::kDenseRows / 2) &&
+      encode_weight(m, weight) &&
       (is_silu(c) ? set_dense_attributes<true>() : set_dense_attributes<false>()) &&
       m->acquire(nullptr) && cudaStreamSynchronize(nullptr) == cudaSuccess;
   if (!ok) {
@@ -363,7 +378,8 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   p.nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
   int ctas;
   if (!dense_grid(c, plan, R, m->num_sms, p.mt, p.tt, ctas)) return MOE_ERR_UNSUPPORTED_SHAPE;
-  p.tm_w = plan.split && silu ? m->tm_w_half : m->tm_w;
+  p.tm_w = plan.split ? m->tm_split : m->tm_tiles;
+  p.groups = m->groups;
   if (!encode_rows(&p.tm_x, x, R, c.K, plan.split ? plan.nt : plan.nt / 2)) return MOE_ERR_CUDA;
   p.bias = m->bias;
   p.residual = residual;

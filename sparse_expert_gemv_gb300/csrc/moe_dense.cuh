@@ -30,7 +30,9 @@ constexpr int kDenseABytes = kDenseRows * kDenseK * 2;
 constexpr int kDenseCols = 256;   // rows of x a tile of moe_dense_tiles, at most
 
 struct DenseParams {
-  CUtensorMap tm_w;          // boxes of 128 rows
+  // boxes of 128 rows; with SILU_MUL of 64 (split), or (tiles) [groups of 16][gate,
+  // up][16 rows] in boxes of four groups, or where I is no multiple of 16, of 16 rows
+  CUtensorMap tm_w;
   CUtensorMap tm_x;          // boxes of nt / 2 rows (tiles), nt rows (split)
   const uint16_t* bias;      // [N] or null
   const uint16_t* residual;  // [R, M] or null
@@ -42,6 +44,7 @@ struct DenseParams {
   int nt;                    // rows of x a tile
   int mt, tt;                // tiles along M and R
   int stages;                // of the ring
+  int groups;                // tm_w has the groups of 16 (tiles, SILU_MUL)
   uint32_t polls;            // of a bounded wait: kMbarPolls
   uint32_t withheld;         // 1: stages lack an arrival, so that waits run out (tests)
 };
@@ -135,6 +138,16 @@ __device__ __forceinline__ void tma1_load_2d(void* dst, const void* tmap, int x,
       : "memory");
 }
 
+__device__ __forceinline__ void tma2_load_4d(void* dst, const void* tmap, int c0, int c1, int c2,
+                                             int c3, uint32_t bar) {
+  asm volatile(
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];\n\t}" ::"r"(smem_addr(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
 // The inverse of stm4_trans.
 __device__ __forceinline__ void ldm4_trans(uint32_t addr, uint32_t (&v)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -182,8 +195,8 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const
 //   warps 4-11  epilogue, one per lane quarter of tensor memory, two groups of
 //               four that take chunks of 32 rows in turn
 // Two accumulators in tensor memory let the epilogue of a tile overlap the next
-// tile's MMAs. With SILU a tile is 256 gate rows, the 256 up rows of the same
-// neurons and up to 128 rows of x, and an accumulator holds both.
+// tile's MMAs. With SILU a tile is 128 neurons' gate and up rows, 16 and 16 in turn,
+// so that each epilogue warp has a neuron's gate and up in one thread.
 // ---------------------------------------------------------------------------
 constexpr int kDenseThreads = 384;
 constexpr int kDenseChunk = 32 * 256;   // epilogue staging: 32 rows of 128 bf16
@@ -194,24 +207,19 @@ constexpr int kDenseSmemMax = 232448 - 1024;
 // The ring takes what the epilogue's chunks leave: a slot's way from the MMA's
 // release through a copy back to the MMA takes more than a microsecond, and narrow
 // tiles' stages are small (router logits of 8191 x 7168 x 256 in tiles of 128 rows:
-// 30.4 us with six stages, FIGURE with eight).
-template <bool SILU>
+// 30.4 us with six stages, 27.5 with eight).
 struct DenseSmem {
-  static constexpr int cols = SILU ? kDenseCols / 2 : kDenseCols;   // rows of x a tile, at most
-  static constexpr int chunks = SILU ? 1 : 2;                      // a group's, in turn
-  static constexpr int out = 0;                                    // [2 groups][chunks]
-  static constexpr int bars = out + 2 * chunks * kDenseChunk;
+  static constexpr int out = 0;                     // [2 groups][2] chunks
+  static constexpr int bars = out + 4 * kDenseChunk;
   static constexpr int ring = bars + 1024;
-  __host__ __device__ static constexpr int stage(int nt) {
-    return (SILU ? 2 : 1) * kDenseABytes + nt / 2 * kDenseK * 2;
-  }
+  __host__ __device__ static constexpr int stage(int nt) { return kDenseABytes + nt / 2 * kDenseK * 2; }
   __host__ __device__ static constexpr int stages(int nt) {
     return (kDenseSmemMax - ring) / stage(nt) < kDenseStages ? (kDenseSmemMax - ring) / stage(nt)
                                                              : kDenseStages;
   }
 };
 static_assert((2 * kDenseStages + 5) * 8 + 16 <= 1024, "barriers");
-static_assert(DenseSmem<false>::stages(256) >= 6 && DenseSmem<true>::stages(128) >= 5, "ring");
+static_assert(DenseSmem::stages(kDenseCols) >= 6, "ring");
 
 // Tile i of a call: bands of kDenseBand token tiles, within a band all token
 // tiles of a weight tile in turn, so that pairs side by side share both
@@ -230,8 +238,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  using L = DenseSmem<SILU>;
-  constexpr int kA = (SILU ? 2 : 1) * kDenseABytes;
+  using L = DenseSmem;
+  constexpr int kOut = SILU ? kDenseRows / 2 : kDenseRows;   // outputs of a CTA's tile
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);   // used in the first CTA
   uint64_t* empty = full + kDenseStages;
   uint64_t* d_full = empty + kDenseStages;
@@ -275,14 +283,21 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     RingPos rg(stages);
     const uint32_t full0 = tc::cluster_addr(full, 0);
     const int half = p.nt / 2;
-    const uint32_t bytes = 2 * (kA + half * kDenseK * 2);
+    const uint32_t bytes = 2 * (kDenseABytes + half * kDenseK * 2);
     auto weights = [&](int s, int m, int kb) {
       uint8_t* dst = ring + s * stage_bytes;
-      const int n = (2 * m + rank) * kDenseRows;
+      const int n = (2 * m + rank) * kOut;
       if (rank == 0) tc::expect(&full[s], bytes);
-      tc::tma2_load_2d(dst, &p.tm_w, kb * kDenseK, n, full0 + 8 * s);
-      if (SILU)
-        tc::tma2_load_2d(dst + kDenseABytes, &p.tm_w, kb * kDenseK, p.M + n, full0 + 8 * s);
+      if constexpr (!SILU) {
+        tc::tma2_load_2d(dst, &p.tm_w, kb * kDenseK, n, full0 + 8 * s);
+      } else if (p.groups) {
+        tc::tma2_load_4d(dst, &p.tm_w, kb * kDenseK, 0, 0, n / 16, full0 + 8 * s);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          tc::tma2_load_2d(dst + i * 16 * 128, &p.tm_w, kb * kDenseK,
+                           n + 16 * (i >> 1) + (i & 1) * p.M, full0 + 8 * s);
+      }
     };
     // the first stages' weights, which no earlier kernel writes, come before the
     // wait for the kernels before this one
@@ -304,7 +319,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           break;
         }
         if (g >= ahead) weights(s, m, kb);
-        tc::tma2_load_2d(ring + s * stage_bytes + kA, &p.tm_x, kb * kDenseK, r0, full0 + 8 * s);
+        tc::tma2_load_2d(ring + s * stage_bytes + kDenseABytes, &p.tm_x, kb * kDenseK, r0, full0 + 8 * s);
         rg.next();
       }
     }
@@ -332,13 +347,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           ok = dense_wait<true>(&full[s], rg.phase, p, dead);
           if (!ok) break;
           const uint32_t base = smem_addr(ring + s * stage_bytes);
-          const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kA);
-          const uint64_t ud = tc::sdesc_sw128(base + kDenseABytes);
+          const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kDenseABytes);
 #pragma unroll
-          for (int q = 0; q < kDenseK / 16; ++q) {   // 32 bytes further in the swizzled rows
+          for (int q = 0; q < kDenseK / 16; ++q)   // 32 bytes further in the swizzled rows
             tc::mma_f16<true>(d, ad + 2 * q, bd + 2 * q, idesc, kb + q > 0 ? 1u : 0u);
-            if (SILU) tc::mma_f16<true>(d + 128, ud + 2 * q, bd + 2 * q, idesc, kb + q > 0 ? 1u : 0u);
-          }
           tc::commit2(&empty[s]);
           rg.next();
         }
@@ -353,37 +365,43 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     const int bar = 1 + grp;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
-    // this thread's 16 bytes of rows pr + 8 k of a chunk, and its place in the
-    // matrices that turn 32 columns of tensor memory into rows: 16-byte piece
-    // 4q + m of row r holds weight rows 8m.. and sits at piece ^ (r & 7)
-    const int pc = et & 15, pr = et >> 4;
-    const int mr = lane & 7;
-    const uint32_t mat = mr * 256 + (((4 * q + (lane >> 3)) ^ mr) << 4);
+    // a chunk: 32 rows of x by kOut outputs, of which a thread moves 16 bytes of rows
+    // pr + kRows k
+    constexpr int kPieces = kOut / 8, kRows = 128 / kPieces, kMoves = 32 / kRows;
+    const int pc = et & (kPieces - 1), pr = et / kPieces;
+    const uint32_t moved = pr * kOut * 2 + ((pc ^ (pr & 7)) << 4);   // (kRows is a multiple of 8)
+    // its row of the matrices that turn 32 columns of tensor memory into rows:
+    // 16-byte piece kPieces / 4 q + i of row r holds outputs 8 i.. of this warp's and
+    // sits at piece ^ (r & 7). Without SILU matrix m of four is output group m, with
+    // SILU m & 1 of rows 8 (m >> 1) further
+    const int mr = lane & 7, mm = lane >> 3;
+    const uint32_t mat =
+        SILU ? (8 * (mm >> 1) + mr) * kOut * 2 + (((2 * q + (mm & 1)) ^ mr) << 4)
+             : mr * kOut * 2 + (((4 * q + mm) ^ mr) << 4);
     int lt = 0, chunk = 0;
     pdl_wait();
     for (int i = first; i < tiles; i += step, ++lt) {
       int m, t;
       dense_tile(p, i, m, t);
-      const int n0 = (2 * m + rank) * kDenseRows, r0 = t * p.nt;
+      const int n0 = (2 * m + rank) * kOut, r0 = t * p.nt;
       const int n = min(p.nt, p.R - r0), pn = n0 + 8 * pc;
       const int buf = lt & 1;
-      // bias of this thread's weight rows 8 k + lane / 4 of the warp's 32
-      float bias[SILU ? 8 : 4] = {};
+      // bias of this thread's weight rows 8 k + lane / 4 of the warp's 32 (with SILU the
+      // last two are its neurons' up rows)
+      float bias[4] = {};
       if (p.bias) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int row = n0 + 32 * q + 8 * k + (lane >> 2);
-          if (row < p.M) {
-            bias[k] = bf16_at(p.bias + row);
-            if constexpr (SILU) bias[4 + k] = bf16_at(p.bias + p.M + row);
-          }
+          const int row = SILU ? n0 + 16 * q + 8 * (k & 1) + (lane >> 2)
+                               : n0 + 32 * q + 8 * k + (lane >> 2);
+          if (row < p.M) bias[k] = bf16_at(p.bias + row + (SILU && k > 1 ? p.M : 0));
         }
       }
-      uint4 res[4];
+      uint4 res[kMoves];
       auto load_residual = [&](int c0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = c0 + pr + 8 * k;
+        for (int k = 0; k < kMoves; ++k) {
+          const int row = c0 + pr + kRows * k;
           res[k] = make_uint4(0, 0, 0, 0);
           if (row >= n || pn >= p.M) continue;
           const uint16_t* src = p.residual + (size_t)(r0 + row) * p.M + pn;
@@ -407,72 +425,71 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
       if (!ok) break;
       tc::fence_after();
       for (int c0 = 32 * grp; c0 < n; c0 += 64, ++chunk) {
-        uint8_t* stage = smem + L::out + (grp * L::chunks + chunk % L::chunks) * kDenseChunk;
+        uint8_t* stage = smem + L::out + (2 * grp + (chunk & 1)) * kDenseChunk;
         // register 4 b + 2 i + j of the two halves: weight row 8 i + lane / 4 (16
         // further in the second), row 8 b + 2 (lane % 4) + j of x
+        constexpr int kVals = SILU ? 16 : 32;
         uint32_t raw[2][16];
-        float v[32];
+        float v[kVals];
         tc::ld_16x32(lanes + buf * 256 + c0, raw[0]);
         tc::ld_16x32(lanes + (16u << 16) + buf * 256 + c0, raw[1]);
         tc::wait_ld();
-#pragma unroll
-        for (int x = 0; x < 32; ++x)
-          v[x] = __uint_as_float(raw[x >> 4][x & 15]) + bias[2 * (x >> 4) + ((x >> 1) & 1)];
         if constexpr (SILU) {
-          tc::ld_16x32(lanes + buf * 256 + 128 + c0, raw[0]);
-          tc::ld_16x32(lanes + (16u << 16) + buf * 256 + 128 + c0, raw[1]);
-          tc::wait_ld();
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            v[x] = dense_silu(__uint_as_float(raw[0][x]) + bias[(x >> 1) & 1]) *
+                   (__uint_as_float(raw[1][x]) + bias[2 + ((x >> 1) & 1)]);
+        } else {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            v[x] = dense_silu(v[x]) * (__uint_as_float(raw[x >> 4][x & 15]) +
-                                       bias[4 + 2 * (x >> 4) + ((x >> 1) & 1)]);
-        } else {
+            v[x] = __uint_as_float(raw[x >> 4][x & 15]) + bias[2 * (x >> 4) + ((x >> 1) & 1)];
           dense_act(p.act, v);
         }
+        // value of pair k (of two rows of x) of matrix set b: four matrices a set
+        auto at = [](int b, int k) {
+          return SILU ? 8 * b + 4 * (k >> 1) + 2 * (k & 1) : 16 * (k >> 1) + 4 * b + 2 * (k & 1);
+        };
+        constexpr int kSets = kVals / 8;
+        constexpr uint32_t kSetBytes = (SILU ? 16 : 8) * kOut * 2;
         const uint32_t mats = smem_addr(stage) + mat;
         if (p.residual) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(stage + (pr + 8 * k) * 256 + ((pc ^ (pr & 7)) << 4)) = res[k];
+          for (int k = 0; k < kMoves; ++k)
+            *reinterpret_cast<uint4*>(stage + moved + k * kRows * kOut * 2) = res[k];
           if (c0 + 64 < n) load_residual(c0 + 64);
           named_sync(bar, 128);
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
+          for (int b = 0; b < kSets; ++b) {
             uint32_t w[4];
-            tc::ldm4_trans(mats + b * 8 * 256, w);
+            tc::ldm4_trans(mats + b * kSetBytes, w);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int x = 16 * (k >> 1) + 4 * b + 2 * (k & 1);
-              v[x] += bf16_lo(w[k]);
-              v[x + 1] += bf16_hi(w[k]);
+              v[at(b, k)] += bf16_lo(w[k]);
+              v[at(b, k) + 1] += bf16_hi(w[k]);
             }
           }
         }
         if (p.out_float) {
           float* out = static_cast<float*>(p.out);
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < kVals; ++x) {
             const int row = c0 + 8 * ((x >> 2) & 3) + 2 * (lane & 3) + (x & 1);
-            const int col = n0 + 32 * q + 16 * (x >> 4) + 8 * ((x >> 1) & 1) + (lane >> 2);
+            const int col = n0 + kOut / 4 * q + 16 * (x >> 4) + 8 * ((x >> 1) & 1) + (lane >> 2);
             if (row < n && col < p.M) out[(size_t)(r0 + row) * p.M + col] = v[x];
           }
         } else {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            auto pack = [&](int k) {
-              const int x = 16 * (k >> 1) + 4 * b + 2 * (k & 1);
-              return RowVec<8>::pack(v[x], v[x + 1]);
-            };
-            tc::stm4_trans(mats + b * 8 * 256, pack(0), pack(1), pack(2), pack(3));
+          for (int b = 0; b < kSets; ++b) {
+            auto pack = [&](int k) { return RowVec<8>::pack(v[at(b, k)], v[at(b, k) + 1]); };
+            tc::stm4_trans(mats + b * kSetBytes, pack(0), pack(1), pack(2), pack(3));
           }
           named_sync(bar, 128);
           uint16_t* out = static_cast<uint16_t*>(p.out);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row = c0 + pr + 8 * k;
+          for (int k = 0; k < kMoves; ++k) {
+            const int row = c0 + pr + kRows * k;
             if (row >= n || pn >= p.M) continue;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + (pr + 8 * k) * 256 +
-                                                            ((pc ^ (pr & 7)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + moved + k * kRows * kOut * 2);
             uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
             if (p.vec) {
               *reinterpret_cast<uint4*>(dst) = w;
@@ -484,7 +501,6 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
             }
           }
         }
-        if (L::chunks == 1) named_sync(bar, 128);   // the chunk's place is free again
       }
       tc::fence_before();
       __syncwarp();

@@ -110,8 +110,9 @@ def test_dense_plans_keep_the_kernels_limits(lib):
             assert 3 * (p.smem + 1024) > 228 * 1024 and 2 * p.nt <= 512
             assert p.ctas == -(-M // (64 if act else 128)) * -(-R // p.nt) * p.parts
         else:
-            assert p.nt % 32 == 0 and 32 <= p.nt <= 256 // two and p.smem <= 232448
-            assert p.ctas == 2 * min(max(1, sms // 2), -(-M // 256) * -(-R // p.nt))
+            assert p.nt % 32 == 0 and 32 <= p.nt <= 256 and p.smem <= 232448 and p.stages <= 12
+            assert 1024 + 4 * 8192 + 1024 + p.stages * (16384 + p.nt * 64) <= p.smem
+            assert p.ctas == 2 * min(max(1, sms // 2), -(-M // (256 // two)) * -(-R // p.nt))
     assert seen >= {(0, 1), (1, 1), (1, 2), (1, 4), (1, 8)}
 
 
