@@ -64,7 +64,7 @@ typedef struct {
  * is never chosen; one whose bias is NaN or -inf is never chosen. Slots for
  * which no expert is left get the id -1, which moe_group and the decode layer
  * take as an unused slot, and the weight 0. Softmax over infinite logits is
- * shared by those alone. Weights whose sum is 0 in FP32 are 0.
+ * shared by those alone; chosen scores that are all 0 give weights of 0.
  *   logits  float or bf16 [T, E]
  *   bias    float [E] or NULL
  *   ids     int32 [T, k];  w float [T, k]

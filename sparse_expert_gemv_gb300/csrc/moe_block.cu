@@ -32,22 +32,51 @@ using moe::launch;
 
 // ---- routing -----------------------------------------------------------------
 
+// What route_row with R experts a lane needs of p.
 template <int R>
-moe_status_t route_launch(moe::RouteParams p, void* stream) {
-  const int size = p.bf16 ? 2 : 4;
-  p.vec = p.E % R == 0 && aligned(p.logits, std::min(16, R * size));
+void route_prepare(moe::RouteParams& p) {
+  p.vec = p.E % R == 0 && aligned(p.logits, std::min(16, R * (p.bf16 ? 2 : 4)));
   p.lane_shift = -1;
   if (p.per % R == 0)
     for (int s = 0; s <= 5; ++s)
       if (p.per / R == 1 << s) p.lane_shift = s;
   p.bias_vec = p.E % R == 0 && aligned(p.bias, 16);
   p.smem = std::max(p.E * (int)sizeof(double), 128 * (R + 1));   // route_slow's, sorted keys
+}
+
+template <int R>
+moe_status_t route_launch(moe::RouteParams p, void* stream) {
+  route_prepare<R>(p);
   const size_t smem = (size_t)moe::kRouteWarps * p.smem;
   const unsigned grid = (p.T + moe::kRouteWarps - 1) / moe::kRouteWarps;
   return p.bf16 && !p.bias ? launch(moe::moe_route_experts_rows<R, true>, grid,
                                     moe::kRouteWarps * 32, smem, stream, 1, p)
                            : launch(moe::moe_route_experts_rows<R, false>, grid,
                                     moe::kRouteWarps * 32, smem, stream, 1, p);
+}
+
+// W lanes a token; rows that need it are decided by a whole warp.
+template <int W>
+moe_status_t route_packed_launch(moe::RouteParams p, void* stream) {
+  route_prepare<W>(p);
+  p.packed_shift = 0;
+  while (32 << p.packed_shift < p.per) ++p.packed_shift;
+  const int tokens = moe::kRouteWarps * (32 / W);
+  const size_t smem = (size_t)moe::kRouteWarps * p.smem;
+  const unsigned grid = (p.T + tokens - 1) / tokens;
+  return p.bf16 && !p.bias ? launch(moe::moe_route_experts_packed<W, true>, grid,
+                                    moe::kRouteWarps * 32, smem, stream, 1, p)
+                           : launch(moe::moe_route_experts_packed<W, false>, grid,
+                                    moe::kRouteWarps * 32, smem, stream, 1, p);
+}
+
+// Whether moe_route_experts_packed takes a call: many tokens, where it is the faster
+// one (figures at the kernel), lanes of 32 experts read in aligned vectors, groups of
+// whole lanes (and 2^n of them).
+bool route_packed(const moe::RouteParams& p) {
+  return p.T >= 4096 && (p.E == 64 || p.E == 128 || (p.E == 256 && !p.bias)) && p.k <= 8 &&
+         aligned(p.logits, 16) && aligned(p.bias, 16) &&
+         (p.groups == 1 || (p.per % 32 == 0 && (p.per / 32 & (p.per / 32 - 1)) == 0));
 }
 
 // ---- norms -------------------------------------------------------------------
@@ -271,6 +300,11 @@ moe_status_t moe_route_experts(const moe_route_config_t* cfg, int32_t T, const v
   p.sigmoid = (c.flags & MOE_ROUTE_SIGMOID) != 0;
   p.top2 = (c.flags & MOE_ROUTE_GROUP_TOP2) != 0;
   p.renormalize = (c.flags & MOE_ROUTE_RENORMALIZE) != 0;
+  if (route_packed(p)) {
+    if (c.E == 64) return route_packed_launch<2>(p, stream);
+    if (c.E == 128) return route_packed_launch<4>(p, stream);
+    return route_packed_launch<8>(p, stream);
+  }
   if (c.E <= 32) return route_launch<1>(p, stream);
   if (c.E <= 64) return route_launch<2>(p, stream);
   if (c.E <= 128) return route_launch<4>(p, stream);

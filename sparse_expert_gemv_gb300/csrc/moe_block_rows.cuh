@@ -38,6 +38,7 @@ struct RouteParams {
   // log2 of the lanes a group's experts lie in, where that is a whole power of
   // two; else -1
   int lane_shift;
+  int packed_shift;   // the same of moe_route_experts_packed's lanes
   float scale;
   int bf16, sigmoid, top2, renormalize;
   int vec;        // a lane's logits are one aligned piece of the row
@@ -138,6 +139,14 @@ __device__ __forceinline__ int route_slow(const RouteParams& p, int t, double* k
     if (lane == j) mine = at;
   }
   return mine;
+}
+
+// A chosen expert's score but for a factor of the row: the softmax's term relative to
+// `top`, or the sigmoid, relative to e^top where that is below 1, so that weights
+// keep their digits where all scores are tiny.
+__device__ __forceinline__ float route_weight(bool sigmoid, float l, float top) {
+  if (sigmoid) return (l < 0.f ? expf(l - fminf(top, 0.f)) : 1.f) / (1.f + expf(-fabsf(l)));
+  return top == -route_off() ? (l == top ? 1.f : 0.f) : expf(l - top);
 }
 
 // What expert e compares by, in FP64: its score plus bias, or with `plain` its
@@ -305,17 +314,12 @@ __device__ __forceinline__ void route_add_bias(const RouteParams& p, int e0, flo
   }
 }
 
-// EXACT: bf16 logits without a bias.
+// Token t by a whole warp, which has `own`, p.smem bytes of shared memory. EXACT:
+// bf16 logits without a bias.
 template <int R, bool EXACT>
-__global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 9 : 4) moe_route_experts_rows(
-    const __grid_constant__ RouteParams p) {
-  extern __shared__ double route_smem[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * kRouteWarps + warp;
+__device__ __forceinline__ void route_row(const RouteParams& p, const int t, uint8_t* const own) {
+  const int lane = threadIdx.x & 31;
   constexpr uint32_t kMask = EXACT ? 1023u : (uint32_t)R - 1u;
-  pdl_wait();
-  pdl_trigger();
-  if (t >= p.T) return;
   const int e0 = lane * R;
   float l[R];
   route_load<R>(p, t, lane, l);
@@ -373,7 +377,6 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 9 : 4) moe_route_ex
   };
   uint32_t key[R];
   make_keys(l, key);
-  uint8_t* own = reinterpret_cast<uint8_t*>(route_smem) + warp * p.smem;   // the warp's
   int* list = reinterpret_cast<int*>(own);
   // ---- groups
   const int shift = max(p.lane_shift, 0);
@@ -590,22 +593,333 @@ __global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 9 : 4) moe_route_ex
   if (lane >= p.k) mine = -1;
   // ---- the chosen experts' weights
   const float lm = mine >= 0 ? route_logit(p, (size_t)t * p.E + mine) : route_off();
-  float v = 0.f;
-  if (p.sigmoid) {
-    if (mine >= 0) v = 1.f / (1.f + expf(-lm));
-  } else {
-    // relative to the largest chosen logit where the sum is that of the chosen
-    const float top = p.renormalize ? warp_max(lm) : mx;
-    if (mine >= 0) v = top == -route_off() ? (lm == top ? 1.f : 0.f) : expf(lm - top);
-    if (!p.renormalize && mine >= 0) v /= z;
-  }
+  // Relative to the largest chosen logit where the sum is that of the chosen (and
+  // to infinite ones where there are any, which a bias may pass over).
+  const float top = p.renormalize && mx < -route_off() ? warp_max(lm) : p.sigmoid ? 0.f : mx;
+  float v = mine >= 0 ? route_weight(p.sigmoid, lm, top) : 0.f;
   if (p.renormalize) {
     const float sum = warp_sum(v);
     v = sum > 0.f ? v / sum : 0.f;
+  } else if (!p.sigmoid && mine >= 0) {
+    v /= z;
   }
   if (lane < p.k) {
     p.ids[(size_t)t * p.k + lane] = mine;
     p.w[(size_t)t * p.k + lane] = v * p.scale;
+  }
+}
+
+template <int R, bool EXACT>
+__global__ void __launch_bounds__(kRouteWarps * 32, R <= 8 ? 9 : 4) moe_route_experts_rows(
+    const __grid_constant__ RouteParams p) {
+  extern __shared__ double route_smem[];
+  const int warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kRouteWarps + warp;
+  pdl_wait();
+  pdl_trigger();
+  if (t < p.T) route_row<R, EXACT>(p, t, reinterpret_cast<uint8_t*>(route_smem) + warp * p.smem);
+}
+
+// ---------------------------------------------------------------------------
+// moe_route_experts_packed: many tokens of up to 256 experts, W lanes each with 32
+// experts (E = 32 W), at most 8 experts a token, groups of whole lanes. What a warp
+// does once a token in moe_route_experts_rows it does here for 32 / W tokens at once
+// (us of 16384 tokens, one way and the other: 64 experts 8.9 / 5.5, 128 in bf16 8.6 /
+// 5.3, with groups, a bias and sigmoids 13.5 / 12; 256 12.5 / 10.8, with a bias 17 / 19,
+// which therefore stay there, as do calls of fewer tokens: 4096 3.9 / 3.0, 1024 2.4 /
+// 2.9).
+//
+// Keys are signed fixed-point numbers of 27 bits (2^-24 of a score plus bias, 2^-20 of
+// a logit) over the expert's place in the lane, or a bf16's bits over its place of
+// all. A lane sorts its nine largest. Rows that this does not decide go to
+// route_row.
+// ---------------------------------------------------------------------------
+constexpr int kRouteListed = 9;   // 8 chosen and the first one left out
+constexpr int kRouteOff = INT32_MIN;
+
+// Keys in descending order, by the same network as route_sort.
+template <int R, int LO, int N, int S>
+__device__ __forceinline__ void key_merge(int (&k)[R]) {
+  if constexpr (2 * S < N) {
+    key_merge<R, LO, N, 2 * S>(k);
+    key_merge<R, LO + S, N, 2 * S>(k);
+  }
+#pragma unroll
+  for (int i = 2 * S < N ? LO + S : LO; i + S < LO + N; i += 2 * S) {
+    const int a = k[i], b = k[i + S];
+    k[i] = max(a, b);
+    k[i + S] = min(a, b);
+  }
+}
+template <int R, int LO, int N>
+__device__ __forceinline__ void key_sort(int (&k)[R]) {
+  if constexpr (N > 1) {
+    key_sort<R, LO, N / 2>(k);
+    key_sort<R, LO + N / 2, N / 2>(k);
+    key_merge<R, LO, N, 1>(k);
+  }
+}
+// k[A..A + 7] = the eight largest of the descending k[A..] and k[B..], in order;
+// `ninth` = the largest of those left over, or what it was.
+template <int A, int B>
+__device__ __forceinline__ void key_top8(int (&k)[32], int& ninth) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int a = k[A + i], b = k[B + 7 - i];
+    k[A + i] = max(a, b);
+    ninth = max(ninth, min(a, b));
+  }
+#pragma unroll
+  for (int s = 4; s > 0; s >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (!(i & s)) {
+        const int a = k[A + i], b = k[A + i + s];
+        k[A + i] = max(a, b);
+        k[A + i + s] = min(a, b);
+      }
+}
+
+// Nearest whole number, saturated.
+__device__ __forceinline__ int to_fixed(float v) {
+  int r;
+  asm("cvt.rni.s32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
+}
+
+template <int W, bool EXACT>
+__global__ void __launch_bounds__(kRouteWarps * 32, 5) moe_route_experts_packed(
+    const __grid_constant__ RouteParams p) {
+  extern __shared__ double route_smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int sub = lane & (W - 1), base = lane & ~(W - 1);
+  const int first = (blockIdx.x * kRouteWarps + warp) * (32 / W);
+  const int t = first + lane / W;
+  pdl_wait();
+  pdl_trigger();
+  if (first >= p.T) return;
+  const bool sums = p.groups > 1 && p.top2;
+  const bool scored = p.bias != nullptr || (sums && !EXACT);
+  auto sub_max = [&](int v) {
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) v = max(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+  };
+  auto sub_sum = [&](float v) {
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+  };
+  // ---- logits, in their order
+  float l[32];
+  if (t < p.T) {
+    const size_t at = (size_t)t * (32 * W) + 32 * sub;
+    if (p.bf16) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.logits) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 a = __ldg(src + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l[8 * i + j] = j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+      }
+    } else {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.logits) + at);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 a = __ldg(src + i);
+        l[4 * i] = a.x, l[4 * i + 1] = a.y, l[4 * i + 2] = a.z, l[4 * i + 3] = a.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) l[r] = route_off();
+  }
+  // ---- softmax
+  float mx = 0.f, z = 1.f;
+  bool flag = false;   // this does not decide the token's row
+  if (!p.sigmoid && (scored || sums || !p.renormalize)) {
+    mx = route_off();
+#pragma unroll
+    for (int r = 0; r < 32; ++r) mx = fmaxf(mx, l[r]);
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    flag = mx == -route_off();
+    z = 0.f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) z += route_exp(route_clean(l[r]) - mx);
+    z = sub_sum(z);
+  }
+  const float inv_z = route_inverse(z);
+  auto score = [&](float v) {
+    return p.sigmoid ? route_inverse(1.f + route_exp(-v)) : route_exp(v - mx) * inv_z;
+  };
+  // ---- keys
+  int key[32];
+  constexpr float kUnit = 0x1p29f;   // of a score plus bias, below 4
+  if constexpr (EXACT) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      const int b = __float_as_int(l[r] + 0.f);   // (-0 as 0)
+      key[r] = l[r] > route_off() ? (b ^ ((b >> 31) & 0x7fff0000)) | (1023 - 32 * sub - r) : kRouteOff;
+    }
+  } else {
+    float v[32];
+#pragma unroll
+    for (int r = 0; r < 32; ++r) v[r] = l[r];
+    if (scored) {
+      if (p.sigmoid) {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) v[r] = route_inverse(1.f + route_exp(-v[r]));
+      } else {
+#pragma unroll
+        for (int r = 0; r < 32; ++r) v[r] = route_exp(v[r] - mx) * inv_z;
+      }
+      if (p.bias) {
+        const float4* src = reinterpret_cast<const float4*>(p.bias + 32 * sub);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 b = __ldg(src + i);
+          v[4 * i] += b.x, v[4 * i + 1] += b.y, v[4 * i + 2] += b.z, v[4 * i + 3] += b.w;
+        }
+      }
+    }
+    const float unit = scored ? kUnit : 0x1p25f;
+#pragma unroll
+    for (int r = 0; r < 32; ++r)   // (cut off above kRouteOff's neighbours)
+      key[r] = l[r] > route_off() && v[r] > route_off()
+                   ? (to_fixed(fmaxf(v[r] * unit, -0x1.fffffep30f)) & ~31) | (31 - r)
+                   : kRouteOff;
+  }
+  int ninth = kRouteOff;
+  key_sort<32, 0, 8>(key);
+  key_sort<32, 8, 8>(key);
+  key_sort<32, 16, 8>(key);
+  key_sort<32, 24, 8>(key);
+  key_top8<0, 8>(key, ninth);
+  key_top8<16, 24>(key, ninth);
+  key_top8<0, 16>(key, ninth);
+  // units by which keys of values that FP32 tells apart differ: the scores' errors (as
+  // in route_row), the sum's rounding below 4, place bits
+  const float tol = !(scored || sums) ? 0.f : p.sigmoid ? 0x1p-20f : 0x1p-18f * inv_z;
+  const uint32_t gap = scored ? (uint32_t)(tol * kUnit) + 256u + 64u : 31u;
+  // ---- groups
+  bool keep = true;
+  if (p.groups > 1) {
+    int h1 = key[0], h2 = key[1];
+    for (int o = 1; o < 1 << p.packed_shift; o <<= 1) {
+      const int a1 = __shfl_xor_sync(kFull, h1, o), a2 = __shfl_xor_sync(kFull, h2, o);
+      h2 = max(min(h1, a1), max(h2, a2));
+      h1 = max(h1, a1);
+    }
+    int mine = h1;
+    uint32_t apart = gap;
+    if (sums) {
+      if constexpr (EXACT) {   // scores in units of 2^-28
+        auto part = [&](int k) {
+          const int b = k & 0xffff0000;
+          const float s = score(__int_as_float(b ^ ((b >> 31) & 0x7fff0000)));
+          return k == kRouteOff ? 0 : to_fixed(s * (0.5f * kUnit));
+        };
+        if (h1 != kRouteOff) mine = part(h1) + part(h2);
+        apart = (uint32_t)(tol * kUnit) + 8u;
+      } else {
+        // halves, so that two below 4 add up; what was cut off at 4 decides nothing
+        if (h2 != kRouteOff) mine = (h1 >> 1) + (h2 >> 1);
+        else if (h1 != kRouteOff) mine = h1 >> 1;
+        flag |= h1 >= INT32_MAX - 64 || (h2 != kRouteOff && h2 < -INT32_MAX + 256);
+      }
+    }
+    const int g = sub >> p.packed_shift;
+    int rank = 0;
+    unsigned near = 0u;   // groups too close to this one, in bits as lanes are
+    for (int j = 0; j < p.groups; ++j) {
+      const int other = __shfl_sync(kFull, mine, base | (j << p.packed_shift));
+      rank += other > mine || (other == mine && j < g);
+      const uint32_t d = (uint32_t)max(other, mine) - (uint32_t)min(other, mine);
+      near |= (unsigned)(d <= apart) << (j << p.packed_shift);
+    }
+    keep = rank < p.top_groups;
+    const unsigned kept = __ballot_sync(kFull, keep) >> base;
+    // (two groups with nothing left are not told apart, and need not be)
+    if (sums || !EXACT) flag |= mine != kRouteOff && (near & (keep ? ~kept : kept)) != 0u;
+    if (!keep) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) key[i] = kRouteOff;
+      ninth = kRouteOff;
+    }
+  }
+  // ---- experts: slot j is the lane's with sub = j mod W
+  constexpr int kSlots = W >= 8 ? 1 : 8 / W;
+  int got[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) got[i] = -1;
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < kRouteListed; ++j) {
+    if (EXACT ? j >= p.k : j > p.k) break;
+    const int top = sub_max(key[0]);
+    const bool some = top != kRouteOff, win = some && key[0] == top;
+    int id;
+    if constexpr (EXACT) {
+      id = 1023 - (top & 1023);
+    } else {
+      const unsigned who = (__ballot_sync(kFull, win) >> base) & (unsigned)((1ull << W) - 1);
+      id = 32 * (__ffs(who) - 1) + 31 - (top & 31);
+      flag |= some && ((j > 0 && (uint32_t)before - (uint32_t)top <= gap) ||
+                       (j < p.k && (who & (who - 1u)) != 0u));
+      before = top;
+    }
+    if (j < p.k && sub == (j & (W - 1)) && some) got[j / W < kSlots ? j / W : 0] = id;
+    if (win) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i) key[i] = key[i + 1];
+      key[7] = ninth;
+      ninth = kRouteOff;
+    }
+  }
+  // ---- the chosen experts' weights
+  const bool mine = t < p.T;
+  float lm[kSlots], v[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    lm[i] = mine && got[i] >= 0 ? route_logit(p, (size_t)t * (32 * W) + got[i]) : route_off();
+  float top = p.sigmoid ? 0.f : mx;
+  if (p.renormalize) {
+    const bool infinite = mx == -route_off();   // (as in route_row)
+    float best = route_off();
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) best = fmaxf(best, lm[i]);
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
+    if (!infinite) top = best;
+  }
+  float total = 0.f;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    v[i] = got[i] >= 0 ? route_weight(p.sigmoid, lm[i], top) : 0.f;
+    total += v[i];
+  }
+  if (p.renormalize)
+    total = sub_sum(total);
+  else
+    total = p.sigmoid ? 1.f : z;
+  const unsigned flags = __ballot_sync(kFull, flag) >> base;
+  const bool again = mine && (flags & (unsigned)((1ull << W) - 1)) != 0u;
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) {
+    const int j = sub + W * i;
+    if (mine && !again && j < p.k) {
+      p.ids[(size_t)t * p.k + j] = got[i];
+      p.w[(size_t)t * p.k + j] = (total > 0.f ? v[i] / total : 0.f) * p.scale;
+    }
+  }
+  unsigned todo = __ballot_sync(kFull, again && sub == 0);
+  while (__builtin_expect(todo != 0u, 0)) {
+    route_row<W, EXACT>(p, first + (__ffs(todo) - 1) / W,
+                        reinterpret_cast<uint8_t*>(route_smem) + warp * p.smem);
+    __syncwarp();
+    todo &= todo - 1u;
   }
 }
 

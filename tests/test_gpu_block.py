@@ -84,6 +84,37 @@ def test_route(dev, T, E, k, groups, top, group_score, score, bias):  # noqa: F8
                     group_score=group_score, renormalize=E % 2 == 0, scale=2.5)
 
 
+PACKED = [
+    # E, k, groups, top: several tokens a warp (from 4096 on)
+    (64, 6, 1, 1), (64, 8, 2, 1), (128, 8, 1, 1), (128, 5, 4, 2), (128, 8, 2, 1), (256, 8, 1, 1),
+    (256, 8, 8, 4), (256, 1, 4, 3), (64, 2, 2, 2)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,k,groups,top", PACKED)
+def test_route_many_tokens(dev, E, k, groups, top, score):  # noqa: F811
+    # ordinary rows, ties, masked experts, far and infinite logits, NaN, near ties; an
+    # odd number of tokens, the last ones padding
+    T = 4103
+    r = rng(14, E)
+    z = logits_of(T, E, torch.float32, 15, masked=3, padded=9).numpy()
+    z[:400] = r.integers(0, 3, (400, E))
+    base = np.float32(1 + 3 * r.random((400, 1)))
+    z[400:800] = base + r.integers(-4, 5, (400, E)) * np.spacing(base)
+    z[800:900] *= 40
+    z[900:950] = np.where(r.random((50, E)) < 0.9, -INF, z[900:950])
+    z[950, :], z[951, 5], z[952, :], z[953, 7:9], z[954, 3] = np.nan, np.nan, INF, INF, INF
+    z[955:960] = 0.0
+    z[960:970] = -70 - r.random((10, E))
+    z[970, ::2] = -0.0
+    z[970, 1::2] = 0.0
+    for dtype in (torch.float32, torch.bfloat16):
+        for bias in (None, np.round(r.standard_normal(E) * 100) / 1000, 3 * r.standard_normal(E)):
+            for group_score in ("max", "top2") if groups > 1 else ("max",):
+                check_route(dev, torch.from_numpy(z).to(dtype), k, bias, score=score, groups=groups,
+                            top_groups=top, group_score=group_score, renormalize=k != 5)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("group_score", ["max", "top2"])
 def test_route_masked_and_padded_rows(dev, score, group_score):  # noqa: F811
