@@ -151,8 +151,8 @@ moe_status_t moe_dense_run(moe_dense_t handle, int32_t R, const uint16_t* x,
  * value is MOE_ERR_DEVICE_FAULT when a bit was set. */
 moe_status_t moe_dense_get_error(moe_dense_t handle, void* stream, uint32_t* device_flags);
 
-/* Test support: how a run of R rows is cut on a GPU of num_sms SMs, computed on
- * the host (no device needed). */
+/* Test support: how a run of R rows, with FP32 outputs or bf16 ones, is cut on a GPU
+ * of num_sms SMs, computed on the host (no device needed). */
 typedef struct {
   int32_t split;  /* 1: moe_dense_split, 0: moe_dense_tiles */
   int32_t nt;     /* rows of x a tile */
@@ -161,8 +161,8 @@ typedef struct {
   int32_t smem;   /* dynamic shared memory of a CTA, bytes */
   int32_t ctas;   /* of the launch */
 } moe_dense_plan_t;
-moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t num_sms,
-                            moe_dense_plan_t* out);
+moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t out_float,
+                            int32_t num_sms, moe_dense_plan_t* out);
 
 /* Test support: in the next run that launches something, the MMAs wait for an
  * arrival that nothing makes, with a limit of some milliseconds instead of a

@@ -130,7 +130,7 @@ BLOCK_SIGNATURES = {
     "moe_dense_destroy": (_st, [_p]),
     "moe_dense_run": (_st, [_p, _i32, _p, _p, _p, _i32, _p]),
     "moe_dense_get_error": (_st, [_p, _p, ctypes.POINTER(ctypes.c_uint32)]),
-    "moe_dense_plan": (_st, [ctypes.POINTER(MoEDenseConfig), _i32, _i32,
+    "moe_dense_plan": (_st, [ctypes.POINTER(MoEDenseConfig), _i32, _i32, _i32,
                              ctypes.POINTER(MoEDensePlan)]),
     "moe_dense_arm_timeout": (_st, [_p]),
 }

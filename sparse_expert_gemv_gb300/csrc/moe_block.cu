@@ -178,7 +178,7 @@ size_t split_smem(const DensePlan& p) {
 //           the parts' exchange; clusters that find no room wait for a round more
 //   tiles   rounds of tiles over the pairs, whose stages take their MMAs or their
 //           bytes' way into an SM
-DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
+DensePlan plan_dense(const moe_dense_config_t& c, int R, bool out_float, int num_sms) {
   const bool silu = is_silu(c);
   const int M = silu ? c.N / 2 : c.N;
   const int nk = (c.K + moe::kDenseK - 1) / moe::kDenseK;
@@ -188,7 +188,7 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
     if (!best.nt || p.us < best.us) best = p;
   };
   const int pairs = std::max(1, num_sms / 2);
-  for (int nt = moe::kDenseCols; nt >= 32; nt -= 32) {
+  for (int nt = out_float ? moe::kDenseFloatCols : moe::kDenseCols; nt >= 32; nt -= 32) {
     if (nt - 32 >= R) continue;
     const double tiles = std::ceil(M / (silu ? 128.0 : 256.0)) * std::ceil((double)R / nt);
     const double bytes = moe::DenseSmem::stage(nt);   // a stage's, of one CTA
@@ -201,7 +201,9 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
   for (int nt = moe::kSplitMaxCols; nt >= 16; nt -= 16) {
     if (nt - 16 >= R) continue;
     const int n = std::min(nt, R), bytes = moe::split_stage_bytes(nt);
-    for (int S = 1; S <= 8 && S <= nk; S *= 2)
+    for (int S = 1; S <= 8 && S <= nk; S *= 2) {
+      // FP32 outputs: not too long sums in the tensor cores
+      if (out_float && S < 8 && (nk + S - 1) / S > moe::kDensePart) continue;
       for (const int room : {kSplitFull, kSplitHalf}) {
         const int stages = split_stages(nt, S, room);
         if (stages < 2) continue;
@@ -217,6 +219,7 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, int num_sms) {
         const double per = 1.71 + stream + n * (0.01 / S + (S > 1 ? 0.0129 : 0)) + 0.118 * (S - 1);
         take({true, nt, S, stages, kStart + std::max(std::ceil(ctas / most) * per, hbm + 1.71)});
       }
+    }
   }
   return best;
 }
@@ -232,7 +235,10 @@ static_assert(kDenseSmem <= 232448, "shared memory of a CTA");
 
 template <bool SILU>
 bool set_dense_attributes() {
-  return cudaFuncSetAttribute(moe::moe_dense_tiles<SILU>,
+  return cudaFuncSetAttribute(moe::moe_dense_tiles<SILU, false>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)kDenseSmem) == cudaSuccess &&
+         cudaFuncSetAttribute(moe::moe_dense_tiles<SILU, true>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)kDenseSmem) == cudaSuccess &&
          cudaFuncSetAttribute(moe::moe_dense_split<SILU>,
@@ -405,7 +411,7 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   if (device != m->device) return MOE_ERR_INVALID_ARG;
   const moe_dense_config_t& c = m->cfg;
   const bool silu = is_silu(c);
-  const DensePlan plan = plan_dense(c, R, m->num_sms);
+  const DensePlan plan = plan_dense(c, R, out_float != 0, m->num_sms);
   moe::DenseParams p;
   p.M = silu ? c.N / 2 : c.N;
   p.nt = plan.nt;
@@ -432,19 +438,21 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
     st = launch(silu ? moe::moe_dense_split<true> : moe::moe_dense_split<false>, ctas,
                 moe::kSplitThreads, split_smem(plan), stream, plan.S, p, log2_of(plan.S));
   else
-    st = launch(silu ? moe::moe_dense_tiles<true> : moe::moe_dense_tiles<false>, ctas,
+    st = launch(silu ? (out_float ? moe::moe_dense_tiles<true, true> : moe::moe_dense_tiles<true, false>)
+                     : (out_float ? moe::moe_dense_tiles<false, true> : moe::moe_dense_tiles<false, false>),
+                ctas,
                 moe::kDenseThreads, kDenseSmem, stream, 2, p);
   if (st == MOE_OK) m->mark_done(static_cast<cudaStream_t>(stream));
   return st;
 }
 
-moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t num_sms,
-                            moe_dense_plan_t* out) {
+moe_status_t moe_dense_plan(const moe_dense_config_t* cfg, int32_t R, int32_t out_float,
+                            int32_t num_sms, moe_dense_plan_t* out) {
   if (!cfg || !out || R < 1 || num_sms < 1) return MOE_ERR_INVALID_ARG;
   const moe_status_t st = check_dense(*cfg);
   if (st != MOE_OK) return st;
   const bool silu = is_silu(*cfg);
-  const DensePlan p = plan_dense(*cfg, R, num_sms);
+  const DensePlan p = plan_dense(*cfg, R, out_float != 0, num_sms);
   int mt, tt, ctas;
   if (!dense_grid(*cfg, p, R, num_sms, mt, tt, ctas)) return MOE_ERR_UNSUPPORTED_SHAPE;
   out->split = p.split;

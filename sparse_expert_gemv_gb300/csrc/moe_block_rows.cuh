@@ -961,7 +961,7 @@ __device__ __forceinline__ float cta_sum(float v, float* part) {
 }
 
 __device__ __forceinline__ float gate_value(const NormPairParams& p, float g) {
-  if (p.gate_sigmoid) return __fdividef(1.f, 1.f + expf(-g));
+  if (p.gate_sigmoid) return 1.f / (1.f + expf(-g));
   if (p.gate_tanh) return tanhf(g);
   return g;
 }

@@ -39,7 +39,7 @@ struct DenseParams {
   void* out;                 // [R, M]
   uint32_t* err;
   int R, M, nk;              // nk: stages K takes
-  int act, out_float;
+  int act, out_float;        // (out_float: split)
   int vec;                   // rows of out and residual take 16-byte accesses
   int nt;                    // rows of x a tile
   int mt, tt;                // tiles along M and R
@@ -197,8 +197,16 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const
 // Two accumulators in tensor memory let the epilogue of a tile overlap the next
 // tile's MMAs. With SILU a tile is 128 neurons' gate and up rows, 16 and 16 in turn,
 // so that each epilogue warp has a neuron's gate and up in one thread.
+//
+// The tensor cores cut a sum off at each step of 16 K instead of rounding it, which
+// adds up along K (relative error of 8191 x 7168 x 256 by its 2-norm: 7.9e-6, of FP32
+// FMAs 0.9e-6). bf16 outputs do not show it. Where the outputs are FP32 (FLOAT), the
+// sums of kDensePart stages in turn are added up in registers: 1.0e-6 in the same
+// time, with parts of eight stages 0.5e-6.
 // ---------------------------------------------------------------------------
 constexpr int kDenseThreads = 384;
+constexpr int kDensePart = 16;                 // stages
+constexpr int kDenseFloatCols = 128;           // rows of x a tile with FLOAT, at most
 constexpr int kDenseChunk = 32 * 256;   // epilogue staging: 32 rows of 128 bf16
 
 constexpr int kDenseStages = 12;        // of the ring, at most
@@ -207,7 +215,7 @@ constexpr int kDenseSmemMax = 232448 - 1024;
 // The ring takes what the epilogue's chunks leave: a slot's way from the MMA's
 // release through a copy back to the MMA takes more than a microsecond, and narrow
 // tiles' stages are small (router logits of 8191 x 7168 x 256 in tiles of 128 rows:
-// 30.4 us with six stages, 27.5 with eight).
+// 30.4 us with six stages, 27.5 with eight, 28.9 with the sums of FP32 outputs).
 struct DenseSmem {
   static constexpr int out = 0;                     // [2 groups][2] chunks
   static constexpr int bars = out + 4 * kDenseChunk;
@@ -232,7 +240,7 @@ __device__ __forceinline__ void dense_tile(const DenseParams& p, int i, int& m, 
   t = band * kDenseBand + j - m * g;
 }
 
-template <bool SILU>
+template <bool SILU, bool FLOAT>
 __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     const __grid_constant__ DenseParams p) {
   extern __shared__ uint8_t smem_dyn[];
@@ -334,15 +342,16 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     if (rank == 0) {
       RingPos rg(stages);
       const uint32_t idesc = tc::f16_idesc(2 * kDenseRows, p.nt);
-      int lt = 0;
+      int lt = 0;   // accumulators filled
       bool ok = true;
-      for (int i = first; ok && i < tiles; i += step, ++lt) {
+      for (int i = first, k0 = 0; ok && i < tiles; ++lt) {
         const int buf = lt & 1;
         if (lt >= 2) ok = dense_wait<true>(&d_empty[buf], ((lt >> 1) - 1) & 1, p, dead);
         if (!ok) break;
         tc::fence_after();
         const uint32_t d = buf * 256;
-        for (int kb = 0; kb < p.nk; ++kb) {
+        const int k1 = FLOAT ? min(k0 + kDensePart, p.nk) : p.nk;
+        for (int kb = k0; kb < k1; ++kb) {
           const int s = rg.slot;
           ok = dense_wait<true>(&full[s], rg.phase, p, dead);
           if (!ok) break;
@@ -350,15 +359,120 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kDenseABytes);
 #pragma unroll
           for (int q = 0; q < kDenseK / 16; ++q)   // 32 bytes further in the swizzled rows
-            tc::mma_f16<true>(d, ad + 2 * q, bd + 2 * q, idesc, kb + q > 0 ? 1u : 0u);
+            tc::mma_f16<true>(d, ad + 2 * q, bd + 2 * q, idesc, kb > k0 || q > 0 ? 1u : 0u);
           tc::commit2(&empty[s]);
           rg.next();
         }
         if (ok) tc::commit2(&d_full[buf]);
+        k0 = k1;
+        if (k0 == p.nk) k0 = 0, i += step;
       }
       tc::commit2(drain);
     }
-  } else if (warp >= 4) {
+  } else if (FLOAT && warp >= 4) {
+    // ------------------------------------------------- epilogue, FP32 outputs
+    const int q = warp & 3, et = threadIdx.x & 127, grp = (warp >> 2) - 1;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
+    // a chunk of 32 rows of x by kOut outputs, turned in shared memory: column c of
+    // row r lies at c ^ 8 ((r / 2) mod 4), so that the eight columns and four rows of
+    // a warp's store lie in different banks
+    float* turn = reinterpret_cast<float*>(smem + L::out + grp * 2 * kDenseChunk);
+    constexpr int kPieces = kOut / 4, kRows = 128 / kPieces;
+    const int pc = et & (kPieces - 1), pr = et / kPieces;
+    int lt = 0;
+    pdl_wait();
+    for (int i = first; i < tiles; i += step) {
+      int m, t;
+      dense_tile(p, i, m, t);
+      const int n0 = (2 * m + rank) * kOut, r0 = t * p.nt;
+      const int n = min(p.nt, p.R - r0);
+      // the tile's chunks 32 grp and 64 further; registers as in the epilogue below
+      float sum[2][2][16];
+#pragma unroll
+      for (int x = 0; x < 64; ++x) sum[x >> 5][(x >> 4) & 1][x & 15] = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int k0 = 0; k0 < p.nk; k0 += kDensePart, ++lt) {
+        const int buf = lt & 1;
+        ok = dense_wait<true>(&d_full[buf], (lt >> 1) & 1, p, dead);
+        if (!ok) break;
+        tc::fence_after();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int c0 = 32 * grp + 64 * c;
+          if (c0 >= n) continue;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t raw[16];
+            tc::ld_16x32(lanes + ((uint32_t)(16 * h) << 16) + buf * 256 + c0, raw);
+            tc::wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) sum[c][h][x] += __uint_as_float(raw[x]);
+          }
+        }
+        tc::fence_before();
+        __syncwarp();
+        tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
+      }
+      // (a group's warps go on or leave together)
+      if (!named_all(1 + grp, 128, ok)) break;
+      float bias[4] = {};
+      if (p.bias) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = SILU ? n0 + 16 * q + 8 * (k & 1) + (lane >> 2)
+                               : n0 + 32 * q + 8 * k + (lane >> 2);
+          if (row < p.M) bias[k] = bf16_at(p.bias + row + (SILU && k > 1 ? p.M : 0));
+        }
+      }
+      float* out = static_cast<float*>(p.out);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int c0 = 32 * grp + 64 * c;
+        if (c0 >= n) continue;
+#pragma unroll
+        for (int h = 0; h < (SILU ? 1 : 2); ++h) {
+          float v[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            v[x] = sum[c][h][x] + bias[2 * h + ((x >> 1) & 1)];
+            if constexpr (SILU) v[x] = dense_silu(v[x]) * (sum[c][1][x] + bias[2 + ((x >> 1) & 1)]);
+          }
+          if constexpr (!SILU) dense_act(p.act, v);
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int row = 8 * (x >> 2) + 2 * (lane & 3) + (x & 1);
+            const int col = kOut / 4 * q + 16 * h + 8 * ((x >> 1) & 1) + (lane >> 2);
+            turn[row * kOut + (col ^ ((lane & 3) << 3))] = v[x];
+          }
+        }
+        named_sync(1 + grp, 128);
+        const int col = n0 + 4 * pc;
+#pragma unroll
+        for (int k = 0; k < 32 / kRows; ++k) {
+          const int row = pr + kRows * k;
+          if (c0 + row >= n || col >= p.M) continue;
+          float4 w = *reinterpret_cast<const float4*>(
+              turn + row * kOut + ((4 * pc) ^ (((row >> 1) & 3) << 3)));
+          const size_t at = (size_t)(r0 + c0 + row) * p.M + col;
+          if (p.vec) {
+            if (p.residual) {
+              const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
+              w.x += bf16_lo(r.x), w.y += bf16_hi(r.x), w.z += bf16_lo(r.y), w.w += bf16_hi(r.y);
+            }
+            *reinterpret_cast<float4*>(out + at) = w;
+          } else {
+            const float e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (col + j < p.M) out[at + j] = e[j] + (p.residual ? bf16_at(p.residual + at + j) : 0.f);
+          }
+        }
+        named_sync(1 + grp, 128);   // the chunk's place is free again
+      }
+    }
+  } else if (!FLOAT && warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int q = warp & 3, et = threadIdx.x & 127;
     const int grp = (warp >> 2) - 1;
@@ -469,36 +583,26 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
             }
           }
         }
-        if (p.out_float) {
-          float* out = static_cast<float*>(p.out);
 #pragma unroll
-          for (int x = 0; x < kVals; ++x) {
-            const int row = c0 + 8 * ((x >> 2) & 3) + 2 * (lane & 3) + (x & 1);
-            const int col = n0 + kOut / 4 * q + 16 * (x >> 4) + 8 * ((x >> 1) & 1) + (lane >> 2);
-            if (row < n && col < p.M) out[(size_t)(r0 + row) * p.M + col] = v[x];
-          }
-        } else {
+        for (int b = 0; b < kSets; ++b) {
+          auto pack = [&](int k) { return RowVec<8>::pack(v[at(b, k)], v[at(b, k) + 1]); };
+          tc::stm4_trans(mats + b * kSetBytes, pack(0), pack(1), pack(2), pack(3));
+        }
+        named_sync(bar, 128);
+        uint16_t* out = static_cast<uint16_t*>(p.out);
 #pragma unroll
-          for (int b = 0; b < kSets; ++b) {
-            auto pack = [&](int k) { return RowVec<8>::pack(v[at(b, k)], v[at(b, k) + 1]); };
-            tc::stm4_trans(mats + b * kSetBytes, pack(0), pack(1), pack(2), pack(3));
-          }
-          named_sync(bar, 128);
-          uint16_t* out = static_cast<uint16_t*>(p.out);
+        for (int k = 0; k < kMoves; ++k) {
+          const int row = c0 + pr + kRows * k;
+          if (row >= n || pn >= p.M) continue;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + moved + k * kRows * kOut * 2);
+          uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
+          if (p.vec) {
+            *reinterpret_cast<uint4*>(dst) = w;
+          } else {
+            const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int k = 0; k < kMoves; ++k) {
-            const int row = c0 + pr + kRows * k;
-            if (row >= n || pn >= p.M) continue;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + moved + k * kRows * kOut * 2);
-            uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
-            if (p.vec) {
-              *reinterpret_cast<uint4*>(dst) = w;
-            } else {
-              const uint32_t e[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (pn + j < p.M) dst[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
-            }
+            for (int j = 0; j < 8; ++j)
+              if (pn + j < p.M) dst[j] = (uint16_t)(e[j >> 1] >> (16 * (j & 1)));
           }
         }
       }

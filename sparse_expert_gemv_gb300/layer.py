@@ -12,6 +12,7 @@ import torch
 from ._lib import (MOE_FLAG_MXFP4, MOE_PATH_AUTO, MOE_PATH_TENSOR, MOE_PATH_WARP, MoEConfig, check,
                    lib)
 from ._tensors import _need, _on, _ptr, _stream
+from .block import route_experts
 from .prompt import GroupedProduct, combine, group_by_expert
 
 
@@ -106,7 +107,16 @@ class MoEDecode:
         return out
 
     # -- calls ----------------------------------------------------------------
-    def route(self, logits, ids=None, w=None, stream=None):
+    def route(self, logits, ids=None, w=None, stream=None, **options):
+        """(ids int32 [T, k], w float32 [T, k]) of router logits float32 [T, E]:
+        the k most probable experts by a softmax and their probabilities,
+        renormalised. With `options`, route_experts' (score, bias, groups,
+        top_groups, group_score, renormalize, scale), the choice is that
+        operator's, which takes bf16 logits too."""
+        if options:
+            if logits.shape[-1] != self.E:
+                raise ValueError(f"logits: expected {self.E} experts, got {logits.shape[-1]}")
+            return route_experts(logits, self.k, ids=ids, w=w, stream=stream, **options)
         T = logits.shape[0]
         _need(logits, torch.float32, (T, self.E), "logits")
         ids = self._dev((T, self.k), torch.int32, ids, "topk_ids", stream)

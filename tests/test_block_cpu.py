@@ -82,10 +82,10 @@ def test_dense_create_refusals(lib, kw, status):
     assert h.value is None
 
 
-def plan(lib, R, K, N, act=0, sms=152):
+def plan(lib, R, K, N, act=0, sms=152, out_float=0):
     from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan
     p = MoEDensePlan()
-    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(N, K, act)), R, sms, ctypes.byref(p)) == 0
+    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(N, K, act)), R, out_float, sms, ctypes.byref(p)) == 0
     return p
 
 
@@ -96,13 +96,16 @@ def test_dense_plans_keep_the_kernels_limits(lib):
         R, K, N = (int(np.exp(r.uniform(0, np.log(hi)))) for hi in (20000, 1000, 10000))
         K, act, sms = 8 * K, int(r.choice([0, 5])), int(r.choice([1, 2, 76, 148, 152]))
         N += N % 2
-        p, two = plan(lib, R, K, N, act, sms), 2 if act == 5 else 1
+        flt, two = int(r.choice([0, 1])), 2 if act == 5 else 1
+        p = plan(lib, R, K, N, act, sms, flt)
         M, nk = N // two, -(-K // 64)
         seen.add((p.split, p.parts))
         assert p.stages >= 2
         if p.split:
             assert p.nt % 16 == 0 and 16 <= p.nt <= 128 and p.stages <= 16
             assert p.parts in (1, 2, 4, 8) and p.parts <= nk
+            # FP32 sums of up to 1024 K (or an eighth) in the tensor cores
+            assert not flt or p.parts == 8 or -(-nk // p.parts) <= 16
             # barriers, ring, sums; at most two CTAs an SM, whose tensor memory it has
             stage, sums = 16384 + p.nt * 128, p.nt * 512
             assert sums <= p.stages * stage
@@ -110,7 +113,7 @@ def test_dense_plans_keep_the_kernels_limits(lib):
             assert 3 * (p.smem + 1024) > 228 * 1024 and 2 * p.nt <= 512
             assert p.ctas == -(-M // (64 if act else 128)) * -(-R // p.nt) * p.parts
         else:
-            assert p.nt % 32 == 0 and 32 <= p.nt <= 256 and p.smem <= 232448 and p.stages <= 12
+            assert p.nt % 32 == 0 and 32 <= p.nt <= (128 if flt else 256) and p.smem <= 232448 and p.stages <= 12
             assert 1024 + 4 * 8192 + 1024 + p.stages * (16384 + p.nt * 64) <= p.smem
             assert p.ctas == 2 * min(max(1, sms // 2), -(-M // (256 // two)) * -(-R // p.nt))
     assert seen >= {(0, 1), (1, 1), (1, 2), (1, 4), (1, 8)}
@@ -119,13 +122,13 @@ def test_dense_plans_keep_the_kernels_limits(lib):
 def test_dense_plan_refusals(lib):
     from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan
     p, ok = MoEDensePlan(), MoEDenseConfig(64, 64, 0)
-    assert lib.moe_dense_plan(None, 1, 152, ctypes.byref(p)) == 1
-    assert lib.moe_dense_plan(ctypes.byref(ok), 0, 152, ctypes.byref(p)) == 1
-    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 0, ctypes.byref(p)) == 1
-    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 152, None) == 1
-    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(64, 60, 0)), 1, 152, ctypes.byref(p)) == 2
+    assert lib.moe_dense_plan(None, 1, 0, 152, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 0, 0, 152, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 0, 0, ctypes.byref(p)) == 1
+    assert lib.moe_dense_plan(ctypes.byref(ok), 1, 0, 152, None) == 1
+    assert lib.moe_dense_plan(ctypes.byref(MoEDenseConfig(64, 60, 0)), 1, 0, 152, ctypes.byref(p)) == 2
     huge = MoEDenseConfig(2 ** 31 - 2, 8, 0)
-    assert lib.moe_dense_plan(ctypes.byref(huge), 2 ** 31 - 1, 152, ctypes.byref(p)) == 2
+    assert lib.moe_dense_plan(ctypes.byref(huge), 2 ** 31 - 1, 0, 152, ctypes.byref(p)) == 2
 
 
 def test_dense_null_handles(lib):
