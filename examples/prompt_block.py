@@ -2,10 +2,13 @@
 
 One pass: residual addition and norm (bf16 rows for the router, MXFP8 rows for
 the experts), router, routed experts on the tensor cores, weighted sum back
-onto the residual stream. Weights and inputs are synthetic.
+onto the residual stream. Weights and inputs are synthetic. With --shared the
+block has a norm behind the attention too, a router in FP32 with sigmoid scores,
+a balancing bias and groups of experts, and a shared expert whose output the
+routed ones are added to.
 
     python examples/prompt_block.py [--tokens 4096] [--format mxfp8|mxfp4]
-        [--experts 128] [--topk 8] [--hidden 2048] [--intermediate 768]
+        [--experts 128] [--topk 8] [--hidden 2048] [--intermediate 768] [--shared]
 """
 from __future__ import annotations
 
@@ -17,7 +20,8 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from sparse_expert_gemv_gb300 import MoEDecode, add_rms_norm  # noqa: E402
+from sparse_expert_gemv_gb300 import (DenseProduct, MoEDecode, add_rms_norm,  # noqa: E402
+                                      norm_add_norm)
 
 
 class PromptBlock:
@@ -35,6 +39,27 @@ class PromptBlock:
         ids, w = self.layer.route(logits)
         return self.layer.prompt(n.codes, n.scales, ids, w,
                                  residual=x if n.sum is None else n.sum)
+
+
+class SharedBlock:
+    """The same with a shared expert, a norm behind the block's input and grouped,
+    biased routing."""
+
+    def __init__(self, layer: MoEDecode, post_weight: torch.Tensor, norm_weight: torch.Tensor,
+                 router: torch.Tensor, bias: torch.Tensor, shared_gate_up: torch.Tensor,
+                 shared_down: torch.Tensor, groups: int = 8, top_groups: int = 4, scale: float = 2.5):
+        self.layer, self.post_weight, self.norm_weight = layer, post_weight, norm_weight
+        self.router = DenseProduct(router)
+        self.gate_up = DenseProduct(shared_gate_up, activation="silu_mul")
+        self.down = DenseProduct(shared_down)
+        self.routing = dict(score="sigmoid", bias=bias, groups=groups, top_groups=top_groups,
+                            group_score="top2", scale=scale)
+
+    def __call__(self, x: torch.Tensor, residual: torch.Tensor) -> torch.Tensor:
+        n = norm_add_norm(x, residual, self.post_weight, self.norm_weight, mxfp8=True)
+        ids, w = self.layer.route(self.router(n.y, float32=True), **self.routing)
+        shared = self.down(self.gate_up(n.y), n.sum)
+        return self.layer.prompt(n.codes, n.scales, ids, w, residual=shared)
 
 
 def random_layer(E, k, H, I, fmt, max_T, seed=0, device="cuda") -> MoEDecode:
@@ -62,12 +87,23 @@ def main(argv=None) -> float:
     p.add_argument("--hidden", type=int, default=2048)
     p.add_argument("--intermediate", type=int, default=768)
     p.add_argument("--format", choices=("mxfp8", "mxfp4"), default="mxfp8")
+    p.add_argument("--shared", action="store_true")
     a = p.parse_args(argv)
     T, E, H = a.tokens, a.experts, a.hidden
     g = torch.Generator(device="cuda").manual_seed(1)
     layer = random_layer(E, a.topk, H, a.intermediate, a.format, max_T=T)
-    block = PromptBlock(layer, torch.ones(H, dtype=torch.bfloat16, device="cuda"),
-                        torch.randn(E, H, device="cuda", generator=g).mul_(H ** -0.5).bfloat16())
+    ones = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+
+    def weight(n, k):
+        return torch.randn(n, k, device="cuda", generator=g).mul_(k ** -0.5).bfloat16()
+
+    if a.shared:
+        bias = 0.1 * torch.randn(E, device="cuda", generator=g)
+        block = SharedBlock(layer, ones, ones, weight(E, H), bias, weight(2 * a.intermediate, H),
+                            weight(H, a.intermediate), groups=4 if E % 4 == 0 else 1,
+                            top_groups=2 if E % 4 == 0 else 1)
+    else:
+        block = PromptBlock(layer, ones, weight(E, H))
     x, residual = (torch.randn(T, H, device="cuda", generator=g).bfloat16() for _ in range(2))
     for _ in range(3):
         out = block(x, residual)
@@ -79,7 +115,8 @@ def main(argv=None) -> float:
     torch.cuda.synchronize()
     us = begin.elapsed_time(end) * 1e3 / 20
     assert out.isfinite().all() and layer.get_error() == 0
-    print(f"{T} tokens, E={E} k={a.topk} H={H} I={a.intermediate} {a.format}: {us:.1f} us a block, "
+    shared = " and a shared expert" if a.shared else ""
+    print(f"{T} tokens, E={E} k={a.topk} H={H} I={a.intermediate} {a.format}{shared}: {us:.1f} us a block, "
           f"{T / us:.2f} tokens a us")
     return us
 

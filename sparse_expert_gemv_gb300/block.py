@@ -100,11 +100,13 @@ class DenseProduct:
     """Products of bf16 rows with one weight matrix: act(x @ weight.T + bias) + residual.
 
     weight is bf16 [N, K] with K a multiple of 8, bias bf16 [N] or None; both
-    are borrowed (kept alive by this object) and their device is where the rows
-    of every call have to lie. `activation` is None, "relu", "silu", "gelu",
+    are borrowed (kept alive by this object), are not to be written while it
+    lives (a call reads ahead of earlier work on its stream), and lie where the
+    rows of every call have to. `activation` is None, "relu", "silu", "gelu",
     "gelu_tanh", or "silu_mul": the N = 2I weight rows are then I gate rows and
     I up rows, and the result is the I values SiLU(gate) * up. The handle is
-    made outside graph captures; calls may be captured.
+    made outside graph captures; calls may be captured, and calls on several
+    streams may overlap.
     """
 
     def __init__(self, weight, bias=None, *, activation: str | None = None):

@@ -27,6 +27,10 @@ struct moe_dense : moe::Handle {
 
 namespace {
 
+// Rows of a call and outputs of a product: what rounding up to a tile does not take
+// past 32 bits.
+constexpr int32_t kMaxRows = 0x7fffff00;
+
 using moe::aligned;
 using moe::launch;
 
@@ -249,13 +253,16 @@ bool set_dense_attributes() {
 moe_status_t check_dense(const moe_dense_config_t& c) {
   if (c.N < 1 || c.K < 1 || c.activation < MOE_ACT_NONE || c.activation > MOE_ACT_SILU_MUL)
     return MOE_ERR_INVALID_ARG;
-  return c.K % 8 || (is_silu(c) && c.N % 2) ? MOE_ERR_UNSUPPORTED_SHAPE : MOE_OK;
+  return c.K % 8 || c.K > kMaxRows || c.N > kMaxRows || (is_silu(c) && c.N % 2)
+             ? MOE_ERR_UNSUPPORTED_SHAPE
+             : MOE_OK;
 }
 
 // Tiles along M and R and the CTAs of a launch; false when there are too many.
 bool dense_grid(const moe_dense_config_t& c, const DensePlan& p, int R, int num_sms, int& mt, int& tt,
                 int& ctas) {
   const int64_t M = is_silu(c) ? c.N / 2 : c.N, rows = (p.split ? 128 : 256) / (is_silu(c) ? 2 : 1);
+  if (R > kMaxRows) return false;
   const int64_t m = (M + rows - 1) / rows, t = ((int64_t)R + p.nt - 1) / p.nt;
   if (m * t * p.S > 0x3fffffff) return false;
   mt = (int)m;
@@ -282,7 +289,8 @@ moe_status_t moe_route_experts(const moe_route_config_t* cfg, int32_t T, const v
   if (T < 0 || c.E < 1 || c.k < 1 || c.groups < 1 || c.top_groups < 1 ||
       c.top_groups > c.groups || !std::isfinite(c.scale) || (c.flags & ~known))
     return MOE_ERR_INVALID_ARG;
-  if (c.E > moe::kRouteMaxE || c.k > 32 || c.groups > 32) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (c.E > moe::kRouteMaxE || c.k > 32 || c.groups > 32 || T > kMaxRows)
+    return MOE_ERR_UNSUPPORTED_SHAPE;
   if (c.E % c.groups || c.k > c.top_groups * (c.E / c.groups)) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !w) return MOE_ERR_INVALID_ARG;
@@ -330,7 +338,7 @@ moe_status_t moe_norm_add_norm(int32_t T, int32_t H, const uint16_t* x, const ui
       (flags & ~(shape | func | MOE_NORM_UNIT_OFFSET)) || (flags & shape) == shape ||
       (flags & func) == func || ((flags & (shape | func)) && !gate && T > 0))
     return MOE_ERR_INVALID_ARG;
-  if (H > moe::kNormMaxH || (codes && H % 32)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (H > moe::kNormMaxH || (codes && H % 32) || T > kMaxRows) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MOE_OK;
   if (!x || !residual || !sum || (pre_weight == nullptr) != (!y && !codes) ||
       (codes == nullptr) != (scales == nullptr))

@@ -43,7 +43,8 @@ def test_binding_and_library_cover_the_header(lib):
     (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(flags=0x10), 1), (dict(logits=0), 1),
     (dict(ids=0), 1), (dict(w=0), 1), (dict(E=1028), 2), (dict(E=64, k=33), 2),
     (dict(E=66, groups=33, top=4), 2), (dict(logits=P + 2), 3), (dict(logits=P + 1, flags=1), 3),
-    (dict(bias=P + 2), 3), (dict(ids=P + 2), 3), (dict(w=P + 2), 3), (dict(T=0, logits=0), 0)])
+    (dict(bias=P + 2), 3), (dict(ids=P + 2), 3), (dict(w=P + 2), 3), (dict(T=0, logits=0), 0),
+    (dict(T=2 ** 31 - 1), 2)])
 def test_route_refusals(lib, kw, status):
     from sparse_expert_gemv_gb300._lib import MoERouteConfig
     a = dict(T=2, E=16, k=4, groups=4, top=2, scale=1.0, flags=0, logits=P, bias=P, ids=P, w=P) | kw
@@ -63,7 +64,7 @@ def test_route_without_a_config(lib):
     (dict(flags=0x3), 1), (dict(flags=0xc), 1), (dict(flags=0x20), 1), (dict(flags=0x1, gate=0), 1),
     (dict(flags=0x4, gate=0), 1), (dict(H=16385), 2), (dict(H=40), 2), (dict(x=P + 1), 3),
     (dict(residual=P + 1), 3), (dict(post=P + 1), 3), (dict(pre=P + 1), 3), (dict(gate=P + 1), 3),
-    (dict(sum=P + 1), 3), (dict(y=P + 1), 3), (dict(T=0, x=0), 0)])
+    (dict(sum=P + 1), 3), (dict(y=P + 1), 3), (dict(T=0, x=0), 0), (dict(T=2 ** 31 - 1), 2)])
 def test_norm_refusals(lib, kw, status):
     a = dict(T=2, H=64, x=P, residual=P, post=P, pre=P, gate=P, scale=1.0, rscale=1.0, eps=1e-6,
              flags=0, sum=P, y=P, codes=P, scales=P) | kw
@@ -72,7 +73,8 @@ def test_norm_refusals(lib, kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(N=0), 1), (dict(K=0), 1), (dict(act=-1), 1), (dict(act=6), 1), (dict(w=0), 1),
-    (dict(K=12), 2), (dict(N=7, act=5), 2), (dict(w=P + 8), 3), (dict(b=P + 1), 3)])
+    (dict(K=12), 2), (dict(N=7, act=5), 2), (dict(w=P + 8), 3), (dict(b=P + 1), 3),
+    (dict(N=2 ** 31 - 1), 2), (dict(K=2 ** 31 - 8), 2)])
 def test_dense_create_refusals(lib, kw, status):
     from sparse_expert_gemv_gb300._lib import MoEDenseConfig
     a = dict(N=64, K=64, act=0, w=P, b=P) | kw

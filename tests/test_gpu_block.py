@@ -646,3 +646,120 @@ def test_a_block_replayed_and_on_another_stream(dev):  # noqa: F811
     for u, v in zip(got, want):
         assert torch.equal(u, v)
     assert b.router.get_error() == 0
+
+
+def test_the_layers_router_takes_the_options(dev):  # noqa: F811
+    from sparse_expert_gemv_gb300 import route_experts
+    b = Block(dev, 30)
+    z = logits_of(30, 16, torch.float32, 60).to(dev)
+    plain = b.layer.route(z)
+    want = ref.route_experts(z.double().cpu().numpy(), 4)
+    assert np.array_equal(plain[0].cpu().numpy(), want[0])
+    # the operator without options is the layer's own router
+    same = route_experts(z, 4)
+    assert torch.equal(same[0], plain[0]) and torch.allclose(same[1], plain[1], rtol=1e-6)
+    kw = dict(score="sigmoid", bias=b.bias, groups=4, top_groups=2, group_score="top2", scale=1.5)
+    for got, like in zip(b.layer.route(z.bfloat16(), **kw), route_experts(z.bfloat16(), 4, **kw)):
+        assert torch.equal(got, like)
+    ids = torch.empty(30, 4, dtype=torch.int32, device=dev)
+    assert b.layer.route(z, ids=ids, **kw)[0].data_ptr() == ids.data_ptr()
+    with pytest.raises(ValueError, match="expected 16 experts"):
+        b.layer.route(z[:, :8].contiguous(), **kw)
+
+
+def test_example_with_a_shared_expert(dev, capsys):  # noqa: F811
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "prompt_block.py")
+    spec = importlib.util.spec_from_file_location("prompt_block", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    assert ex.main(["--tokens", "70", "--experts", "16", "--topk", "2", "--hidden", "256",
+                    "--intermediate", "128", "--shared"]) > 0
+    assert "shared expert" in capsys.readouterr().out
+    b = Block(dev, 33)
+    block = ex.SharedBlock(b.layer, b.post, b.pre, b.wr, b.bias, b.wgu, b.wd, groups=4, top_groups=2,
+                           scale=1.5)
+    assert torch.equal(block(b.x, b.res), b()[-1])
+
+
+# ---------------------------------------------------------------------------
+# one handle from several places, long tensors
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("R,K,N,act", [(5, 2048, 256, None), (40, 1024, 2048, "silu_mul"),
+                                       (700, 512, 1024, "gelu"), (3000, 256, 2048, "silu_mul")])
+def test_dense_on_two_streams_at_once(dev, R, K, N, act):  # noqa: F811
+    # one handle, calls side by side on two streams and in two graphs replayed side by
+    # side: calls share nothing but the weight
+    c, d = Dense(R, K, N, True, act, True, seed=70), Dense(R, K, N, True, act, True, seed=71)
+    p = c.handle(dev)
+    d.w, d.b = c.w, c.b
+    args = [(bf16(k.x, dev), bf16(k.res, dev)) for k in (c, d)]
+    want = [p(*a) for a in args]
+    c.check(want[0])
+    outs = [[torch.empty_like(want[0]) for _ in range(20)] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs = []
+    for s, a, o in zip(streams, args, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            for t in o:
+                p(*a, out=t)
+        graphs.append(g)
+    for run in ("calls", "graphs"):
+        for o in outs[0] + outs[1]:
+            o.fill_(7)
+        torch.cuda.synchronize()
+        for i in range(20):
+            for s, a, o, g in zip(streams, args, outs, graphs):
+                with torch.cuda.stream(s):
+                    if run == "calls":
+                        p(*a, out=o[i])
+                    elif i == 0:
+                        g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(t, w) for t in o)
+    assert p.get_error() == 0
+
+
+def test_dense_offsets_past_32_bits(dev):  # noqa: F811
+    from sparse_expert_gemv_gb300 import DenseProduct
+    R, K, N = 1_100_003, 64, 2056
+    g = torch.Generator(device=dev).manual_seed(72)
+    x = torch.randn(R, K, device=dev, generator=g).bfloat16()
+    w, b = torch.randn(N, K, device=dev, generator=g).bfloat16(), torch.randn(N, device=dev).bfloat16()
+    res = torch.full((R, N), 0.5, dtype=torch.bfloat16, device=dev)
+    rows = torch.tensor([0, 1_044_461, 1_044_500, R - 1], device=dev)
+    p = DenseProduct(w, b)
+    want = x[rows].double() @ w.double().T + b.double() + 0.5
+    for float32 in (False, True):
+        got = p(x, res, float32=float32)[rows].double()
+        assert torch.allclose(got, want, rtol=1e-5 if float32 else 2.0 ** -8, atol=1e-4)
+        del got
+    assert p.get_error() == 0
+
+
+def test_norms_and_routing_offsets_past_32_bits(dev):  # noqa: F811
+    from sparse_expert_gemv_gb300 import norm_add_norm, route_experts
+    T, H = 300_001, 7168
+    g = torch.Generator(device=dev).manual_seed(73)
+    x = torch.randn(T, H, device=dev, generator=g, dtype=torch.bfloat16)
+    res = torch.randn(T, H, device=dev, generator=g, dtype=torch.bfloat16)
+    w = (1 + 0.1 * torch.randn(H, device=dev, generator=g)).bfloat16()
+    n = norm_add_norm(x, res, w, w, gate=x, gate_fn="sigmoid", mxfp8=True)
+    rows = [0, 2 ** 31 // H, 2 ** 31 // H + 1, T - 1]
+    few = norm_add_norm(x[rows], res[rows], w, w, gate=x[rows], gate_fn="sigmoid", mxfp8=True)
+    for a, b in zip(n, few):
+        assert torch.equal(a[rows], b)
+    del n, x, res
+    T, E = 8_400_007, 256
+    z = torch.randn(T, E, device=dev, generator=g)
+    bias = 0.1 * torch.randn(E, device=dev, generator=g)
+    rows = [0, 2 ** 31 // E, 2 ** 31 // E + 1, T - 1]
+    for kw in (dict(score="sigmoid", bias=bias, groups=8, top_groups=4, group_score="top2"), {}):
+        ids, wt = route_experts(z, 8, **kw)
+        few = route_experts(z[rows], 8, **kw)
+        assert torch.equal(ids[rows], few[0]) and torch.allclose(wt[rows], few[1], rtol=1e-6)
