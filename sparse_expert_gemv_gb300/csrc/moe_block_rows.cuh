@@ -1163,7 +1163,7 @@ __global__ void __launch_bounds__(V == 8 && NV > 2 ? 256 : 1024) moe_norm_add_no
     ss = F2::both(0.f);
   }
   // weights and gates a few vectors ahead of their use
-  constexpr int B = NV < 4 ? NV : 4;
+  constexpr int B = !kAhead ? 1 : NV < 4 ? NV : 4;
 #pragma unroll
   for (int i0 = 0; i0 < NV; i0 += B) {
     Raw w[B], g[B];
