@@ -121,7 +121,7 @@ moe_status_t norm_pair_launch(const moe::NormPairParams& p, bool vec, void* stre
 
 bool is_silu(const moe_dense_config_t& c) { return c.activation == MOE_ACT_SILU_MUL; }
 
-// bf16 [rows, K] in boxes of `box` rows by one stage of K
+// bf16 [rows, K] in boxes of `box` rows by one stage of K (64 values)
 bool encode_rows(CUtensorMap* tm, const void* base, int rows, int K, int box) {
   const cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
@@ -429,6 +429,11 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   p.tm_w = plan.split ? m->tm_split : m->tm_tiles;
   p.groups = m->groups;
   if (!encode_rows(&p.tm_x, x, R, c.K, plan.split ? plan.nt : plan.nt / 2)) return MOE_ERR_CUDA;
+  p.vec = p.M % 8 == 0 && aligned(out, 16) && aligned(residual, 16);
+  if (!plan.split && !out_float && p.vec &&
+      !(encode_rows(&p.tm_out, out, R, p.M, 32) &&
+        (!residual || encode_rows(&p.tm_res, residual, R, p.M, 32))))
+    return MOE_ERR_CUDA;
   p.bias = m->bias;
   p.residual = residual;
   p.out = out;
@@ -436,7 +441,6 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   p.R = R;
   p.act = c.activation;
   p.out_float = out_float != 0;
-  p.vec = p.M % 8 == 0 && aligned(out, 16) && aligned(residual, 16);
   p.stages = plan.stages;
   const bool armed = m->armed.exchange(false, std::memory_order_relaxed);
   p.polls = armed ? 50 : moe::kMbarPolls;   // a millisecond

@@ -34,6 +34,8 @@ struct DenseParams {
   // up][16 rows] in boxes of four groups, or where I is no multiple of 16, of 16 rows
   CUtensorMap tm_w;
   CUtensorMap tm_x;          // boxes of nt / 2 rows (tiles), nt rows (split)
+  // out and residual in boxes of 32 rows by 64 (tiles with bf16 outputs and vec)
+  CUtensorMap tm_out, tm_res;
   const uint16_t* bias;      // [N] or null
   const uint16_t* residual;  // [R, M] or null
   void* out;                 // [R, M]
@@ -138,6 +140,22 @@ __device__ __forceinline__ void tma1_load_2d(void* dst, const void* tmap, int x,
       : "memory");
 }
 
+// A box from shared memory to a tensor, one of the issuing thread's bulk groups.
+// Every lane may close and wait for groups: but for the elected one's they are empty.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int x, int y, const void* src) {
+  asm volatile(
+      "{\n\t" MOE_ELECT
+      "@e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n\t}" ::"l"(tmap),
+      "r"(x), "r"(y), "r"(smem_addr(src))
+      : "memory");
+}
+__device__ __forceinline__ void store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 __device__ __forceinline__ void tma2_load_4d(void* dst, const void* tmap, int c0, int c1, int c2,
                                              int c3, uint32_t bar) {
   asm volatile(
@@ -164,6 +182,15 @@ __device__ __forceinline__ void cluster_arrive() {
 }
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// The first half without its release, which waits for this thread's stores to
+// global memory too. What has to be seen goes ahead by a fence of its own.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+// Earlier writes to this CTA's shared memory, before a relaxed arrival.
+__device__ __forceinline__ void release_shared() {
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
 }
 
 // A whole warp's bounded wait on a phase of this CTA's mbarrier; a timeout
@@ -226,7 +253,7 @@ struct DenseSmem {
                                                              : kDenseStages;
   }
 };
-static_assert((2 * kDenseStages + 5) * 8 + 16 <= 1024, "barriers");
+static_assert((2 * kDenseStages + 10) * 8 + 16 <= 1024, "barriers");
 static_assert(DenseSmem::stages(kDenseCols) >= 6, "ring");
 
 // Tile i of a call: bands of kDenseBand token tiles, within a band all token
@@ -253,7 +280,9 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   uint64_t* d_full = empty + kDenseStages;
   uint64_t* d_empty = d_full + 2;                                 // used in the first CTA
   uint64_t* drain = d_empty + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* allocated = drain + 1;                                // used in the first CTA
+  uint64_t* res_full = allocated + 1;                             // [2 groups][2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(res_full + 4);
   volatile int* dead = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(kFull, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -266,6 +295,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   if (warp == 0 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
     tc::prefetch_tmap(&p.tm_x);
+    if (!FLOAT && p.vec) {
+      tc::prefetch_tmap(&p.tm_out);
+      if (p.residual) tc::prefetch_tmap(&p.tm_res);
+    }
     for (int i = 0; i < stages; ++i) {
       mbar_init(&full[i], 1 + p.withheld);   // the announcement of both CTAs' bytes
       mbar_init(&empty[i], 1);
@@ -275,15 +308,20 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
       mbar_init(&d_empty[i], 16);   // both CTAs' epilogue warps
     }
     mbar_init(drain, 1);
+    mbar_init(allocated, 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&res_full[i], 1);
     *dead = 0;
     mbar_init_fence();
+    release_shared();
   }
+  __syncwarp();
+  // The copies wait for both CTAs' barriers, but not for tensor memory, nor, below,
+  // the end for outputs on their way: with a barrier that does, 1001 x 2080 x 2056
+  // took 12.5 us instead of 12.3, 256 x 2048 x 7168 13.6 instead of 13.1.
+  cluster_arrive_relaxed();
   if (warp == 1) tc::tmem_alloc2(tmem_slot, 512);
-  tc::fence_before();
-  __syncthreads();
-  cluster_sync();   // the other CTA's barriers are ready too
-  tc::fence_after();
-  pdl_trigger();   // the next kernel's prologue may run beside this one
+  cluster_wait();   // the other CTA's barriers are ready too
+  pdl_trigger();    // the next kernel's prologue may run beside this one
   // all of tensor memory is this CTA's, so its columns start at 0
 
   if (warp == 0) {
@@ -339,11 +377,14 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
+    tc::fence_before();
+    tc::arrive_at(tc::cluster_addr(allocated, 0), rank != 0);
     if (rank == 0) {
       RingPos rg(stages);
       const uint32_t idesc = tc::f16_idesc(2 * kDenseRows, p.nt);
       int lt = 0;   // accumulators filled
-      bool ok = true;
+      bool ok = dense_wait<true>(allocated, 0, p, dead);
+      tc::fence_after();
       for (int i = first, k0 = 0; ok && i < tiles; ++lt) {
         const int buf = lt & 1;
         if (lt >= 2) ok = dense_wait<true>(&d_empty[buf], ((lt >> 1) - 1) & 1, p, dead);
@@ -380,6 +421,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     float* turn = reinterpret_cast<float*>(smem + L::out + grp * 2 * kDenseChunk);
     constexpr int kPieces = kOut / 4, kRows = 128 / kPieces;
     const int pc = et & (kPieces - 1), pr = et / kPieces;
+    const int sums_all =
+        first < tiles ? ((tiles - 1 - first) / step + 1) * ((p.nk + kDensePart - 1) / kDensePart) : 0;
     int lt = 0;
     pdl_wait();
     for (int i = first; i < tiles; i += step) {
@@ -413,7 +456,8 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
         }
         tc::fence_before();
         __syncwarp();
-        tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
+        // (to the last two nobody listens, nor would anyone wait for their way)
+        if (lt + 2 < sums_all) tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
       }
       // (a group's warps go on or leave together)
       if (!named_all(1 + grp, 128, ok)) break;
@@ -479,20 +523,35 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     const int bar = 1 + grp;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t d_empty0 = tc::cluster_addr(d_empty, 0);
-    // a chunk: 32 rows of x by kOut outputs, of which a thread moves 16 bytes of rows
-    // pr + kRows k
-    constexpr int kPieces = kOut / 8, kRows = 128 / kPieces, kMoves = 32 / kRows;
-    const int pc = et & (kPieces - 1), pr = et / kPieces;
-    const uint32_t moved = pr * kOut * 2 + ((pc ^ (pr & 7)) << 4);   // (kRows is a multiple of 8)
-    // its row of the matrices that turn 32 columns of tensor memory into rows:
-    // 16-byte piece kPieces / 4 q + i of row r holds outputs 8 i.. of this warp's and
-    // sits at piece ^ (r & 7). Without SILU matrix m of four is output group m, with
-    // SILU m & 1 of rows 8 (m >> 1) further
+    // a chunk: 32 rows of x by kOut outputs, in blocks of 64 outputs: 16-byte piece i
+    // of row r sits at i ^ (r & 7) of 128 bytes, as the copies' swizzle has it
+    constexpr int kBlocks = kOut / 64, kBlockBytes = 32 * 128;
+    // its row of the matrices that turn 32 columns of tensor memory into rows: piece
+    // 4 q + i (with SILU 2 q + i) holds outputs 8 i.. of this warp's. Without SILU
+    // matrix m of four is output group m, with SILU m & 1 of rows 8 (m >> 1) further
     const int mr = lane & 7, mm = lane >> 3;
     const uint32_t mat =
-        SILU ? (8 * (mm >> 1) + mr) * kOut * 2 + (((2 * q + (mm & 1)) ^ mr) << 4)
-             : mr * kOut * 2 + (((4 * q + mm) ^ mr) << 4);
+        SILU ? (8 * (mm >> 1) + mr) * 128 + (((2 * q + (mm & 1)) ^ mr) << 4)
+             : (q >> 1) * kBlockBytes + mr * 128 + (((4 * (q & 1) + mm) ^ mr) << 4);
+    // The group's first warp copies chunks in and out (vec): the residual's come a
+    // chunk ahead, onto the place that the results leave from. (By registers and the
+    // threads' own loads and stores 4096 x 768 x 2048 with a residual took 17.4 us
+    // instead of 15.6, 1001 x 2080 x 2056 12.9 instead of 12.5, 8192 x 2048 x 7168
+    // under load 152.4 instead of 151.3.)
+    auto place = [&](int ch) { return smem + L::out + (2 * grp + (ch & 1)) * kDenseChunk; };
+    auto ask = [&](int ch, int n0, int row) {
+      uint64_t* landed = res_full + 2 * grp + (ch & 1);
+      tc::expect(landed, kBlocks * kBlockBytes);
+#pragma unroll
+      for (int h = 0; h < kBlocks; ++h)
+        tc::tma1_load_2d(place(ch) + h * kBlockBytes, &p.tm_res, n0 + 64 * h, row, landed);
+    };
+    // else a thread moves piece pc of rows pr + kRows k
+    constexpr int kPieces = kOut / 8, kRows = 128 / kPieces, kMoves = 32 / kRows;
+    const int pc = et & (kPieces - 1), pr = et / kPieces;
+    const uint32_t moved = (pc >> 3) * kBlockBytes + pr * 128 + (((pc ^ pr) & 7) << 4);   // (kRows is a multiple of 8)
     int lt = 0, chunk = 0;
+    bool ok = true;
     pdl_wait();
     for (int i = first; i < tiles; i += step, ++lt) {
       int m, t;
@@ -511,35 +570,19 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           if (row < p.M) bias[k] = bf16_at(p.bias + row + (SILU && k > 1 ? p.M : 0));
         }
       }
-      uint4 res[kMoves];
-      auto load_residual = [&](int c0) {
-#pragma unroll
-        for (int k = 0; k < kMoves; ++k) {
-          const int row = c0 + pr + kRows * k;
-          res[k] = make_uint4(0, 0, 0, 0);
-          if (row >= n || pn >= p.M) continue;
-          const uint16_t* src = p.residual + (size_t)(r0 + row) * p.M + pn;
-          if (p.vec) {
-            res[k] = __ldcs(reinterpret_cast<const uint4*>(src));
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = (pn + 2 * j < p.M ? src[2 * j] : 0u) |
-                     (pn + 2 * j + 1 < p.M ? (uint32_t)src[2 * j + 1] << 16 : 0u);
-            res[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      };
-      if (p.residual) load_residual(32 * grp);
-      bool ok = dense_wait<true>(&d_full[buf], (lt >> 1) & 1, p, dead);
+      if (p.residual && p.vec && q == 0 && ok) {
+        tc::store_wait_read();   // both places are free
+        if (32 * grp < n) ask(chunk, n0, r0 + 32 * grp);
+        if (32 * grp + 64 < n) ask(chunk + 1, n0, r0 + 32 * grp + 64);
+      }
+      ok = dense_wait<true>(&d_full[buf], (lt >> 1) & 1, p, dead) && ok;
       // a group's warps go on or leave together: no named barrier below waits
       // for a warp that gave up
       ok = named_all(bar, 128, ok);
       if (!ok) break;
       tc::fence_after();
       for (int c0 = 32 * grp; c0 < n; c0 += 64, ++chunk) {
-        uint8_t* stage = smem + L::out + (2 * grp + (chunk & 1)) * kDenseChunk;
+        uint8_t* stage = place(chunk);
         // register 4 b + 2 i + j of the two halves: weight row 8 i + lane / 4 (16
         // further in the second), row 8 b + 2 (lane % 4) + j of x
         constexpr int kVals = SILU ? 16 : 32;
@@ -564,14 +607,34 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           return SILU ? 8 * b + 4 * (k >> 1) + 2 * (k & 1) : 16 * (k >> 1) + 4 * b + 2 * (k & 1);
         };
         constexpr int kSets = kVals / 8;
-        constexpr uint32_t kSetBytes = (SILU ? 16 : 8) * kOut * 2;
+        constexpr uint32_t kSetBytes = (SILU ? 16 : 8) * 128;
         const uint32_t mats = smem_addr(stage) + mat;
+        // the other place is free once its results have left
+        if (p.vec && q == 0) {
+          tc::store_wait_read();
+          if (p.residual && ok && c0 >= 64 && c0 + 64 < n) ask(chunk + 1, n0, r0 + c0 + 64);
+        }
         if (p.residual) {
+          if (p.vec) {
+            // (a timeout marks the pair dead; the group leaves together at its next tile)
+            ok = dense_wait<true>(&res_full[2 * grp + (chunk & 1)], (chunk >> 1) & 1, p, dead) && ok;
+          } else {
 #pragma unroll
-          for (int k = 0; k < kMoves; ++k)
-            *reinterpret_cast<uint4*>(stage + moved + k * kRows * kOut * 2) = res[k];
-          if (c0 + 64 < n) load_residual(c0 + 64);
-          named_sync(bar, 128);
+            for (int k = 0; k < kMoves; ++k) {
+              const int row = c0 + pr + kRows * k;
+              uint32_t w[4] = {};
+              if (row < n) {
+                const uint16_t* src = p.residual + (size_t)(r0 + row) * p.M + pn;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  w[j] = (pn + 2 * j < p.M ? src[2 * j] : 0u) |
+                         (pn + 2 * j + 1 < p.M ? (uint32_t)src[2 * j + 1] << 16 : 0u);
+              }
+              *reinterpret_cast<uint4*>(stage + moved + k * kRows * 128) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            named_sync(bar, 128);
+          }
 #pragma unroll
           for (int b = 0; b < kSets; ++b) {
             uint32_t w[4];
@@ -588,17 +651,25 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
           auto pack = [&](int k) { return RowVec<8>::pack(v[at(b, k)], v[at(b, k) + 1]); };
           tc::stm4_trans(mats + b * kSetBytes, pack(0), pack(1), pack(2), pack(3));
         }
-        named_sync(bar, 128);
-        uint16_t* out = static_cast<uint16_t*>(p.out);
+        if (p.vec) {
+          tc::fence_proxy_async();
+          named_sync(bar, 128);
+          if (q == 0) {
 #pragma unroll
-        for (int k = 0; k < kMoves; ++k) {
-          const int row = c0 + pr + kRows * k;
-          if (row >= n || pn >= p.M) continue;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + moved + k * kRows * kOut * 2);
-          uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
-          if (p.vec) {
-            *reinterpret_cast<uint4*>(dst) = w;
-          } else {
+            for (int h = 0; h < kBlocks; ++h)
+              if (n0 + 64 * h < p.M)
+                tc::tma_store_2d(&p.tm_out, n0 + 64 * h, r0 + c0, stage + h * kBlockBytes);
+            tc::store_commit();
+          }
+        } else {
+          named_sync(bar, 128);
+          uint16_t* out = static_cast<uint16_t*>(p.out);
+#pragma unroll
+          for (int k = 0; k < kMoves; ++k) {
+            const int row = c0 + pr + kRows * k;
+            if (row >= n) continue;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + moved + k * kRows * 128);
+            uint16_t* dst = out + (size_t)(r0 + row) * p.M + pn;
             const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -608,8 +679,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
       }
       tc::fence_before();
       __syncwarp();
-      tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
+      // (as above)
+      if (i + 2 * step < tiles) tc::arrive_at(d_empty0 + 8 * buf, rank != 0);
     }
+    if (q == 0) tc::store_wait_read();
   }
   __syncwarp();
   tc::fence_before();
@@ -622,7 +695,10 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
   if (warp == 0 && *dead)
     for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
   __syncwarp();
-  cluster_sync();   // no CTA leaves while the other may still reach into it
+  // No CTA leaves while the other may still reach into it: arrivals from there have
+  // been waited for, MMAs are done (allocated, d_empty, empty, d_full, drain).
+  cluster_arrive_relaxed();
+  cluster_wait();
   tc::fence_after();
   if (warp == 1) tc::tmem_dealloc2(*tmem_slot, 512);
 }
