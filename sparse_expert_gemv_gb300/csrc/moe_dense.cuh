@@ -876,6 +876,17 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = up_bias[i] = 0.f;
   if (warp < 8) {
+    if (p.residual) {
+      // on its way to L2 while the products are made, 128 bytes a request (64 x 2048 x
+      // 7168: 9.4 us instead of 9.75)
+      pdl_wait();
+      if ((grp & 7) == 0 && out_m < p.M)
+#pragma unroll 1
+        for (int slot = threadIdx.x / kGroups; (slot << log_parts) + rank < n;
+             slot += kSplitEpilogue / kGroups)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(__cvta_generic_to_global(
+              p.residual + (size_t)(r0 + (slot << log_parts) + rank) * p.M + out_m)));
+    }
     if (p.bias) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
