@@ -417,6 +417,35 @@ def test_dense_outputs_off_the_vector_alignment(dev, N, float32):  # noqa: F811
         assert out[:skew_out].eq(7).all() and out[skew_out + 37 * N:].eq(7).all()
 
 
+@pytest.mark.parametrize("R,K,N,act", [(1301, 264, 2120, None), (2900, 136, 1208, "gelu_tanh"),
+                                       (1301, 264, 4240, "silu_mul"), (2900, 136, 2288, "silu_mul")])
+def test_dense_of_many_rows_in_place_and_off_the_alignment(dev, R, K, N, act):  # noqa: F811
+    import ctypes
+    from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan, lib
+    plan = MoEDensePlan()
+    config = MoEDenseConfig(N, K, 5 if act == "silu_mul" else 4 if act else 0)
+    assert lib.moe_dense_plan(ctypes.byref(config), R, 0, 152, ctypes.byref(plan)) == 0 and not plan.split
+    c = Dense(R, K, N, True, act, True, seed=35)
+    p, M = c.handle(dev), c.M
+    x, res = bf16(c.x, dev), bf16(c.res, dev)
+    want = p(x, res)
+    c.check(want)
+    for skew_res, skew_out in ((0, 0), (0, 8), (8, 0), (1, 0), (0, 1), (3, 5)):
+        r = torch.full((R * M + 16,), 7.0, dtype=torch.bfloat16, device=dev)
+        out = torch.full((R * M + 16,), 7.0, dtype=torch.bfloat16, device=dev)
+        rv, ov = r[skew_res:][:R * M].view(R, M), out[skew_out:][:R * M].view(R, M)
+        rv.copy_(res)
+        p(x, rv, out=ov)
+        assert torch.equal(ov, want) and torch.equal(rv, res)
+        assert out[:skew_out].eq(7).all() and out[skew_out + R * M:].eq(7).all()
+        p(x, rv, out=rv)
+        assert torch.equal(rv, want)
+        assert r[:skew_res].eq(7).all() and r[skew_res + R * M:].eq(7).all()
+    p(x[:-3], res[:-3], out=out[:(R - 3) * M].view(R - 3, M))
+    assert torch.equal(out[:(R - 3) * M].view(R - 3, M), want[:-3])
+    assert p.get_error() == 0
+
+
 @pytest.mark.parametrize("act", [None, "silu_mul"])
 @pytest.mark.parametrize("R,K,N", [(2, 64, 128), (5, 2048, 384), (40, 1024, 4096), (600, 512, 2048),
                                    (3000, 256, 2048)])
