@@ -174,9 +174,9 @@ size_t split_smem(const DensePlan& p) {
   return std::max(need, kSplitSmemMin);
 }
 
-// The cheapest cut by a model of its time, in us. Its constants were fitted to 560
-// timings (24 shapes from 1 to 4096 rows, every cut of each, inputs beyond L2); its
-// choices are on average 1.4 % slower than the best of them, 9 % at worst.
+// The cheapest cut by a model of its time, in us. Its constants were fitted to some
+// 500 timings (30 shapes from 1 to 8192 rows, every cut of each, inputs beyond L2);
+// its choices are on average 1.1 % slower than the best of them, 12 % at worst.
 //   split   a start, then the stages of a CTA at what an SM, shared by the CTAs on
 //           it, or all of L2 delivers, or its ring's latency allows where it turns;
 //           the parts' exchange; clusters that find no room wait for a round more
@@ -198,7 +198,7 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, bool out_float, int num
     const double bytes = moe::DenseSmem::stage(nt);   // a stage's, of one CTA
     const double stage = std::max({0.0012 * nt, bytes / 108.8e3,
                                    std::min<double>(tiles, pairs) * 2 * bytes / kL2});
-    take({false, nt, 1, moe::DenseSmem::stages(nt), kStart + 1.51 + std::ceil(tiles / pairs) * nk * stage +
+    take({false, nt, 1, moe::DenseSmem::stages(nt), kStart + 1.2 + std::ceil(tiles / pairs) * nk * stage +
                                0.0082 * std::min(nt, R)});
   }
   const double hbm = 2.0 * c.K * ((double)c.N + R) / 6.8e6;
@@ -218,10 +218,10 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, bool out_float, int num
                                             : (S == 8 ? 120 : S == 4 ? 144 : 152)) / 152.0;
         const double run = std::min(ctas, most), shared = half ? std::min(2.0, std::ceil(run / num_sms)) : 1;
         const double g = std::ceil((double)nk / S);
-        const double rate = std::min(153e3 / shared, g > stages ? stages * bytes / 1.68 : 153e3);
+        const double rate = std::min(153e3 / shared, g > stages ? stages * bytes / 1.83 : 153e3);
         const double stream = std::max(g * bytes / rate, run * g * bytes / kL2);
-        const double per = 1.71 + stream + n * (0.01 / S + (S > 1 ? 0.0129 : 0)) + 0.118 * (S - 1);
-        take({true, nt, S, stages, kStart + std::max(std::ceil(ctas / most) * per, hbm + 1.71)});
+        const double per = 1.65 + stream + n * (0.005 / S + (S > 1 ? 0.0112 : 0)) + 0.118 * (S - 1);
+        take({true, nt, S, stages, kStart + std::max(std::ceil(ctas / most) * per, hbm + 1.65)});
       }
     }
   }
