@@ -418,7 +418,8 @@ def test_dense_outputs_off_the_vector_alignment(dev, N, float32):  # noqa: F811
 
 
 @pytest.mark.parametrize("R,K,N,act", [(1301, 264, 2120, None), (2900, 136, 1208, "gelu_tanh"),
-                                       (1301, 264, 4240, "silu_mul"), (2900, 136, 2288, "silu_mul")])
+                                       (1301, 264, 4240, "silu_mul"), (2900, 136, 2288, "silu_mul"),
+                                       (9000, 64, 8, None), (9000, 64, 16, "silu_mul")])
 def test_dense_of_many_rows_in_place_and_off_the_alignment(dev, R, K, N, act):  # noqa: F811
     import ctypes
     from sparse_expert_gemv_gb300._lib import MoEDenseConfig, MoEDensePlan, lib
