@@ -228,11 +228,11 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const
 // The tensor cores cut a sum off at each step of 16 K instead of rounding it, which
 // adds up along K (relative error of 8191 x 7168 x 256 by its 2-norm: 7.9e-6, of FP32
 // FMAs 0.9e-6). bf16 outputs do not show it. Where the outputs are FP32 (FLOAT), the
-// sums of kDensePart stages in turn are added up in registers: 1.0e-6 in the same
-// time, with parts of eight stages 0.5e-6.
+// sums of kDensePart stages in turn are added up in registers: 0.5e-6 with eight
+// stages, 1.0e-6 with 16, in the same time.
 // ---------------------------------------------------------------------------
 constexpr int kDenseThreads = 384;
-constexpr int kDensePart = 16;                 // stages
+constexpr int kDensePart = 8;                  // stages
 constexpr int kDenseFloatCols = 128;           // rows of x a tile with FLOAT, at most
 constexpr int kDenseChunk = 32 * 256;   // epilogue staging: 32 rows of 128 bf16
 
@@ -242,7 +242,7 @@ constexpr int kDenseSmemMax = 232448 - 1024;
 // The ring takes what the epilogue's chunks leave: a slot's way from the MMA's
 // release through a copy back to the MMA takes more than a microsecond, and narrow
 // tiles' stages are small (router logits of 8191 x 7168 x 256 in tiles of 128 rows:
-// 30.4 us with six stages, 27.5 with eight, 28.9 with the sums of FP32 outputs).
+// 30.4 us with six stages, 27.5 with eight, 28.7 with the sums of FP32 outputs).
 struct DenseSmem {
   static constexpr int out = 0;                     // [2 groups][2] chunks
   static constexpr int bars = out + 4 * kDenseChunk;
@@ -719,6 +719,9 @@ constexpr int kSplitBars = 1024;   // bytes kept for barriers in front of the ri
 constexpr int kSplitStages = 16;   // of the ring, at most
 
 __host__ __device__ constexpr int split_stage_bytes(int nt) { return kDenseABytes + nt * kDenseK * 2; }
+// Columns of an accumulator, and how many half of tensor memory holds.
+__host__ __device__ constexpr int split_cols(int nt) { return nt <= 32 ? 32 : nt <= 64 ? 64 : 128; }
+__host__ __device__ constexpr int split_accs(int nt) { return 256 / split_cols(nt); }
 // What the parts of a tile's sums take in the CTAs that add them (a single part
 // takes the ring's place, which is free then).
 __host__ __device__ constexpr int split_sum_bytes(int nt, int S) {
@@ -802,7 +805,13 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
   const int n = min(p.nt, p.R - r0);
   const int k0 = (int)((int64_t)p.nk * rank >> log_parts);
   const int k1 = (int)((int64_t)p.nk * (rank + 1) >> log_parts);
-  const uint32_t tcols = p.nt <= 32 ? 32 : p.nt <= 64 ? 64 : 128;
+  const uint32_t tcols = split_cols(p.nt);
+  // FP32 outputs: accumulators side by side take kDensePart stages in turn, as many
+  // as half of tensor memory holds (two CTAs may share an SM's). 2 x 5816 x 316: error
+  // 1.1e-6 -> 0.5e-6, 3.9 -> 4.0 us.
+  const int accs = p.out_float ? min((k1 - k0 + kDensePart - 1) / kDensePart, split_accs(p.nt)) : 1;
+  const int acc_stages = (k1 - k0 + accs - 1) / accs;
+  const uint32_t all_cols = tcols << (accs > 4 ? 3 : accs > 2 ? 2 : accs > 1 ? 1 : 0);
 
   if (warp == 8 && lane == 0) {
     tc::prefetch_tmap(&p.tm_w);
@@ -815,7 +824,7 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     *dead = 0;
     mbar_init_fence();
   }
-  if (warp == 9) tc::tmem_alloc(tmem_slot, tcols);
+  if (warp == 9) tc::tmem_alloc(tmem_slot, all_cols);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -851,7 +860,9 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
   } else if (warp == 9) {
     RingPos rg(p.stages);
     const uint32_t idesc = tc::f16_idesc(kDenseRows, p.nt);
-    for (int kb = k0; kb < k1; ++kb) {
+    uint32_t d = tmem;
+    for (int kb = k0, in = 0; kb < k1; ++kb, ++in) {
+      if (in == acc_stages) in = 0, d += tcols;
       const int s = rg.slot;
       ok = dense_wait<false>(&full[s], rg.phase, p, dead);
       if (!ok) break;
@@ -859,7 +870,7 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
       const uint64_t ad = tc::sdesc_sw128(base), bd = tc::sdesc_sw128(base + kDenseABytes);
 #pragma unroll
       for (int q = 0; q < kDenseK / 16; ++q)
-        tc::mma_f16<false>(tmem, ad + 2 * q, bd + 2 * q, idesc, kb > k0 || q > 0 ? 1u : 0u);
+        tc::mma_f16<false>(d, ad + 2 * q, bd + 2 * q, idesc, in > 0 || q > 0 ? 1u : 0u);
       tc::commit1(&empty[s]);
       rg.next();
     }
@@ -903,8 +914,18 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
 #pragma unroll 1
       for (int c0 = 16 * (warp >> 2); c0 < n; c0 += 32) {
         uint32_t raw[16];
-        tc::ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0, raw);
+        const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c0;
+        tc::ld16(from, raw);
         tc::wait_ld();
+#pragma unroll 1
+        for (int a = acc_stages, i = 1; a < k1 - k0; a += acc_stages, ++i) {
+          uint32_t more[16];
+          tc::ld16(from + i * tcols, more);
+          tc::wait_ld();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            raw[j] = __float_as_uint(__uint_as_float(raw[j]) + __uint_as_float(more[j]));
+        }
         float* to = sums + rank * slots * kDenseRows + (threadIdx.x & 127);
         if (S == 1) {
 #pragma unroll
@@ -961,7 +982,7 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     for (int i = 0; i < kProdSettleSleeps; ++i) __nanosleep(kWaitSuspendNs);
   __syncthreads();
   tc::fence_after();
-  if (warp == 9) tc::tmem_dealloc(tmem, tcols);
+  if (warp == 9) tc::tmem_dealloc(tmem, all_cols);
 }
 
 }  // namespace moe
