@@ -207,7 +207,7 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, bool out_float, int num
     const int n = std::min(nt, R), bytes = moe::split_stage_bytes(nt);
     for (int S = 1; S <= 8 && S <= nk; S *= 2) {
       // FP32 outputs: not too long sums in the tensor cores
-      if (out_float && S < 8 && (nk + S - 1) / S > moe::kDensePart * moe::split_accs(nt)) continue;
+      if (out_float && S < 8 && (nk + S - 1) / S > 2 * moe::kDensePart) continue;
       for (const int room : {kSplitFull, kSplitHalf}) {
         const int stages = split_stages(nt, S, room);
         if (stages < 2) continue;
