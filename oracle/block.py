@@ -13,7 +13,7 @@ import numpy as np
 from .bf16 import bf16_rne
 
 INF = float("inf")
-_erf = np.vectorize(math.erf, otypes=[np.float64])
+_erfc = np.vectorize(math.erfc, otypes=[np.float64])
 
 
 def sigmoid(v):
@@ -102,9 +102,9 @@ def activate(y, activation=None):
     if activation == "silu":
         return y * sigmoid(y)
     if activation == "gelu":
-        return 0.5 * y * (1 + _erf(y / math.sqrt(2)))
+        return 0.5 * y * _erfc(-y / math.sqrt(2))   # (1 + erf z = erfc -z)
     if activation == "gelu_tanh":
-        return 0.5 * y * (1 + np.tanh(math.sqrt(2 / math.pi) * (y + 0.044715 * y ** 3)))
+        return y * sigmoid(math.sqrt(8 / math.pi) * (y + 0.044715 * y ** 3))   # (1 + tanh z) / 2
     I = y.shape[1] // 2
     return y[:, :I] * sigmoid(y[:, :I]) * y[:, I:]
 

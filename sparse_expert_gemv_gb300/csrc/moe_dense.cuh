@@ -68,8 +68,30 @@ __device__ __forceinline__ float dense_gelu_tanh(float v) {
   const float e = __expf(-fabsf(z2));
   return __fdividef(z2 < 0.f ? v * e : v, 1.f + e);
 }
+// v (1 + erf(v / sqrt 2)) / 2 from erfc(z), z = |v| / sqrt 2: v erfc(z) / 2 below zero,
+// where 1 + erf cancels (6 % of the result at -5, all of it from -5.5 on), v - v erfc(z) / 2
+// above. e^(z^2) erfc(z) is a polynomial in t = 1 / (1 + 0.55 z) times t (the variable of
+// Schonfelder's expansions, Math. Comp. 32, 1978; the coefficients are a relative
+// least-squares fit of our own over z <= 10, off by 7e-9), in powers of t - 9/16: 4 units
+// of 2^-24 with FP32's rounding. (1001 x 2080 x 2056 with a residual and 8192 x 2048 x
+// 2048: 13.5 and 44.4 us, with erfcf 15.2 and 52.9, with the cancelling erff 13.0 and 44.0.)
 __device__ __forceinline__ float dense_gelu(float v) {
-  return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+  const float a = fminf(fabsf(v), 16.f);   // e^(-a^2 / 2) is 0 there
+  const float t = __fdividef(1.f, fmaf(a, 0.388908744f, 1.f));
+  const float s = t - 0.5625f;
+  float r = 5.804775655e-02f;
+  r = fmaf(r, s, -4.279274493e-02f);
+  r = fmaf(r, s, -7.251586765e-02f);
+  r = fmaf(r, s, 1.079753712e-01f);
+  r = fmaf(r, s, 5.148212239e-02f);
+  r = fmaf(r, s, -2.026180327e-01f);
+  r = fmaf(r, s, -6.769769639e-02f);
+  r = fmaf(r, s, 4.481518269e-01f);
+  r = fmaf(r, s, 7.503036857e-01f);
+  r = fmaf(r, s, 5.977187753e-01f);
+  r *= t * exp2f(a * a * -0.72134751f);
+  const float w = 0.5f * (v < 0.f ? v : a) * r;
+  return v < 0.f ? w : v - w;   // (infinity and NaN stay what they are, -infinity is NaN)
 }
 // (NaN stays NaN)
 __device__ __forceinline__ float dense_relu(float v) { return v < 0.f ? 0.f : v; }
