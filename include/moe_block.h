@@ -126,8 +126,10 @@ typedef struct moe_dense* moe_dense_t;
 /*
  * A handle over one weight matrix on the current device.
  *   weight  bf16 [N, K], 16-byte aligned;  bias bf16 [N] or NULL
- * Both are borrowed until moe_dense_destroy and keep their values until then (a
- * run reads the weight before it waits for earlier work on its stream). Allocates
+ * Both are borrowed until moe_dense_destroy. They hold their values when this is
+ * called, their writers' work being over (that of the default stream is waited for
+ * here), and keep them until then: a run reads them before it waits for earlier
+ * work on its stream. Allocates
  * an error word, one CUDA event and one non-blocking stream (for reading the error
  * word), so it is made outside graph captures; runs may be captured, and runs on
  * several streams may overlap. N and K up to 2^31 - 256.

@@ -102,14 +102,16 @@ class DenseProduct:
     weight is bf16 [N, K] with K a multiple of 8, bias bf16 [N] or None; both
     are borrowed (kept alive by this object), are not to be written while it
     lives (a call reads ahead of earlier work on its stream), and lie where the
-    rows of every call have to. `activation` is None, "relu", "silu", "gelu",
+    rows of every call have to. Making the handle waits for `stream` (the
+    current one of the weight's device if not given), on which they may have
+    been written. `activation` is None, "relu", "silu", "gelu",
     "gelu_tanh", or "silu_mul": the N = 2I weight rows are then I gate rows and
     I up rows, and the result is the I values SiLU(gate) * up. The handle is
     made outside graph captures; calls may be captured, and calls on several
     streams may overlap.
     """
 
-    def __init__(self, weight, bias=None, *, activation: str | None = None):
+    def __init__(self, weight, bias=None, *, activation: str | None = None, stream=None):
         act = _one_of(activation, _ACTIVATIONS, "activation")
         if not isinstance(weight, torch.Tensor):
             raise TypeError("weight must be a torch.Tensor")
@@ -121,11 +123,15 @@ class DenseProduct:
             _need(bias, torch.bfloat16, (N,), "bias")
             if bias.device != weight.device:
                 raise ValueError(f"bias: expected a tensor on {weight.device}, got one on {bias.device}")
+        if stream is not None and stream.device != weight.device:
+            raise ValueError(f"stream: expected one of {weight.device}, got one of {stream.device}")
         self.N, self.K, self.activation = N, K, activation
         self.M = N // 2 if activation == "silu_mul" else N
         self._weights, self._device = (weight, bias), weight.device.index
         h = ctypes.c_void_p()
         with torch.cuda.device(weight.device):
+            # nothing orders a call's early reads behind what writes the weight
+            (torch.cuda.current_stream() if stream is None else stream).synchronize()
             check(lib.moe_dense_create(ctypes.byref(MoEDenseConfig(N, K, act)), _ptr(weight),
                                        _ptr(bias), ctypes.byref(h)), "moe_dense_create")
         self._h = h
