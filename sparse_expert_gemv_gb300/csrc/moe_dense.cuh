@@ -402,6 +402,7 @@ __global__ void __launch_bounds__(kDenseThreads, 1) moe_dense_tiles(
     tc::fence_before();
     tc::arrive_at(tc::cluster_addr(allocated, 0), rank != 0);
     if (rank == 0) {
+      pdl_wait();   // no bounded wait begins before the kernels before this one end
       RingPos rg(stages);
       const uint32_t idesc = tc::f16_idesc(2 * kDenseRows, p.nt);
       int lt = 0;   // accumulators filled
@@ -880,6 +881,7 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
       rg.next();
     }
   } else if (warp == 9) {
+    pdl_wait();   // as in moe_dense_tiles
     RingPos rg(p.stages);
     const uint32_t idesc = tc::f16_idesc(kDenseRows, p.nt);
     uint32_t d = tmem;
@@ -909,10 +911,10 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
 #pragma unroll
   for (int i = 0; i < 8; ++i) bias[i] = up_bias[i] = 0.f;
   if (warp < 8) {
+    pdl_wait();
     if (p.residual) {
       // on its way to L2 while the products are made, 128 bytes a request (64 x 2048 x
       // 7168: 9.4 us instead of 9.75)
-      pdl_wait();
       if ((grp & 7) == 0 && out_m < p.M)
 #pragma unroll 1
         for (int slot = threadIdx.x / kGroups; (slot << log_parts) + rank < n;
@@ -974,7 +976,6 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
     cluster_sync();   // the parts have landed, and no CTA reaches into another after it
   else
     __syncthreads();
-  if (warp < 8) pdl_wait();
   if (warp < 8 && ok && out_m < p.M) {
 #pragma unroll 2
     for (int slot = threadIdx.x / kGroups; (slot << log_parts) + rank < n;
