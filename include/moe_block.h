@@ -16,7 +16,9 @@
  * pointers, work enqueued on `stream` without waiting, argument errors found
  * on the host (nothing is enqueued then), results bitwise reproducible.
  * T = 0 or R = 0 is a successful no-op. Calls keep no state between them
- * except a dense product's error word.
+ * except a dense product's error word. An output shares no memory with another
+ * tensor of its call, but for those that are named as the same below; other calls
+ * are refused (MOE_ERR_INVALID_ARG).
  */
 #ifndef MOE_BLOCK_H
 #define MOE_BLOCK_H
@@ -89,7 +91,7 @@ moe_status_t moe_route_experts(const moe_route_config_t* cfg, int32_t T, const v
  *   n    = s * rsqrt(mean(s^2) + eps) * pre_weight
  * with g the identity, sigmoid or tanh (1 without a gate), in FP32. Outputs:
  *   sum     bf16 [T, H]   s, the new residual stream; may be `x` or `residual`
- *   y       bf16 [T, H]   bf16(n), or NULL
+ *   y       bf16 [T, H]   bf16(n), or NULL; may be the one of them that `sum` is not
  *   codes   uint8 [T, H], scales uint8 [T, H/32]   MXFP8(n) as moe_prompt.h
  *           defines it, both or neither
  * Without pre_weight there is no n: y, codes and scales are NULL.

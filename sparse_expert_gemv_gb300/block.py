@@ -17,7 +17,9 @@ and the results carry no graph. Every call forwards device pointers and a
 stream to libmoe_decode.so through the extension module _moe_torch, which
 checks the tensors, allocates the outputs that were not passed in, and takes
 the current stream or the torch.cuda.Stream given as `stream`. New outputs
-belong to the stream of the call, as if it were current.
+belong to the stream of the call, as if it were current. Outputs that are passed
+in share no memory with other tensors of the call, but where it says so; such
+calls are refused.
 """
 from __future__ import annotations
 
@@ -86,7 +88,8 @@ def norm_add_norm(x, residual, post_weight=None, pre_weight=None, *, gate=None, 
     (per row) or [T, H]; gate_fn is None, "sigmoid" or "tanh". Returns s as RmsNorm.sum and n in
     bf16 (`bf16`), as MXFP8 codes and scales (`mxfp8`), or both; without
     pre_weight s alone. The buffers sum, y, codes and scales may be passed in;
-    sum may be x or residual, which is then updated in place.
+    sum may be x or residual, which is then updated in place, and y the one of
+    them that sum is not.
     """
     flags = _one_of(gate_fn, _GATE_FNS, "gate_fn") | (_UNIT_OFFSET if unit_offset else 0)
     if gate is None and gate_fn is not None:

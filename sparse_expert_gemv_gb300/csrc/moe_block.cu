@@ -21,6 +21,7 @@ struct moe_dense : moe::Handle {
   int num_sms;
   CUtensorMap tm_tiles, tm_split;   // the weight as the two kernels take it
   int groups;                       // tm_tiles has groups of 16 rows
+  const uint16_t* weight;
   const uint16_t* bias;
   std::atomic<bool> armed;   // the next run's waits run out (moe_dense_arm_timeout)
 };
@@ -33,6 +34,8 @@ constexpr int32_t kMaxRows = 0x7fffff00;
 
 using moe::aligned;
 using moe::launch;
+using moe::overlap;
+using moe::Span;
 
 // ---- routing -----------------------------------------------------------------
 
@@ -297,6 +300,12 @@ moe_status_t moe_route_experts(const moe_route_config_t* cfg, int32_t T, const v
   const bool bf16 = (c.flags & MOE_ROUTE_BF16) != 0;
   if (!aligned(logits, bf16 ? 2 : 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(w, 4))
     return MOE_ERR_MISALIGNED;
+  const size_t rows = T, size = bf16 ? 2 : 4;
+  const Span in{logits, rows * c.E * size}, add{bias, (size_t)c.E * 4};
+  const Span out{ids, rows * c.k * 4}, weights{w, rows * c.k * 4};
+  if (overlap(out, in) || overlap(out, add) || overlap(weights, in) || overlap(weights, add) ||
+      overlap(out, weights))
+    return MOE_ERR_INVALID_ARG;
   moe::RouteParams p;
   p.logits = logits;
   p.bias = bias;
@@ -346,6 +355,21 @@ moe_status_t moe_norm_add_norm(int32_t T, int32_t H, const uint16_t* x, const ui
   for (const uint16_t* a : {x, residual, post_weight, pre_weight, gate,
                             const_cast<const uint16_t*>(sum), const_cast<const uint16_t*>(y)})
     if (!aligned(a, 2)) return MOE_ERR_MISALIGNED;
+  // A thread reads its elements of x and residual before it writes the same ones of
+  // sum or y, so that those may lie there; nothing else may.
+  const size_t all = (size_t)T * H * 2, row = (size_t)H * 2;
+  const Span outs[] = {{sum, all}, {y, all}, {codes, all / 2}, {scales, all / 64}};
+  const Span ins[] = {{x, all}, {residual, all}, {post_weight, row}, {pre_weight, row},
+                      {gate, flags & MOE_NORM_GATE_FULL  ? all
+                             : flags & MOE_NORM_GATE_ROW ? (size_t)T * 2
+                                                         : row}};
+  for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < 5; ++j)
+      if (overlap(outs[i], ins[j]) && !(i < 2 && j < 2 && outs[i].at == ins[j].at))
+        return MOE_ERR_INVALID_ARG;
+  }
   moe::NormPairParams p;
   p.x = x;
   p.residual = residual;
@@ -385,6 +409,7 @@ moe_status_t moe_dense_create(const moe_dense_config_t* cfg, const uint16_t* wei
   moe_dense* m = new (std::nothrow) moe_dense();
   if (!m) return MOE_ERR_CUDA;
   m->cfg = c;
+  m->weight = weight;
   m->bias = bias;
   const bool ok =
       cudaGetDevice(&m->device) == cudaSuccess &&
@@ -419,6 +444,13 @@ moe_status_t moe_dense_run(moe_dense_t m, int32_t R, const uint16_t* x, const ui
   if (device != m->device) return MOE_ERR_INVALID_ARG;
   const moe_dense_config_t& c = m->cfg;
   const bool silu = is_silu(c);
+  const size_t outputs = (size_t)R * (silu ? c.N / 2 : c.N);
+  const Span result{out, outputs * (out_float ? 4 : 2)};
+  if (overlap(result, {x, (size_t)R * c.K * 2}) ||
+      overlap(result, {m->weight, (size_t)c.N * c.K * 2}) ||
+      overlap(result, {m->bias, (size_t)c.N * 2}) ||
+      (overlap(result, {residual, outputs * 2}) && (out_float || out != residual)))
+    return MOE_ERR_INVALID_ARG;
   const DensePlan plan = plan_dense(c, R, out_float != 0, m->num_sms);
   moe::DenseParams p;
   p.M = silu ? c.N / 2 : c.N;

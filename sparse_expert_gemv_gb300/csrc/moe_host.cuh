@@ -17,6 +17,16 @@ namespace moe {
 
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// A tensor's bytes; null is none.
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+inline bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+
 template <typename... KArgs, typename... Args>
 moe_status_t launch(void (*kernel)(KArgs...), unsigned grid, dim3 block, size_t smem, void* stream,
                     unsigned cluster, const Args&... args) {
