@@ -209,8 +209,9 @@ DensePlan plan_dense(const moe_dense_config_t& c, int R, bool out_float, int num
     if (nt - 16 >= R) continue;
     const int n = std::min(nt, R), bytes = moe::split_stage_bytes(nt);
     for (int S = 1; S <= 8 && S <= nk; S *= 2) {
-      // FP32 outputs: not too long sums in the tensor cores
-      if (out_float && S < 8 && (nk + S - 1) / S > 2 * moe::kDensePart) continue;
+      // FP32 outputs: an accumulator takes kDensePart stages at most (and fewer than
+      // eight parts no more than two accumulators)
+      if (out_float && (nk + S - 1) / S > moe::kDensePart * (S < 8 ? 2 : moe::split_accs(nt))) continue;
       for (const int room : {kSplitFull, kSplitHalf}) {
         const int stages = split_stages(nt, S, room);
         if (stages < 2) continue;

@@ -829,9 +829,9 @@ __global__ void __launch_bounds__(kSplitThreads) moe_dense_split(
   const int k0 = (int)((int64_t)p.nk * rank >> log_parts);
   const int k1 = (int)((int64_t)p.nk * (rank + 1) >> log_parts);
   const uint32_t tcols = split_cols(p.nt);
-  // FP32 outputs: accumulators side by side take kDensePart stages in turn, as many
-  // as half of tensor memory holds (two CTAs may share an SM's). 2 x 5816 x 316: error
-  // 1.1e-6 -> 0.5e-6, 3.9 -> 4.0 us.
+  // FP32 outputs: accumulators side by side take kDensePart stages each, at most as many
+  // as half of tensor memory holds (two CTAs may share an SM's); a CTA's part of K is no
+  // longer than that (plan_dense). 2 x 5816 x 316: error 1.1e-6 -> 0.5e-6, 3.9 -> 4.0 us.
   const int accs = p.out_float ? min((k1 - k0 + kDensePart - 1) / kDensePart, split_accs(p.nt)) : 1;
   const int acc_stages = (k1 - k0 + accs - 1) / accs;
   const uint32_t all_cols = tcols << (accs > 4 ? 3 : accs > 2 ? 2 : accs > 1 ? 1 : 0);
