@@ -64,9 +64,11 @@ typedef struct {
  * in FP64. (Without a bias experts compare by their logits.)
  * An expert whose logit is NaN or -inf is switched off: it counts in no sum and
  * is never chosen; one whose bias is NaN or -inf is never chosen. Slots for
- * which no expert is left get the id -1, which moe_group and the decode layer
- * take as an unused slot, and the weight 0. Softmax over infinite logits is
- * shared by those alone; chosen scores that are all 0 give weights of 0.
+ * which no expert is left get the id -1 and the weight 0. moe_group takes -1 as an
+ * unused slot. To the decode layer it is an id outside [0, E) like any other: it
+ * adds nothing and sets MOE_DEVICE_BAD_ID, which then tells of no fault. Softmax
+ * over infinite logits is shared by those alone; chosen scores that are all 0 give
+ * weights of 0.
  *   logits  float or bf16 [T, E]
  *   bias    float [E] or NULL
  *   ids     int32 [T, k];  w float [T, k]

@@ -11,8 +11,8 @@ operators of prompt.py a block with a shared expert over a prompt is
     h = shared_gate_up(n.y)                                # DenseProduct, "silu_mul"
     out = layer.prompt(n.codes, n.scales, ids, w, residual=shared_down(h))
 
-and for a decode batch the same with layer.layer. Like the rest of the package
-these are forward operators: inputs that require grad are taken as they are,
+and for a decode batch the same with layer.layer (which reports slots without an
+expert by MOE_DEVICE_BAD_ID; see route_experts). Like the rest of the package these are forward operators: inputs that require grad are taken as they are,
 and the results carry no graph. Every call forwards device pointers and a
 stream to libmoe_decode.so through the extension module _moe_torch, which
 checks the tensors, allocates the outputs that were not passed in, and takes
@@ -63,7 +63,9 @@ def route_experts(logits, k: int, *, score: str = "softmax", bias=None, groups: 
 
     A logit of NaN or -inf switches its expert off for that token, a bias of
     NaN or -inf for all. Slots that no expert is left for get the id -1 and
-    the weight 0.
+    the weight 0. They add nothing to what MoEDecode makes of them; its prompt
+    takes them as unused, while to layer, gate_up and down they are ids out of
+    range, after which get_error reports MOE_DEVICE_BAD_ID although nothing failed.
     """
     flags = _one_of(score, _SCORES, "score") | _one_of(group_score, _GROUP_SCORES, "group_score")
     if renormalize:
