@@ -146,6 +146,11 @@ moe_status_t moe_dense_destroy(moe_dense_t handle);
  *   out[r] = act(x[r] weight^T + bias) + residual[r]
  * with FP32 accumulation and epilogue, rounded once. M = N, or N / 2 with
  * MOE_ACT_SILU_MUL. The current device has to be the handle's.
+ * The tensor cores cut their sums off at each 16 of K. FP32 outputs add them up
+ * every 512 K (relative 2-norm of the error 0.5e-6 on random values); bf16 outputs
+ * take longer ones, which their rounding hides but for a neighbouring value now and
+ * then. SiLU and the GELUs are off by at most 2^-23 (6 + 5 a) of their value, a the
+ * magnitude of their exponential's argument (values below 2^-126 may be 0).
  *   x         bf16 [R, K], 16-byte aligned
  *   residual  bf16 [R, M] or NULL; may be `out` where that is bf16
  *   out       bf16 [R, M], or float [R, M] with out_float != 0

@@ -179,7 +179,9 @@ size_t split_smem(const DensePlan& p) {
 
 // The cheapest cut by a model of its time, in us. Its constants were fitted to some
 // 500 timings (30 shapes from 1 to 8192 rows, every cut of each, inputs beyond L2);
-// its choices are on average 1.1 % slower than the best of them, 12 % at worst.
+// its choices are on average 1.1 % slower than the best of them, 12 % at worst. All
+// but a few of them had bf16 outputs of 16-byte rows: the model does not know what the
+// element-wise epilogue (p.vec = 0) or that of FP32 outputs takes.
 //   split   a start, then the stages of a CTA at what an SM, shared by the CTAs on
 //           it, or all of L2 delivers, or its ring's latency allows where it turns;
 //           the parts' exchange; clusters that find no room wait for a round more

@@ -249,9 +249,13 @@ __device__ __forceinline__ bool dense_wait(uint64_t* bar, uint32_t parity, const
 //
 // The tensor cores cut a sum off at each step of 16 K instead of rounding it, which
 // adds up along K (relative error of 8191 x 7168 x 256 by its 2-norm: 7.9e-6, of FP32
-// FMAs 0.9e-6). bf16 outputs do not show it. Where the outputs are FP32 (FLOAT), the
-// sums of kDensePart stages in turn are added up in registers: 0.5e-6 with eight
-// stages, 1.0e-6 with 16, in the same time.
+// FMAs 0.9e-6). bf16 outputs take all of a CTA's K in one accumulator all the same, as
+// the library's products do: their error is 1.7e-3 and grows by less than 1e-4 of it, but
+// at K = 7168 a sum lies on the other side of a rounding boundary in one output of 250,
+// with SiLU(gate) * up of 140, which is then the neighbouring bf16 value (the 2-norm
+// of these differences is 2e-4 and 3e-4; FP32 FMAs: 0.6e-4 and 0.8e-4). Where the
+// outputs are FP32 (FLOAT), the sums of kDensePart stages in turn are added up in
+// registers: 0.5e-6 with eight stages, 1.0e-6 with 16, in the same time.
 // ---------------------------------------------------------------------------
 constexpr int kDenseThreads = 384;
 constexpr int kDensePart = 8;                  // stages
