@@ -458,7 +458,8 @@ __device__ __forceinline__ void route_row(const RouteParams& p, const int t, uin
           route_append(list, n, key[r] && ((nears >> gr) & 1u) && route_value(key[r], kMask) >= bound, e);
         }
         __syncwarp();
-        flag = n > 32;
+        // (an infinite bias leaves no bounds: the bound of a group's second infinity is NaN)
+        flag = n > 32 || !(gap < -route_off());
         if (!flag) {
           const double zd = p.sigmoid || !(sums || p.bias) ? 1.0 : route_sum<R>(l, mx);
           const int e = lane < n ? list[lane] : 0;
