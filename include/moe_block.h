@@ -60,8 +60,9 @@ typedef struct {
  *   ids[t]  = the chosen experts, best choice score first
  *   w[t]    = scale * s[ids] (/ sum of s[ids], with MOE_ROUTE_RENORMALIZE)
  * Of equal scores the lower index is the better one. The choice is that of
- * exact arithmetic on the given inputs: scores too close for FP32 are compared
- * in FP64. (Without a bias experts compare by their logits.)
+ * FP64 arithmetic on the given inputs, whatever lies how close: scores too close
+ * for FP32 are compared in FP64. (Without a bias experts compare by their logits,
+ * which is exact; beside a bias a score below 2^-53 of it is none.)
  * An expert whose logit is NaN or -inf is switched off: it counts in no sum and
  * is never chosen; one whose bias is NaN or -inf is never chosen. Slots for
  * which no expert is left get the id -1 and the weight 0. moe_group takes -1 as an

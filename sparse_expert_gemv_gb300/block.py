@@ -57,8 +57,8 @@ def route_experts(logits, k: int, *, score: str = "softmax", bias=None, groups: 
     neighbouring experts, the choice is made within the `top_groups` groups
     (all of them if not given) of the best group scores: their largest
     compared score ("max"), or the sum of their two largest ("top2"). Of equal
-    scores the lower index wins, and close ones are told apart as exact
-    arithmetic would. The weights are the chosen scores, divided by their sum
+    scores the lower index wins, and close ones are told apart as FP64
+    arithmetic does. The weights are the chosen scores, divided by their sum
     (`renormalize`) and times `scale`.
 
     A logit of NaN or -inf switches its expert off for that token, a bias of

@@ -20,7 +20,7 @@ namespace moe {
 // once by a network, and a round of the choice is one warp-wide maximum of the
 // lanes' first keys.
 //
-// The choice has to be that of exact arithmetic. bf16 logits leave 16 bits for
+// The choice has to be that of FP64 arithmetic. bf16 logits leave 16 bits for
 // the place, so without a bias their keys are exact and all different. Other
 // keys lose the low bits and carry the FP32 score's error: where two values that
 // decide something lie closer than that (the next one chosen, the first one
